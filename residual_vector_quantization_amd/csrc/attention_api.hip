@@ -9,6 +9,7 @@
 
 #include "rvq_attention.h"
 #include "attention_internal.h"
+#include "cache_index.h"
 
 namespace {
 
@@ -80,7 +81,8 @@ rvq_status check_cache(const rvq_cache_shape *s)
         s->table_ld < 0 || !known_dtype(s->dtype))
         return RVQ_ERR_INVALID_ARG;
     if ((s->dim != 64 && s->dim != 128) || s->kv_heads > 65535 ||
-        static_cast<int64_t>(s->table_ld) * s->page_size > INT_MAX - 1024)
+        static_cast<int64_t>(s->table_ld) * s->page_size > INT_MAX - 1024 ||
+        static_cast<__int128>(s->n_pages) * s->page_size * s->kv_heads > rvq::kMaxRows)
         return RVQ_ERR_UNSUPPORTED;
     return RVQ_OK;
 }
