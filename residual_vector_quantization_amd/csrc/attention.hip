@@ -1,12 +1,22 @@
-// Windowed attention with sinks, forward pass, and its gradient.
+// Windowed attention with sinks, forward pass.
 //
 //   x_ij = scale q_i . k_j over the keys j that query i sees,
 //   w = softmax(x), out_i = sum_j w_ij v_j, lse_i = log sum_j exp(x_ij)
-//   delta_i = dout_i . out_i,  dw_ij = dout_i . v_j,  dx_ij = w_ij (dw_ij - delta_i)
-//   dq_i = scale sum_j dx_ij k_j,  dk_j = scale sum_i dx_ij q_i,  dv_j = sum_i w_ij dout_i
 //
-// One wavefront a row: a query with its keys one after another (forward, dq)
-// or a key with the queries that see it (dk, dv), lanes over the head dim.
+// Bound by the matrix cores, the LDS reads that feed them and the exponentials,
+// all of about the same weight: 4 dim flops, 1 exponential a pair.
+// A workgroup takes 128 queries of one head and clip, 32 a wavefront, and goes
+// once over the keys they see: the sinks' tiles, then the window's, 64 keys a
+// tile. With transposed products a lane keeps to one query:
+//   S^T [key][query] = K Q^T, 32-wide products; Q stays in registers
+//   O^T [dim][query] += V^T P^T
+// so maxima and sums run inside a lane (and once with the lane 32 further), and
+// the scores that a lane holds are, in order, the P^T operand of the second
+// product: the keys of a V^T operand are numbered as the scores come out.
+// K lies in the LDS as it is, V transposed (done in registers on the way in),
+// both in 16-byte pieces whose place is exchanged within a row so that neither
+// the writes nor the operand reads meet in a bank.
+#include <float.h>
 #include <limits.h>
 #include <stdint.h>
 
@@ -14,190 +24,186 @@
 
 #include "attention_device.h"
 #include "attention_internal.h"
+#include "attention_tiles.h"
 
 namespace rvq {
 namespace {
 
-constexpr int kRowsPerBlock = 4;
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kRows = 32 * kWaves;     // queries a workgroup
+constexpr float kSlack = 8.0f;         // how far (powers of two) a score may exceed the running maximum
 
-template <typename T, int kD>
-__device__ inline void load_row(const Heads &h, int64_t row, int head, int lane, float (&x)[kD / 64])
+// The passes of a workgroup over its keys. Weights of unseen keys are 0, but 0 times a value that is not finite is
+// not 0. So when a result is not finite, a second pass counts, for every result, the keys seen that have such a value
+// there, and a third computes the results with these values taken as 0: results with a count are NaN, the others are
+// what they would be without the values that are not seen.
+enum Pass { kPlain, kMarkers, kFinite };
+
+__device__ inline int below_window(int p, int window)
 {
-    const T *p = static_cast<const T *>(h.data) + row * h.token + head * h.head;
-#pragma unroll
-    for (int i = 0; i < kD / 64; ++i) x[i] = to_float(p[lane + 64 * i]);
+    return static_cast<int>(max(static_cast<int64_t>(p) - window, static_cast<int64_t>(-1)));
 }
 
 template <typename T, int kD>
-__device__ inline void store_row(const Heads &h, int64_t row, int head, int lane, const float (&x)[kD / 64])
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
+void forward_tiles(AttentionArgs a, float factor, int slots)
 {
-    T *p = static_cast<T *>(h.data) + row * h.token + head * h.head;
-#pragma unroll
-    for (int i = 0; i < kD / 64; ++i) p[lane + 64 * i] = static_cast<T>(x[i]);
-}
-
-template <int kN>
-__device__ inline float dot(const float (&x)[kN], const float (&y)[kN])
-{
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kN; ++i) s += x[i] * y[i];
-    return wave_sum(s);
-}
-
-__device__ inline bool find_row(const int32_t *cu, int n_clips, int64_t tokens, int row, int &clip)
-{
-    int first, count;
-    clip = clip_of_row(cu, n_clips, row);
-    clip_range(cu, clip, tokens, first, count);
-    return row >= first && row < first + count;
-}
-
-template <typename T, int kD>
-__global__ __launch_bounds__(64 * kRowsPerBlock)
-void forward_rows(AttentionArgs a)
-{
-    const int lane = threadIdx.x & 63;
-    const int row = blockIdx.x * kRowsPerBlock + (threadIdx.x >> 6), head = blockIdx.y;
-    if (row >= a.q_tokens) return;
-    int clip, q0, nq, k0, nk;
-    if (!find_row(a.cu_q, a.n_clips, a.q_tokens, row, clip)) return;
+    typedef Tiles<T, kD, kThreads> Tile;
+    __shared__ __attribute__((aligned(16))) char s_mem[2 * Tile::kBytes * 2];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int c = lane & 31, half = lane >> 5;
+    // heads change fastest: with 8 of them or more, one chiplet sees the same heads' keys again and again; the
+    // last queries of a clip, which see most, start first
+    const int slot = slots - 1 - static_cast<int>(blockIdx.x / a.q_heads), head = blockIdx.x % a.q_heads;
+    const int kv = head / (a.q_heads / a.kv_heads);
+    const int clip = clip_of_slot(a.cu_q, a.n_clips, slot, kRows);
+    int q0, nq, k0, nk;
     clip_range(a.cu_q, clip, a.q_tokens, q0, nq);
     clip_range(a.cu_k, clip, a.k_tokens, k0, nk);
-    const int kv = head / (a.q_heads / a.kv_heads);
-    const int p = row - q0 + nk - nq;
-    const int64_t first = static_cast<int64_t>(p) - a.window + 1;
-    float q[kD / 64], k[kD / 64], v[kD / 64], o[kD / 64] = {};
-    load_row<T, kD>(a.q, row, head, lane, q);
+    const int i0 = (slot - (a.cu_q[clip] / kRows + clip)) * kRows;
+    if (i0 < 0 || i0 >= nq) return;
+
+    const int back = nk - nq;                               // position of query 0
+    const int row = i0 + 32 * wave + c;                     // this lane's query
+    const bool real = row < nq;
+    const int p = row + back;
+    const KeyRange range = keys_seen(i0 + back, min(i0 + kRows, nq) - 1 + back, a.window, a.sinks);
+    // this wavefront's first and last position
+    const int w_first = i0 + 32 * wave + back, w_last = min(i0 + 32 * wave + 31, nq - 1) + back;
+    // positions above these are in the window of this query, of the wavefront's first and of its last
+    const int p_low = below_window(p, a.window), w_low = below_window(w_first, a.window);
+    const int w_high = below_window(w_last, a.window);
+
+    vec8<T> q[kD / 16];
+    {
+        const T *at = static_cast<const T *>(a.q.data) + static_cast<int64_t>(q0 + min(row, nq - 1)) * a.q.token + head * a.q.head;
+#pragma unroll
+        for (int t = 0; t < kD / 16; ++t) q[t] = load8(at + 16 * t + 8 * half);
+    }
+    const T *keys = static_cast<const T *>(a.k.data) + static_cast<int64_t>(k0) * a.k.token + kv * a.k.head;
+    const T *values = static_cast<const T *>(a.v.data) + static_cast<int64_t>(k0) * a.v.token + kv * a.v.head;
+
+    f32x16 o[kD / 32];
+    uint32_t marked[kD / 64] = {};
     float m = -INFINITY, l = 0.0f;
-    for (int j = 0; j <= p; ++j) {
-        if (j < first && j >= a.sinks) {
-            j = static_cast<int>(first) - 1;
-            continue;
+    for (int pass = kPlain; pass <= kFinite; ++pass) {
+#pragma unroll
+        for (int n = 0; n < kD / 32; ++n) o[n] = f32x16{};
+        m = -INFINITY;
+        l = 0.0f;
+        typename Tile::Piece pk;
+        typename Tile::Group pv;
+        if (range.tiles > 0) {
+            Tile::fetch_rows(pk, keys, a.k.token, range.start(0), nk);
+            Tile::fetch_groups(pv, values, a.v.token, range.start(0), nk);
         }
-        load_row<T, kD>(a.k, k0 + j, kv, lane, k);
-        load_row<T, kD>(a.v, k0 + j, kv, lane, v);
-        const float x = dot(q, k) * a.scale;
-        const float top = fmaxf(m, x);
-        const float safe = top == -INFINITY ? 0.0f : top;
-        const float keep = exp2f((m - safe) * kLog2e), w = exp2f((x - safe) * kLog2e);
-        l = l * keep + w;
-#pragma unroll
-        for (int i = 0; i < kD / 64; ++i) o[i] = o[i] * keep + w * v[i];
-        m = top;
-    }
-#pragma unroll
-    for (int i = 0; i < kD / 64; ++i) o[i] = l == 0.0f ? 0.0f : o[i] / l;
-    store_row<T, kD>(a.out, row, head, lane, o);
-    if (a.lse && lane == 0) a.lse[static_cast<int64_t>(head) * a.q_tokens + row] = l == 0.0f ? -INFINITY : m + logf(l);
-}
-
-// delta[head, row] = dout . out
-template <typename T, int kD>
-__global__ __launch_bounds__(64 * kRowsPerBlock)
-void delta_rows(AttentionArgs a)
-{
-    const int lane = threadIdx.x & 63;
-    const int row = blockIdx.x * kRowsPerBlock + (threadIdx.x >> 6), head = blockIdx.y;
-    int clip;
-    if (row >= a.q_tokens || !find_row(a.cu_q, a.n_clips, a.q_tokens, row, clip)) return;
-    float g[kD / 64], o[kD / 64];
-    load_row<T, kD>(a.dout, row, head, lane, g);
-    load_row<T, kD>(a.out, row, head, lane, o);
-    const float s = dot(g, o);
-    if (lane == 0) static_cast<float *>(a.workspace)[static_cast<int64_t>(head) * a.q_tokens + row] = s;
-}
-
-template <typename T, int kD>
-__global__ __launch_bounds__(64 * kRowsPerBlock)
-void dq_rows(AttentionArgs a)
-{
-    const int lane = threadIdx.x & 63;
-    const int row = blockIdx.x * kRowsPerBlock + (threadIdx.x >> 6), head = blockIdx.y;
-    if (row >= a.q_tokens) return;
-    int clip, q0, nq, k0, nk;
-    if (!find_row(a.cu_q, a.n_clips, a.q_tokens, row, clip)) return;
-    clip_range(a.cu_q, clip, a.q_tokens, q0, nq);
-    clip_range(a.cu_k, clip, a.k_tokens, k0, nk);
-    const int kv = head / (a.q_heads / a.kv_heads);
-    const int p = row - q0 + nk - nq;
-    const int64_t first = static_cast<int64_t>(p) - a.window + 1;
-    const int64_t at = static_cast<int64_t>(head) * a.q_tokens + row;
-    const float lse = a.lse[at], delta = static_cast<const float *>(a.workspace)[at];
-    float q[kD / 64], k[kD / 64], v[kD / 64], g[kD / 64], dq[kD / 64] = {};
-    load_row<T, kD>(a.q, row, head, lane, q);
-    load_row<T, kD>(a.dout, row, head, lane, g);
-    if (lse != -INFINITY) {
-        for (int j = 0; j <= p; ++j) {
-            if (j < first && j >= a.sinks) {
-                j = static_cast<int>(first) - 1;
-                continue;
+        for (int t = 0; t < range.tiles; ++t) {
+            char *s_k = s_mem + (t & 1) * 2 * Tile::kBytes, *s_v = s_k + Tile::kBytes;
+            if (pass != kPlain) Tile::only_finite(pv, pass == kMarkers);
+            Tile::store_rows(s_k, pk);
+            Tile::store_transposed(s_v, pv);
+            __syncthreads();
+            const int j0 = range.start(t);
+            if (t + 1 < range.tiles) {
+                Tile::fetch_rows(pk, keys, a.k.token, range.start(t + 1), nk);
+                Tile::fetch_groups(pv, values, a.v.token, range.start(t + 1), nk);
             }
-            load_row<T, kD>(a.k, k0 + j, kv, lane, k);
-            load_row<T, kD>(a.v, k0 + j, kv, lane, v);
-            const float w = exp2f((dot(q, k) * a.scale - lse) * kLog2e);
-            const float dx = w * (dot(g, v) - delta) * a.scale;
+            // nothing of this tile is seen by this wavefront
+            if (j0 > w_last || (j0 + 63 <= w_low && j0 >= a.sinks)) continue;
+            f32x16 x[2] = {};
 #pragma unroll
-            for (int i = 0; i < kD / 64; ++i) dq[i] += dx * k[i];
-        }
-    }
-    store_row<T, kD>(a.dq, row, head, lane, dq);
-}
-
-template <typename T, int kD>
-__global__ __launch_bounds__(64 * kRowsPerBlock)
-void dkv_rows(AttentionArgs a)
-{
-    const int lane = threadIdx.x & 63;
-    const int row = blockIdx.x * kRowsPerBlock + (threadIdx.x >> 6), kv = blockIdx.y;
-    if (row >= a.k_tokens) return;
-    int clip, q0, nq, k0, nk;
-    if (!find_row(a.cu_k, a.n_clips, a.k_tokens, row, clip)) return;
-    clip_range(a.cu_q, clip, a.q_tokens, q0, nq);
-    clip_range(a.cu_k, clip, a.k_tokens, k0, nk);
-    const int j = row - k0, group = a.q_heads / a.kv_heads;
-    const int64_t last = j < a.sinks ? nk : static_cast<int64_t>(j) + a.window;   // positions below it see j
-    float q[kD / 64], k[kD / 64], v[kD / 64], g[kD / 64], dk[kD / 64] = {}, dv[kD / 64] = {};
-    load_row<T, kD>(a.k, row, kv, lane, k);
-    load_row<T, kD>(a.v, row, kv, lane, v);
-    for (int h = kv * group; h < (kv + 1) * group; ++h) {
-        for (int64_t p = max(j, nk - nq); p < min(static_cast<int64_t>(nk), last); ++p) {
-            const int64_t qr = q0 + p - (nk - nq), at = h * a.q_tokens + qr;
-            const float lse = a.lse[at], delta = static_cast<const float *>(a.workspace)[at];
-            if (lse == -INFINITY) continue;
-            load_row<T, kD>(a.q, qr, h, lane, q);
-            load_row<T, kD>(a.dout, qr, h, lane, g);
-            const float w = exp2f((dot(q, k) * a.scale - lse) * kLog2e);
-            const float dx = w * (dot(g, v) - delta) * a.scale;
+            for (int n = 0; n < kD / 16; ++n)
 #pragma unroll
-            for (int i = 0; i < kD / 64; ++i) {
-                dk[i] += dx * q[i];
-                dv[i] += w * g[i];
+                for (int b = 0; b < 2; ++b) x[b] = mma32(Tile::row_operand(s_k, 32 * b + c, 2 * n + half), q[n], x[b]);
+            const bool all = j0 + 63 <= w_first && (j0 > w_high || j0 + 63 < a.sinks);
+            float top = -INFINITY;
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    if (!all) {
+                        const int j = j0 + 32 * b + 8 * (r >> 2) + 4 * half + (r & 3);
+                        const bool sees = j <= p && (j > p_low || j < a.sinks);
+                        x[b][r] = sees ? x[b][r] : -INFINITY;
+                    }
+                    top = fmaxf(top, x[b][r]);
+                }
+            top *= factor;
+            if (__any(top > m + kSlack)) {
+                top = fmaxf(top, __shfl_xor(top, 32));
+                if (top > m + kSlack) {
+                    const float keep = fast_exp2(m - top);
+                    m = top;
+                    l *= keep;
+                    if (pass != kMarkers) {
+#pragma unroll
+                        for (int n = 0; n < kD / 32; ++n) o[n] *= keep;
+                    }
+                }
             }
+            const float safe = m == -INFINITY ? 0.0f : m;
+            vec8<T> w[4];
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    float e = fast_exp2(__builtin_fmaf(x[b][r], factor, -safe));
+                    l += e;
+                    if (pass == kMarkers) e = x[b][r] == -INFINITY ? 0.0f : 1.0f;
+                    w[2 * b + (r >> 3)][r & 7] = static_cast<T>(e);
+                }
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int n = 0; n < kD / 32; ++n) o[n] = mma32(Tile::transposed_operand(s_v, 32 * n + c, s, half), w[s], o[n]);
+        }
+        __syncthreads();     // the tiles are no longer read
+        if (pass == kPlain) {
+            bool odd = false;
+#pragma unroll
+            for (int n = 0; n < kD / 32; ++n)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) odd = odd || !(fabsf(o[n][r]) <= FLT_MAX);
+            if (!__syncthreads_or(odd)) break;
+        } else if (pass == kMarkers) {
+#pragma unroll
+            for (int n = 0; n < kD / 32; ++n)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) marked[n >> 1] |= static_cast<uint32_t>(o[n][r] > 0.0f) << (16 * (n & 1) + r);
+        } else {
+#pragma unroll
+            for (int n = 0; n < kD / 32; ++n)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (marked[n >> 1] >> (16 * (n & 1) + r) & 1) o[n][r] = __builtin_nanf("");
         }
     }
-    store_row<T, kD>(a.dk, row, kv, lane, dk);
-    store_row<T, kD>(a.dv, row, kv, lane, dv);
+    if (!real) return;
+    l += __shfl_xor(l, 32);
+    const float inverse = l == 0.0f ? 0.0f : 1.0f / l;
+    T *out = static_cast<T *>(a.out.data) + static_cast<int64_t>(q0 + row) * a.out.token + head * a.out.head;
+#pragma unroll
+    for (int n = 0; n < kD / 32; ++n)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            T y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = static_cast<T>(o[n][4 * r + i] * inverse);
+            store4(out + 32 * n + 8 * r + 4 * half, y);
+        }
+    if (a.lse && half == 0)
+        a.lse[static_cast<int64_t>(head) * a.q_tokens + q0 + row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
-
-unsigned blocks(int64_t rows) { return static_cast<unsigned>((rows + kRowsPerBlock - 1) / kRowsPerBlock); }
 
 template <typename T, int kD>
 hipError_t forward(const AttentionArgs &a, hipStream_t stream)
 {
-    forward_rows<T, kD><<<dim3(blocks(a.q_tokens), a.q_heads), 64 * kRowsPerBlock, 0, stream>>>(a);
-    return hipGetLastError();
-}
-
-template <typename T, int kD>
-hipError_t backward(const AttentionArgs &a, hipStream_t stream)
-{
-    if (a.q_tokens > 0) {
-        delta_rows<T, kD><<<dim3(blocks(a.q_tokens), a.q_heads), 64 * kRowsPerBlock, 0, stream>>>(a);
-        dq_rows<T, kD><<<dim3(blocks(a.q_tokens), a.q_heads), 64 * kRowsPerBlock, 0, stream>>>(a);
-    }
-    if (a.k_tokens > 0)
-        dkv_rows<T, kD><<<dim3(blocks(a.k_tokens), a.kv_heads), 64 * kRowsPerBlock, 0, stream>>>(a);
+    const int64_t slots = a.q_tokens / kRows + a.n_clips + 1;
+    if (slots * a.q_heads > INT_MAX) return hipErrorInvalidConfiguration;
+    // scale 0 (equal weights) becomes the smallest factor: 0 times the -inf of an unseen key does not arise
+    const float factor = fmaxf(a.scale * kLog2e, FLT_MIN);
+    forward_tiles<T, kD><<<static_cast<unsigned>(slots * a.q_heads), kThreads, 0, stream>>>(a, factor, static_cast<int>(slots));
     return hipGetLastError();
 }
 
@@ -208,19 +214,6 @@ hipError_t launch_window_attention(const AttentionArgs &a, hipStream_t stream)
     if (a.dtype == RVQ_F32) return a.dim == 64 ? forward<float, 64>(a, stream) : forward<float, 128>(a, stream);
     if (a.dtype == RVQ_F16) return a.dim == 64 ? forward<f16_t, 64>(a, stream) : forward<f16_t, 128>(a, stream);
     return a.dim == 64 ? forward<bf16_t, 64>(a, stream) : forward<bf16_t, 128>(a, stream);
-}
-
-int64_t window_attention_backward_bytes(int64_t q_tokens, int64_t k_tokens, int n_clips, int q_heads, int kv_heads,
-                                        int dim, int sinks)
-{
-    return q_tokens * q_heads * 4;
-}
-
-hipError_t launch_window_attention_backward(const AttentionArgs &a, hipStream_t stream)
-{
-    if (a.dtype == RVQ_F32) return a.dim == 64 ? backward<float, 64>(a, stream) : backward<float, 128>(a, stream);
-    if (a.dtype == RVQ_F16) return a.dim == 64 ? backward<f16_t, 64>(a, stream) : backward<f16_t, 128>(a, stream);
-    return a.dim == 64 ? backward<bf16_t, 64>(a, stream) : backward<bf16_t, 128>(a, stream);
 }
 
 }  // namespace rvq

@@ -28,6 +28,7 @@
 
 #include "attention_device.h"
 #include "attention_internal.h"
+#include "attention_tiles.h"
 #include "cache_index.h"
 
 namespace rvq {
@@ -51,19 +52,6 @@ struct Params {
 struct Partials {
     float *stats, *out;
 };
-
-template <typename T>
-__device__ inline vec8<T> load8(const T *p);
-template <>
-__device__ inline f32x8 load8<float>(const float *p)
-{
-    const f32x4 a = *reinterpret_cast<const f32x4 *>(p), b = *reinterpret_cast<const f32x4 *>(p + 4);
-    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-template <>
-__device__ inline f16x8 load8<f16_t>(const f16_t *p) { return *reinterpret_cast<const f16x8 *>(p); }
-template <>
-__device__ inline bf16x8 load8<bf16_t>(const bf16_t *p) { return *reinterpret_cast<const bf16x8 *>(p); }
 
 // kN values of 8 frames, as the kN operands of 8 frames at one dim.
 template <typename T, int kN>
@@ -131,7 +119,7 @@ void newest_frame(Params p, Partials part)
     {
         const T *at = static_cast<const T *>(a.q.data) + clip * a.q.token + (head0 + min(c, heads - 1)) * a.q.head;
 #pragma unroll
-        for (int t = 0; t < kSteps; ++t) q[t] = load8<T>(at + 32 * t + 8 * g);
+        for (int t = 0; t < kSteps; ++t) q[t] = load8(at + 32 * t + 8 * g);
     }
     f32x4 o[kN] = {};
     float m = -INFINITY, l = 0.0f;
@@ -160,7 +148,7 @@ void newest_frame(Params p, Partials part)
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int t = 0; t < kSteps; ++t) k[b][t] = load8<T>(keys + static_cast<uint64_t>(kr[b]) * kD + 32 * t + 8 * g);
+                for (int t = 0; t < kSteps; ++t) k[b][t] = load8(keys + static_cast<uint64_t>(kr[b]) * kD + 32 * t + 8 * g);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v.load(i, values + static_cast<uint64_t>(__shfl(mine, 8 * g + i)) * kD + kN * c);
         } else {
@@ -170,7 +158,7 @@ void newest_frame(Params p, Partials part)
 #pragma unroll
                 for (int t = 0; t < kSteps; ++t) {
                     k[b][t] = vec8<T>{};
-                    if (kr[b] < kPastEnd) k[b][t] = load8<T>(keys + static_cast<uint64_t>(kr[b]) * kD + 32 * t + 8 * g);
+                    if (kr[b] < kPastEnd) k[b][t] = load8(keys + static_cast<uint64_t>(kr[b]) * kD + 32 * t + 8 * g);
                 }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
