@@ -13,9 +13,8 @@
 // so maxima and sums run inside a lane (and once with the lane 32 further), and
 // the scores that a lane holds are, in order, the P^T operand of the second
 // product: the keys of a V^T operand are numbered as the scores come out.
-// K lies in the LDS as it is, V transposed (done in registers on the way in),
-// both in 16-byte pieces whose place is exchanged within a row so that neither
-// the writes nor the operand reads meet in a bank.
+// K and V lie in the LDS row by row, two tiles of each: while one is worked on,
+// the next is on its way from global memory.
 #include <float.h>
 #include <limits.h>
 #include <stdint.h>
@@ -40,17 +39,12 @@ constexpr float kSlack = 8.0f;         // how far (powers of two) a score may ex
 // what they would be without the values that are not seen.
 enum Pass { kPlain, kMarkers, kFinite };
 
-__device__ inline int below_window(int p, int window)
-{
-    return static_cast<int>(max(static_cast<int64_t>(p) - window, static_cast<int64_t>(-1)));
-}
-
 template <typename T, int kD>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
 void forward_tiles(AttentionArgs a, float factor, int slots)
 {
-    typedef Tiles<T, kD, kThreads> Tile;
-    __shared__ __attribute__((aligned(16))) char s_mem[2 * Tile::kBytes * 2];
+    typedef Tile<T, kD, kWaves> Rows;
+    __shared__ __attribute__((aligned(16))) char s_mem[4 * Rows::kBytes];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = lane & 31, half = lane >> 5;
     // heads change fastest: with 8 of them or more, one chiplet sees the same heads' keys again and again; the
@@ -92,71 +86,68 @@ void forward_tiles(AttentionArgs a, float factor, int slots)
         for (int n = 0; n < kD / 32; ++n) o[n] = f32x16{};
         m = -INFINITY;
         l = 0.0f;
-        typename Tile::Piece pk;
-        typename Tile::Group pv;
         if (range.tiles > 0) {
-            Tile::fetch_rows(pk, keys, a.k.token, range.start(0), nk);
-            Tile::fetch_groups(pv, values, a.v.token, range.start(0), nk);
+            Rows::load(s_mem, keys, a.k.token, range.start(0), nk);
+            Rows::load(s_mem + Rows::kBytes, values, a.v.token, range.start(0), nk);
         }
         for (int t = 0; t < range.tiles; ++t) {
-            char *s_k = s_mem + (t & 1) * 2 * Tile::kBytes, *s_v = s_k + Tile::kBytes;
-            if (pass != kPlain) Tile::only_finite(pv, pass == kMarkers);
-            Tile::store_rows(s_k, pk);
-            Tile::store_transposed(s_v, pv);
-            __syncthreads();
-            const int j0 = range.start(t);
+            char *s_k = s_mem + (t & 1) * 2 * Rows::kBytes, *s_v = s_k + Rows::kBytes;
+            wait_copies();
+            __syncthreads();     // tile t is there, tile t - 1 is no longer read
             if (t + 1 < range.tiles) {
-                Tile::fetch_rows(pk, keys, a.k.token, range.start(t + 1), nk);
-                Tile::fetch_groups(pv, values, a.v.token, range.start(t + 1), nk);
+                char *s_next = s_mem + ((t + 1) & 1) * 2 * Rows::kBytes;
+                Rows::load(s_next, keys, a.k.token, range.start(t + 1), nk);
+                Rows::load(s_next + Rows::kBytes, values, a.v.token, range.start(t + 1), nk);
             }
-            // nothing of this tile is seen by this wavefront
-            if (j0 > w_last || (j0 + 63 <= w_low && j0 >= a.sinks)) continue;
-            f32x16 x[2] = {};
+            if (pass != kPlain) {
+                Rows::only_finite(s_v, pass == kMarkers);
+                __syncthreads();
+            }
 #pragma unroll
-            for (int n = 0; n < kD / 16; ++n)
+            for (int b = 0; b < 2; ++b) {
+                const int j0 = range.start(t) + 32 * b;
+                // nothing of these keys is seen by this wavefront
+                if (j0 > w_last || (j0 + 31 <= w_low && j0 >= a.sinks)) continue;
+                f32x16 x = {};
 #pragma unroll
-                for (int b = 0; b < 2; ++b) x[b] = mma32(Tile::row_operand(s_k, 32 * b + c, 2 * n + half), q[n], x[b]);
-            const bool all = j0 + 63 <= w_first && (j0 > w_high || j0 + 63 < a.sinks);
-            float top = -INFINITY;
+                for (int n = 0; n < kD / 16; ++n) x = mma32(Rows::along(s_k, 32 * b + c, 2 * n + half), q[n], x);
+                if (!(j0 + 31 <= w_first && (j0 > w_high || j0 + 31 < a.sinks))) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    if (!all) {
-                        const int j = j0 + 32 * b + 8 * (r >> 2) + 4 * half + (r & 3);
-                        const bool sees = j <= p && (j > p_low || j < a.sinks);
-                        x[b][r] = sees ? x[b][r] : -INFINITY;
-                    }
-                    top = fmaxf(top, x[b][r]);
-                }
-            top *= factor;
-            if (__any(top > m + kSlack)) {
-                top = fmaxf(top, __shfl_xor(top, 32));
-                if (top > m + kSlack) {
-                    const float keep = fast_exp2(m - top);
-                    m = top;
-                    l *= keep;
-                    if (pass != kMarkers) {
-#pragma unroll
-                        for (int n = 0; n < kD / 32; ++n) o[n] *= keep;
+                    for (int r = 0; r < 16; ++r) {
+                        const int j = j0 + 8 * (r >> 2) + 4 * half + (r & 3);
+                        x[r] = j <= p && (j > p_low || j < a.sinks) ? x[r] : -INFINITY;
                     }
                 }
-            }
-            const float safe = m == -INFINITY ? 0.0f : m;
-            vec8<T> w[4];
+                float top = x[0];
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+                for (int r = 1; r < 16; ++r) top = fmaxf(top, x[r]);
+                top *= factor;
+                if (__any(top > m + kSlack)) {
+                    top = fmaxf(top, __shfl_xor(top, 32));
+                    if (top > m + kSlack) {
+                        const float keep = fast_exp2(m - top);
+                        m = top;
+                        l *= keep;
+                        if (pass != kMarkers) {
+#pragma unroll
+                            for (int n = 0; n < kD / 32; ++n) o[n] *= keep;
+                        }
+                    }
+                }
+                const float safe = m == -INFINITY ? 0.0f : m;
+                vec8<T> w[2];
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    float e = fast_exp2(__builtin_fmaf(x[b][r], factor, -safe));
+                    float e = fast_exp2(__builtin_fmaf(x[r], factor, -safe));
                     l += e;
-                    if (pass == kMarkers) e = x[b][r] == -INFINITY ? 0.0f : 1.0f;
-                    w[2 * b + (r >> 3)][r & 7] = static_cast<T>(e);
+                    if (pass == kMarkers) e = x[r] == -INFINITY ? 0.0f : 1.0f;
+                    w[r >> 3][r & 7] = static_cast<T>(e);
                 }
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
+                for (int s = 0; s < 2; ++s)
 #pragma unroll
-                for (int n = 0; n < kD / 32; ++n) o[n] = mma32(Tile::transposed_operand(s_v, 32 * n + c, s, half), w[s], o[n]);
+                    for (int n = 0; n < kD / 32; ++n) o[n] = mma32(Rows::across(s_v, n, 2 * b + s), w[s], o[n]);
+            }
         }
         __syncthreads();     // the tiles are no longer read
         if (pass == kPlain) {

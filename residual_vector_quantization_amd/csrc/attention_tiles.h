@@ -1,6 +1,11 @@
-// Tiles of 64 rows of head values on their way from global memory through
-// registers into the LDS, as they are or transposed, and the matrix operands
-// read back from there.
+// Tiles of head rows in the LDS, and the matrix operands read from them along
+// the rows or across them.
+//
+// A tile lies row after row, 16 bytes a piece; the pieces of a row are
+// exchanged (place) so that reads along the rows (16 neighbouring rows, the
+// same piece) and across them (4 neighbouring rows, 64 bytes each) spread over
+// all banks. Rows come straight from global memory into the LDS, each lane
+// picking the piece that belongs to its place.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -21,13 +26,29 @@ __device__ inline f16x8 load8(const f16_t *p) { return *reinterpret_cast<const f
 __device__ inline bf16x8 load8(const bf16_t *p) { return *reinterpret_cast<const bf16x8 *>(p); }
 
 // Four neighbouring values in one store.
-__device__ inline void store4(float *p, const float (&x)[4]) { *reinterpret_cast<f32x4 *>(p) = f32x4{x[0], x[1], x[2], x[3]}; }
 template <typename T>
 __device__ inline void store4(T *p, const T (&x)[4])
 {
     typedef T four __attribute__((ext_vector_type(4)));
     *reinterpret_cast<four *>(p) = four{x[0], x[1], x[2], x[3]};
 }
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+// One wavefront-wide copy from global memory into the LDS: lane i's 16 (4) bytes at src go to dst + 16 i (4 i), dst
+// the same for all lanes. Issued as inline assembly so that the compiler does not order every LDS read behind it;
+// the caller waits with wait_copies and a barrier.
+__device__ inline void copy16(const void *src, void *dst)
+{
+    const unsigned m0 = static_cast<unsigned>(reinterpret_cast<size_t>((lds_void *)dst));
+    asm volatile("global_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(m0) : "memory");
+}
+__device__ inline void copy4(const void *src, void *dst)
+{
+    const unsigned m0 = static_cast<unsigned>(reinterpret_cast<size_t>((lds_void *)dst));
+    asm volatile("global_load_lds_dword %0, off" ::"v"(src), "{m0}"(m0) : "memory");
+}
+__device__ inline void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // The 64-key tiles that the queries at positions p_first .. p_last see some of: the sinks', then the window's.
 struct KeyRange {
@@ -49,126 +70,93 @@ __device__ inline KeyRange keys_seen(int p_first, int p_last, int window, int si
     return r;
 }
 
-template <typename T, int kD, int kThreads>
-struct Tiles {
-    static constexpr int kBytes = kTileRows * kD * static_cast<int>(sizeof(T));
+// The position below which a query at p sees only sinks, less 1 (-1 at least).
+__device__ inline int below_window(int p, int window)
+{
+    return static_cast<int>(max(static_cast<int64_t>(p) - window, static_cast<int64_t>(-1)));
+}
+
+template <typename T, int kD, int kWaves>
+struct Tile {
+    static constexpr int kRowBytes = kD * static_cast<int>(sizeof(T));
+    static constexpr int kBytes = kTileRows * kRowBytes;
     static constexpr int kPiece = 16 / static_cast<int>(sizeof(T));   // values in 16 bytes
-    static constexpr int kRowPieces = kD / kPiece;
-    static constexpr int kCount = kTileRows * kRowPieces / kThreads;  // 16-byte pieces a thread
-    // transposed tiles come in as units of 4 rows and kWide columns, so that every thread has one or more
-    static constexpr int kWide = sizeof(T) == 2 && kD == 128 ? 8 : 4;
-    static constexpr int kUnitCols = kD / kWide;
-    static constexpr int kUnits = kTileRows / 4 * kUnitCols / kThreads;
-    static_assert(kCount >= 1 && kUnits >= 1, "tile smaller than the workgroup");
+    static constexpr int kRowPieces = kRowBytes / 16;
+    static constexpr int kCopies = kTileRows * kRowPieces / (64 * kWaves);
+    static_assert(kCopies >= 1, "tile smaller than the workgroup");
 
-    struct Piece { u32x4 x[kCount]; };
-    typedef T Part __attribute__((ext_vector_type(kWide)));
-    struct Group { Part x[kUnits][4]; };
-
-    // Exchange of the 16-byte pieces of a row: 16 neighbouring rows (of 8 pieces: pairs of rows) put the same piece
-    // in different banks.
-    __device__ static int row_place(int row, int piece)
+    __device__ static int place(int row, int piece)
     {
-        return piece ^ (kRowPieces >= 16 ? row & 15 : (row >> 1) & 7);
-    }
-    // The same for a transposed row (64 values of one dim: 8 or 16 pieces), where the writes of one instruction are
-    // kWide dims apart.
-    __device__ static int dim_place(int dim, int piece)
-    {
-        return piece ^ (sizeof(T) == 2 ? ((dim >> 1) ^ (dim >> 3)) & 7 : (dim ^ (dim >> 3)) & 15);
+        return piece ^ (kRowPieces >= 16 ? (row & 3) << 2 | ((row >> 2) & 3) : ((row >> 1) & 1) << 2 | ((row >> 2) & 3));
     }
 
-    // Rows first .. first + 63 of `rows`, zeros from row `end` on.
-    __device__ static void fetch_rows(Piece &p, const T *rows, int64_t stride, int first, int end)
+    // Rows first .. first + 63 of `rows` into the tile, the last one (end - 1) again for rows past the end.
+    __device__ static void load(char *s, const T *rows, int64_t stride, int first, int end)
     {
+        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
-        for (int n = 0; n < kCount; ++n) {
-            const int at = n * kThreads + threadIdx.x, row = first + at / kRowPieces, col = at % kRowPieces;
-            p.x[n] = u32x4{0, 0, 0, 0};
-            if (row < end) p.x[n] = *reinterpret_cast<const u32x4 *>(rows + row * stride + col * kPiece);
+        for (int n = 0; n < kCopies; ++n) {
+            const int at = (n * kWaves + wave) * 64 + lane, row = at / kRowPieces;
+            const int piece = place(row, at % kRowPieces);
+            copy16(rows + min(first + row, end - 1) * stride + piece * kPiece, s + (n * kWaves + wave) * 1024);
         }
     }
-    __device__ static void store_rows(char *s, const Piece &p)
+
+    // Operand along the rows: values 8 k8 .. 8 k8 + 7 of a row.
+    __device__ static vec8<T> along(const char *s, int row, int k8)
     {
-#pragma unroll
-        for (int n = 0; n < kCount; ++n) {
-            const int at = n * kThreads + threadIdx.x, row = at / kRowPieces, col = at % kRowPieces;
-            *reinterpret_cast<u32x4 *>(s + (row * kRowPieces + row_place(row, col)) * 16) = p.x[n];
-        }
-    }
-    // 8 values of row `row` from 8 * k8 on.
-    __device__ static vec8<T> row_operand(const char *s, int row, int k8)
-    {
+        const char *r = s + row * kRowBytes;
         if constexpr (sizeof(T) == 2) {
-            return *reinterpret_cast<const vec8<T> *>(s + (row * kRowPieces + row_place(row, k8)) * 16);
+            return *reinterpret_cast<const vec8<T> *>(r + place(row, k8) * 16);
         } else {
-            const f32x4 a = *reinterpret_cast<const f32x4 *>(s + (row * kRowPieces + row_place(row, 2 * k8)) * 16);
-            const f32x4 b = *reinterpret_cast<const f32x4 *>(s + (row * kRowPieces + row_place(row, 2 * k8 + 1)) * 16);
+            const f32x4 a = *reinterpret_cast<const f32x4 *>(r + place(row, 2 * k8) * 16);
+            const f32x4 b = *reinterpret_cast<const f32x4 *>(r + place(row, 2 * k8 + 1) * 16);
             return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
         }
     }
 
-    __device__ static void fetch_groups(Group &g, const T *rows, int64_t stride, int first, int end)
+    // Operand across the rows: lane l gets dim 32 n + l % 32 of rows 16 step + 4 half .. + 3 and 16 step + 8 + 4 half
+    // .. + 3 (half = l / 32), the order in which a 32-wide product leaves its results. 16-bit values are transposed by
+    // the LDS read: of each 16 lanes, lanes 4 r .. 4 r + 3 point at 16 neighbouring values of row r, and lane i gets
+    // the four rows' value i.
+    __device__ static vec8<T> across(const char *s, int n, int step)
     {
-#pragma unroll
-        for (int n = 0; n < kUnits; ++n) {
-            const int at = n * kThreads + threadIdx.x, four = at / kUnitCols, col = at % kUnitCols;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = first + 4 * four + i;
-                g.x[n][i] = Part{};
-                if (row < end) g.x[n][i] = *reinterpret_cast<const Part *>(rows + row * stride + col * kWide);
-            }
-        }
-    }
-    // Row d of the transposed tile holds the 64 rows' values at dim d. 16-bit: 16-byte piece 2 s + half holds rows
-    // 16 s + 4 half .. + 3 and 16 s + 8 + 4 half .. + 3, the order in which a 32-wide product leaves its results.
-    __device__ static void store_transposed(char *s, const Group &g)
-    {
-        typedef T Four __attribute__((ext_vector_type(4)));
-#pragma unroll
-        for (int n = 0; n < kUnits; ++n) {
-            const int at = n * kThreads + threadIdx.x, four = at / kUnitCols, col = at % kUnitCols;
-#pragma unroll
-            for (int j = 0; j < kWide; ++j) {
-                const int dim = col * kWide + j;
-                const Four y = {g.x[n][0][j], g.x[n][1][j], g.x[n][2][j], g.x[n][3][j]};
-                char *row = s + dim * kTileRows * static_cast<int>(sizeof(T));
-                if constexpr (sizeof(T) == 2) {
-                    const int piece = 2 * (four >> 2) + (four & 1), part = (four >> 1) & 1;
-                    *reinterpret_cast<Four *>(row + dim_place(dim, piece) * 16 + part * 8) = y;
-                } else {
-                    *reinterpret_cast<Four *>(row + dim_place(dim, four) * 16) = y;
-                }
-            }
-        }
-    }
-    // Rows 16 s + 4 half .. + 3 and 16 s + 8 + 4 half .. + 3 at dim `dim`.
-    __device__ static vec8<T> transposed_operand(const char *s, int dim, int step, int half)
-    {
-        const char *row = s + dim * kTileRows * static_cast<int>(sizeof(T));
+        const int lane = threadIdx.x & 63, half = lane >> 5;
         if constexpr (sizeof(T) == 2) {
-            return *reinterpret_cast<const vec8<T> *>(row + dim_place(dim, 2 * step + half) * 16);
+            typedef short s16x4 __attribute__((ext_vector_type(4)));
+            typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+            union { s16x4 part[2]; vec8<T> whole; } u;
+            const int i = lane & 15, group = (lane >> 4) & 1;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int row = 16 * step + 8 * b + 4 * half + (i >> 2);
+                const int piece = 4 * n + 2 * group + ((i >> 1) & 1);
+                const char *at = s + row * kRowBytes + place(row, piece) * 16 + (i & 1) * 8;
+                u.part[b] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at);
+            }
+            return u.whole;
         } else {
-            const f32x4 a = *reinterpret_cast<const f32x4 *>(row + dim_place(dim, 4 * step + half) * 16);
-            const f32x4 b = *reinterpret_cast<const f32x4 *>(row + dim_place(dim, 4 * step + 2 + half) * 16);
-            return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+            vec8<T> x;
+            const int dim = 32 * n + (lane & 31);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int row = 16 * step + 8 * (e >> 2) + 4 * half + (e & 3);
+                x[e] = *reinterpret_cast<const float *>(s + row * kRowBytes + place(row, dim >> 2) * 16 + (dim & 3) * 4);
+            }
+            return x;
         }
     }
 
-    // Values that are not finite become 0; or, as markers, they become 1 and all others 0.
-    __device__ static void only_finite(Group &g, bool markers)
+    // Values of the tile that are not finite become 0; or, as markers, they become 1 and all others 0. Every thread
+    // of the workgroup takes part, barriers are the caller's.
+    __device__ static void only_finite(char *s, bool markers)
     {
-#pragma unroll
-        for (int n = 0; n < kUnits; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < kWide; ++j) {
-                    const float x = to_float(g.x[n][i][j]);
-                    const bool fine = x - x == 0.0f;
-                    g.x[n][i][j] = static_cast<T>(markers ? (fine ? 0.0f : 1.0f) : (fine ? x : 0.0f));
-                }
+        T *x = reinterpret_cast<T *>(s);
+        for (int i = threadIdx.x; i < kTileRows * kD; i += 64 * kWaves) {
+            const float y = to_float(x[i]);
+            const bool fine = y - y == 0.0f;
+            x[i] = static_cast<T>(markers ? (fine ? 0.0f : 1.0f) : (fine ? y : 0.0f));
+        }
     }
 };
 
