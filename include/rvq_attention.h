@@ -58,7 +58,8 @@ typedef struct rvq_heads {
  * cu_k[b+1]-1 (device int32 [n_clips + 1], non-decreasing, within
  * 0..q_tokens / 0..k_tokens). Its queries are the last ones of its keys'
  * positions: query i of n_q is at position i + n_k - n_q. Rows outside every
- * clip are neither read nor written. Offsets that break these rules give
+ * clip have no influence (in float16 gradients: but for the choice of a power
+ * of two) and are not written. Offsets that break these rules give
  * unspecified results, but no access outside the arrays.
  *
  * dim must be 64 or 128, q_heads a multiple of kv_heads (query head h reads
@@ -99,7 +100,9 @@ RVQ_API rvq_status rvq_window_attention(const rvq_attention_shape *shape, const 
  *   dout, q, k, v   as in the forward pass, dout laid out like out
  *   out, lse        what the forward pass gave
  *   dq, dk, dv      outputs, laid out like q, k, v; keys and values shared
- *                   by several query heads get the sum over them
+ *                   by several query heads get the sum over them. A value of q, k, v or
+ *                   dout that is not finite reaches the gradients of the
+ *                   queries that see it and of the keys they see, no others
  *   workspace       device memory of at least
  *                   rvq_window_attention_backward_bytes(shape) bytes,
  *                   16-byte aligned (the size is a negative rvq_status for

@@ -1,12 +1,29 @@
 // Gradient of the windowed attention with sinks.
 //
-//   x_ij = scale q_i . k_j over the keys j that query i sees,
-//   w = softmax(x), out_i = sum_j w_ij v_j, lse_i = log sum_j exp(x_ij)
-//   delta_i = dout_i . out_i,  dw_ij = dout_i . v_j,  dx_ij = w_ij (dw_ij - delta_i)
+//   x_ij = scale q_i . k_j,  w_ij = exp(x_ij - lse_i),  delta_i = dout_i . out_i
+//   dw_ij = dout_i . v_j,  dx_ij = w_ij (dw_ij - delta_i)
 //   dq_i = scale sum_j dx_ij k_j,  dk_j = scale sum_i dx_ij q_i,  dv_j = sum_i w_ij dout_i
 //
-// One wavefront a row: a query with its keys one after another (dq)
-// or a key with the queries that see it (dk, dv), lanes over the head dim.
+// Three launches and no atomics, so the sums' order is fixed: row statistics,
+// dq (queries in registers, keys go by), dk and dv (keys in registers, queries
+// go by, all query heads of a key head one after another). Scores and dw are
+// made twice, 14 dim flops a pair with the forward pass' 4 make 18 where 14
+// would do; in exchange no partial dq goes through memory.
+// Bound by the matrix cores and the LDS reads that feed them, as in the
+// forward pass, with the same operand layouts: a lane keeps to one query (dq)
+// or one key (dk, dv), and what a product leaves in it is the next one's operand.
+//
+// Weights and dx enter the products in the inputs' type. bfloat16 has float32's
+// range, but float16 has 5 bits of exponent, so there weights are taken times
+// 2^4 and dx is brought near 1 by powers of two: dq by its own row's largest
+// |dout|, dk by the whole call's (a sum over rows needs one factor); both leave
+// again in float32 at the end. Powers of two change no rounding.
+//
+// The first sinks of a clip are seen by all of its later queries, hundreds of
+// tiles where other keys have a window's. When that matters (see split_sinks)
+// the queries beyond the window go in pieces of kFarRows to workgroups of their
+// own, and a last launch adds the float32 parts in order.
+#include <float.h>
 #include <limits.h>
 #include <stdint.h>
 
@@ -14,144 +31,492 @@
 
 #include "attention_device.h"
 #include "attention_internal.h"
+#include "attention_tiles.h"
 
 namespace rvq {
 namespace {
 
-constexpr int kRowsPerBlock = 4;
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kRows = 32 * kWaves;      // queries (dq) or keys (dk, dv) a workgroup
+constexpr int kFarRows = 1024;          // queries of a piece beyond the window
+constexpr int kMaxSplitSinks = 64;
 
-template <typename T, int kD>
-__device__ inline void load_row(const Heads &h, int64_t row, int head, int lane, float (&x)[kD / 64])
+// Workspace: lse in powers of two (+inf for rows that see nothing, so that their weights are 0) and delta a query
+// and head, then the float32 parts of the sinks' gradients, { dk, dv } [sinks][dim] each.
+struct Work {
+    float *lse2, *delta;     // [q_heads][q_tokens]
+    uint32_t *largest;       // bits of the largest finite |dout| (float16 only)
+    float *near;             // [n_clips][kv_heads]
+    float *far;              // [far slots][kv_heads][2]
+    bool split;
+};
+
+int64_t rounded(int64_t floats) { return (floats + 3) / 4 * 4; }
+
+int64_t far_slots(int64_t q_tokens, int n_clips) { return q_tokens / kFarRows + n_clips + 1; }
+
+// Sinks are split off where clips are long on average: short ones have too few queries for their sinks to last
+// longer than the rest.
+bool split_sinks(int64_t q_tokens, int n_clips, int sinks)
 {
-    const T *p = static_cast<const T *>(h.data) + row * h.token + head * h.head;
-#pragma unroll
-    for (int i = 0; i < kD / 64; ++i) x[i] = to_float(p[lane + 64 * i]);
+    return sinks > 0 && sinks <= kMaxSplitSinks && q_tokens / 2 >= static_cast<int64_t>(n_clips) * kFarRows;
 }
 
-template <typename T, int kD>
-__device__ inline void store_row(const Heads &h, int64_t row, int head, int lane, const float (&x)[kD / 64])
+int64_t work_floats(int64_t q_tokens, int n_clips, int q_heads, int kv_heads, int dim, int sinks)
 {
-    T *p = static_cast<T *>(h.data) + row * h.token + head * h.head;
-#pragma unroll
-    for (int i = 0; i < kD / 64; ++i) p[lane + 64 * i] = static_cast<T>(x[i]);
+    int64_t n = 2 * rounded(q_tokens * q_heads) + 4;
+    if (split_sinks(q_tokens, n_clips, sinks))
+        n += (n_clips + 2 * far_slots(q_tokens, n_clips)) * kv_heads * sinks * dim * 2;
+    return n;
 }
 
-template <int kN>
-__device__ inline float dot(const float (&x)[kN], const float (&y)[kN])
+Work work_of(const AttentionArgs &a)
 {
+    Work w;
+    w.lse2 = static_cast<float *>(a.workspace);
+    w.delta = w.lse2 + rounded(a.q_tokens * a.q_heads);
+    w.largest = reinterpret_cast<uint32_t *>(w.delta + rounded(a.q_tokens * a.q_heads));
+    w.near = reinterpret_cast<float *>(w.largest) + 4;
+    w.far = w.near + static_cast<int64_t>(a.n_clips) * a.kv_heads * a.sinks * a.dim * 2;
+    w.split = a.window != INT_MAX && split_sinks(a.q_tokens, a.n_clips, a.sinks);
+    return w;
+}
+
+template <typename T> constexpr bool kNarrow = false;      // few exponent bits
+template <> constexpr bool kNarrow<f16_t> = true;
+constexpr float kWeightShift = 4.0f;                       // float16 weights are taken times 2^this
+
+__device__ inline bool not_finite(float x) { return !(fabsf(x) <= FLT_MAX); }
+
+// e with 2^(e - 1) <= x < 2^e, 0 for x = 0 and values that are not finite.
+__device__ inline int exponent_of(float x) { return x == 0.0f || not_finite(x) ? 0 : __builtin_amdgcn_frexp_expf(x); }
+
+__global__ void clear_largest(Work work) { *work.largest = 0; }
+
+// lse2 and delta; kD / 8 lanes a row. Bound by HBM (out and dout once).
+template <typename T, int kD>
+__global__ __launch_bounds__(kThreads)
+void row_statistics(AttentionArgs a, Work work)
+{
+    constexpr int kLanes = kD / 8;
+    const int64_t at = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / kLanes;
+    const int part = threadIdx.x % kLanes;
+    if (at >= a.q_tokens * a.q_heads) return;
+    const int64_t row = at / a.q_heads;
+    const int head = static_cast<int>(at - row * a.q_heads);
+    const vec8<T> g = load8(static_cast<const T *>(a.dout.data) + row * a.dout.token + head * a.dout.head + 8 * part);
+    const vec8<T> o = load8(static_cast<const T *>(a.out.data) + row * a.out.token + head * a.out.head + 8 * part);
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kN; ++i) s += x[i] * y[i];
-    return wave_sum(s);
+    for (int i = 0; i < 8; ++i) s += to_float(g[i]) * to_float(o[i]);
+#pragma unroll
+    for (int m = kLanes / 2; m > 0; m >>= 1) s += __shfl_xor(s, m);
+    if (part == 0) {
+        const int64_t to = head * a.q_tokens + row;
+        const float lse = a.lse[to];
+        work.delta[to] = s;
+        work.lse2[to] = lse == -INFINITY ? INFINITY : lse * kLog2e;
+    }
+    if constexpr (kNarrow<T>) {
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, not_finite(to_float(g[i])) ? 0.0f : fabsf(to_float(g[i])));
+#pragma unroll
+        for (int m = 32; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
+        // a maximum does not depend on the order in which it is taken
+        if ((threadIdx.x & 63) == 0 && top > 0.0f) atomicMax(work.largest, __float_as_uint(top));
+    }
 }
 
-__device__ inline bool find_row(const int32_t *cu, int n_clips, int64_t tokens, int row, int &clip)
-{
-    int first, count;
-    clip = clip_of_row(cu, n_clips, row);
-    clip_range(cu, clip, tokens, first, count);
-    return row >= first && row < first + count;
-}
-
-// delta[head, row] = dout . out
+// Rows of a tile with a value that is not finite: their flag is set and they become zeros. Barriers are the caller's.
 template <typename T, int kD>
-__global__ __launch_bounds__(64 * kRowsPerBlock)
-void delta_rows(AttentionArgs a)
+__device__ inline void clear_bad_rows(char *s, int *flags)
 {
-    const int lane = threadIdx.x & 63;
-    const int row = blockIdx.x * kRowsPerBlock + (threadIdx.x >> 6), head = blockIdx.y;
-    int clip;
-    if (row >= a.q_tokens || !find_row(a.cu_q, a.n_clips, a.q_tokens, row, clip)) return;
-    float g[kD / 64], o[kD / 64];
-    load_row<T, kD>(a.dout, row, head, lane, g);
-    load_row<T, kD>(a.out, row, head, lane, o);
-    const float s = dot(g, o);
-    if (lane == 0) static_cast<float *>(a.workspace)[static_cast<int64_t>(head) * a.q_tokens + row] = s;
+    constexpr int kLanes = kThreads / kTileRows;
+    const int row = threadIdx.x / kLanes;
+    T *x = reinterpret_cast<T *>(s) + row * kD;
+    bool bad = false;
+    for (int i = threadIdx.x % kLanes; i < kD; i += kLanes) bad = bad || not_finite(to_float(x[i]));
+#pragma unroll
+    for (int m = 1; m < kLanes; m <<= 1) bad = __shfl_xor(static_cast<int>(bad), m) || bad;
+    if (bad) {
+        flags[row] = 1;
+        for (int i = threadIdx.x % kLanes; i < kD; i += kLanes) x[i] = static_cast<T>(0.0f);
+    }
 }
 
+// dq. As in the forward pass a workgroup takes 128 queries and goes over the tiles of keys they see. If a result is
+// not finite, a second pass takes rows of K that are not finite as zeros and the weights of the queries that do see
+// them as NaN, so that only those get it.
 template <typename T, int kD>
-__global__ __launch_bounds__(64 * kRowsPerBlock)
-void dq_rows(AttentionArgs a)
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
+void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
 {
-    const int lane = threadIdx.x & 63;
-    const int row = blockIdx.x * kRowsPerBlock + (threadIdx.x >> 6), head = blockIdx.y;
-    if (row >= a.q_tokens) return;
-    int clip, q0, nq, k0, nk;
-    if (!find_row(a.cu_q, a.n_clips, a.q_tokens, row, clip)) return;
-    clip_range(a.cu_q, clip, a.q_tokens, q0, nq);
-    clip_range(a.cu_k, clip, a.k_tokens, k0, nk);
+    typedef Tile<T, kD, kWaves> Rows;
+    __shared__ __attribute__((aligned(16))) char s_mem[4 * Rows::kBytes];
+    __shared__ int s_bad[kTileRows];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int c = lane & 31, half = lane >> 5;
+    const int slot = slots - 1 - static_cast<int>(blockIdx.x / a.q_heads), head = blockIdx.x % a.q_heads;
     const int kv = head / (a.q_heads / a.kv_heads);
-    const int p = row - q0 + nk - nq;
-    const int64_t first = static_cast<int64_t>(p) - a.window + 1;
-    const int64_t at = static_cast<int64_t>(head) * a.q_tokens + row;
-    const float lse = a.lse[at], delta = static_cast<const float *>(a.workspace)[at];
-    float q[kD / 64], k[kD / 64], v[kD / 64], g[kD / 64], dq[kD / 64] = {};
-    load_row<T, kD>(a.q, row, head, lane, q);
-    load_row<T, kD>(a.dout, row, head, lane, g);
-    if (lse != -INFINITY) {
-        for (int j = 0; j <= p; ++j) {
-            if (j < first && j >= a.sinks) {
-                j = static_cast<int>(first) - 1;
-                continue;
-            }
-            load_row<T, kD>(a.k, k0 + j, kv, lane, k);
-            load_row<T, kD>(a.v, k0 + j, kv, lane, v);
-            const float w = exp2f((dot(q, k) * a.scale - lse) * kLog2e);
-            const float dx = w * (dot(g, v) - delta) * a.scale;
-#pragma unroll
-            for (int i = 0; i < kD / 64; ++i) dq[i] += dx * k[i];
-        }
-    }
-    store_row<T, kD>(a.dq, row, head, lane, dq);
-}
-
-template <typename T, int kD>
-__global__ __launch_bounds__(64 * kRowsPerBlock)
-void dkv_rows(AttentionArgs a)
-{
-    const int lane = threadIdx.x & 63;
-    const int row = blockIdx.x * kRowsPerBlock + (threadIdx.x >> 6), kv = blockIdx.y;
-    if (row >= a.k_tokens) return;
-    int clip, q0, nq, k0, nk;
-    if (!find_row(a.cu_k, a.n_clips, a.k_tokens, row, clip)) return;
+    const int clip = clip_of_slot(a.cu_q, a.n_clips, slot, kRows);
+    int q0, nq, k0, nk;
     clip_range(a.cu_q, clip, a.q_tokens, q0, nq);
     clip_range(a.cu_k, clip, a.k_tokens, k0, nk);
-    const int j = row - k0, group = a.q_heads / a.kv_heads;
-    const int64_t last = j < a.sinks ? nk : static_cast<int64_t>(j) + a.window;   // positions below it see j
-    float q[kD / 64], k[kD / 64], v[kD / 64], g[kD / 64], dk[kD / 64] = {}, dv[kD / 64] = {};
-    load_row<T, kD>(a.k, row, kv, lane, k);
-    load_row<T, kD>(a.v, row, kv, lane, v);
-    for (int h = kv * group; h < (kv + 1) * group; ++h) {
-        for (int64_t p = max(j, nk - nq); p < min(static_cast<int64_t>(nk), last); ++p) {
-            const int64_t qr = q0 + p - (nk - nq), at = h * a.q_tokens + qr;
-            const float lse = a.lse[at], delta = static_cast<const float *>(a.workspace)[at];
-            if (lse == -INFINITY) continue;
-            load_row<T, kD>(a.q, qr, h, lane, q);
-            load_row<T, kD>(a.dout, qr, h, lane, g);
-            const float w = exp2f((dot(q, k) * a.scale - lse) * kLog2e);
-            const float dx = w * (dot(g, v) - delta) * a.scale;
+    const int i0 = (slot - (a.cu_q[clip] / kRows + clip)) * kRows;
+    if (i0 < 0 || i0 >= nq) return;
+
+    const int back = nk - nq;
+    const int row = i0 + 32 * wave + c;
+    const int p = row + back;
+    const KeyRange range = keys_seen(i0 + back, min(i0 + kRows, nq) - 1 + back, a.window, a.sinks);
+    const int w_first = i0 + 32 * wave + back, w_last = min(i0 + 32 * wave + 31, nq - 1) + back;
+    const int p_low = below_window(p, a.window), w_low = below_window(w_first, a.window);
+    const int w_high = below_window(w_last, a.window);
+    const int64_t at = q0 + min(row, nq - 1);
+    float lse2 = work.lse2[head * a.q_tokens + at], unit = a.scale;
+    const float delta = work.delta[head * a.q_tokens + at];
+
+    vec8<T> q[kD / 16], g[kD / 16];
 #pragma unroll
-            for (int i = 0; i < kD / 64; ++i) {
-                dk[i] += dx * q[i];
-                dv[i] += w * g[i];
+    for (int t = 0; t < kD / 16; ++t) {
+        q[t] = load8(static_cast<const T *>(a.q.data) + at * a.q.token + head * a.q.head + 16 * t + 8 * half);
+        g[t] = load8(static_cast<const T *>(a.dout.data) + at * a.dout.token + head * a.dout.head + 16 * t + 8 * half);
+    }
+    if constexpr (kNarrow<T>) {
+        float top = 0.0f;
+#pragma unroll
+        for (int t = 0; t < kD / 16; ++t)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(to_float(g[t][i])));
+        const float shift = kWeightShift - exponent_of(fmaxf(top, __shfl_xor(top, 32)));
+        lse2 -= shift;
+        unit *= fast_exp2(-shift);
+    }
+    const T *keys = static_cast<const T *>(a.k.data) + static_cast<int64_t>(k0) * a.k.token + kv * a.k.head;
+    const T *values = static_cast<const T *>(a.v.data) + static_cast<int64_t>(k0) * a.v.token + kv * a.v.head;
+
+    f32x16 dq[kD / 32];
+    for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll
+        for (int n = 0; n < kD / 32; ++n) dq[n] = f32x16{};
+        if (range.tiles > 0) {
+            Rows::load(s_mem, keys, a.k.token, range.start(0), nk);
+            Rows::load(s_mem + Rows::kBytes, values, a.v.token, range.start(0), nk);
+        }
+        for (int t = 0; t < range.tiles; ++t) {
+            char *s_k = s_mem + (t & 1) * 2 * Rows::kBytes, *s_v = s_k + Rows::kBytes;
+            wait_copies();
+            __syncthreads();     // tile t is there, tile t - 1 is no longer read
+            if (t + 1 < range.tiles) {
+                char *s_next = s_mem + ((t + 1) & 1) * 2 * Rows::kBytes;
+                Rows::load(s_next, keys, a.k.token, range.start(t + 1), nk);
+                Rows::load(s_next + Rows::kBytes, values, a.v.token, range.start(t + 1), nk);
+            }
+            if (pass) {
+                if (threadIdx.x < kTileRows) s_bad[threadIdx.x] = 0;
+                __syncthreads();
+                clear_bad_rows<T, kD>(s_k, s_bad);
+                __syncthreads();
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int j0 = range.start(t) + 32 * b;
+                if (j0 > w_last || (j0 + 31 <= w_low && j0 >= a.sinks)) continue;
+                f32x16 x = {}, y = {};
+#pragma unroll
+                for (int n = 0; n < kD / 16; ++n) {
+                    x = mma32(Rows::along(s_k, 32 * b + c, 2 * n + half), q[n], x);
+                    y = mma32(Rows::along(s_v, 32 * b + c, 2 * n + half), g[n], y);
+                }
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    x[r] = fast_exp2(__builtin_fmaf(x[r], factor, -lse2));
+                    y[r] = x[r] * (y[r] - delta);
+                }
+                if (pass || !(j0 + 31 <= w_first && (j0 > w_high || j0 + 31 < a.sinks))) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const int in = 8 * (r >> 2) + 4 * half + (r & 3), j = j0 + in;
+                        if (pass && s_bad[32 * b + in]) y[r] = __builtin_nanf("");
+                        y[r] = j <= p && (j > p_low || j < a.sinks) ? y[r] : 0.0f;
+                    }
+                }
+                vec8<T> w[2];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) w[r >> 3][r & 7] = static_cast<T>(y[r]);
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int n = 0; n < kD / 32; ++n) dq[n] = mma32(Rows::across(s_k, n, 2 * b + s), w[s], dq[n]);
             }
         }
+        bool odd = false;
+#pragma unroll
+        for (int n = 0; n < kD / 32; ++n)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) odd = odd || not_finite(dq[n][r]);
+        if (!__syncthreads_or(odd)) break;     // and the tiles are no longer read
     }
-    store_row<T, kD>(a.dk, row, kv, lane, dk);
-    store_row<T, kD>(a.dv, row, kv, lane, dv);
+    if (row >= nq) return;
+    T *out = static_cast<T *>(a.dq.data) + at * a.dq.token + head * a.dq.head;
+#pragma unroll
+    for (int n = 0; n < kD / 32; ++n)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            T e[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[i] = static_cast<T>(dq[n][4 * r + i] * unit);
+            store4(out + 32 * n + 8 * r + 4 * half, e);
+        }
 }
 
-unsigned blocks(int64_t rows) { return static_cast<unsigned>((rows + kRowsPerBlock - 1) / kRowsPerBlock); }
+// dk and dv. A workgroup takes 128 keys of a key head, 32 a wavefront, and goes over the queries that see them, one
+// query head after another. kFar: the sinks with the queries beyond the first keys' window, kFarRows of them; the
+// wavefronts share the sinks (32 each) and take half of a tile's queries each.
+template <typename T, int kD, bool kFar>
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 && kD == 64 ? 2 : 1)
+void dkv_tiles(AttentionArgs a, Work work, float factor)
+{
+    typedef Tile<T, kD, kWaves> Rows;
+    __shared__ __attribute__((aligned(16))) char s_mem[4 * Rows::kBytes];
+    __shared__ __attribute__((aligned(16))) float s_stats[2][2][kTileRows];     // [buffer][lse2, delta][query]
+    __shared__ int s_bad[kTileRows];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 31, half = lane >> 5;
+    const int slot = blockIdx.x / a.kv_heads, kv = blockIdx.x % a.kv_heads, group = a.q_heads / a.kv_heads;
+    const int32_t *cu = kFar ? a.cu_q : a.cu_k;
+    constexpr int kPer = kFar ? kFarRows : kRows;
+    const int clip = clip_of_slot(cu, a.n_clips, slot, kPer);
+    int q0, nq, k0, nk;
+    clip_range(a.cu_q, clip, a.q_tokens, q0, nq);
+    clip_range(a.cu_k, clip, a.k_tokens, k0, nk);
+    const int64_t first = (slot - (cu[clip] / kPer + clip)) * static_cast<int64_t>(kPer);
+    if (first < 0 || first >= (kFar ? nq : nk) || nk == 0) return;
+
+    const int back = nk - nq;
+    const int j_tile = kFar ? 0 : static_cast<int>(first);       // the workgroup's first key
+    const int key = j_tile + (kFar ? 32 * (wave >> 1) : 32 * wave) + c;
+    // positions that see the workgroup's keys: below near_end through the window, all later ones see the sinks
+    const int near_end = static_cast<int>(min(static_cast<int64_t>(nk), static_cast<int64_t>(j_tile) + kRows - 1 + a.window));
+    int i_first, i_end, hi = 0;       // queries gone over; position below which this lane's key is seen
+    if (kFar) {
+        i_first = max(static_cast<int>(first), near_end - back);
+        i_end = static_cast<int>(min(static_cast<int64_t>(nq), first + kFarRows));
+        if (key < min(a.sinks, nk)) hi = nk;
+    } else {
+        const bool all = !work.split && j_tile < a.sinks;
+        i_first = max(0, j_tile - back);
+        i_end = (all ? nk : near_end) - back;
+        if (key < nk) hi = static_cast<int>(min(static_cast<int64_t>(all && key < a.sinks ? INT_MAX : static_cast<int64_t>(key) + a.window), static_cast<int64_t>(nk)));
+        // with the sinks split off, their queries up to near_end still belong here
+        if (work.split && key < min(a.sinks, nk)) hi = near_end;
+    }
+    const int i_start = i_first / kTileRows * kTileRows;
+    const int per_head = i_end > i_first ? (i_end - i_start + kTileRows - 1) / kTileRows : 0;
+    const int tiles = per_head * group;
+    const int key_first = __builtin_amdgcn_readfirstlane(key - c), key_last = key_first + 31;
+    // below this position all of the wavefront's keys are seen, from the other on none
+    int hi_all = hi, hi_any = hi;
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) {
+        hi_all = min(hi_all, __shfl_xor(hi_all, m));
+        hi_any = max(hi_any, __shfl_xor(hi_any, m));
+    }
+
+    // float16: dw and delta times `small`, weights times 2^kWeightShift
+    float small = 1.0f, unit_k = 1.0f, unit_v = 1.0f;
+    if constexpr (kNarrow<T>) {
+        const int e = exponent_of(__uint_as_float(*work.largest));
+        small = fast_exp2(static_cast<float>(-e));
+        unit_v = fast_exp2(-kWeightShift);
+        unit_k = fast_exp2(static_cast<float>(e) - kWeightShift);
+    }
+    vec8<T> k[kD / 16], v[kD / 16];
+    {
+        const int64_t row = k0 + min(key, nk - 1);
+#pragma unroll
+        for (int t = 0; t < kD / 16; ++t) {
+            k[t] = load8(static_cast<const T *>(a.k.data) + row * a.k.token + kv * a.k.head + 16 * t + 8 * half);
+            v[t] = load8(static_cast<const T *>(a.v.data) + row * a.v.token + kv * a.v.head + 16 * t + 8 * half);
+        }
+    }
+    auto load = [&](int buffer, int head, int i) {
+        char *s = s_mem + buffer * 2 * Rows::kBytes;
+        Rows::load(s, static_cast<const T *>(a.q.data) + static_cast<int64_t>(q0) * a.q.token + head * a.q.head, a.q.token, i, nq);
+        Rows::load(s + Rows::kBytes, static_cast<const T *>(a.dout.data) + static_cast<int64_t>(q0) * a.dout.token + head * a.dout.head,
+                   a.dout.token, i, nq);
+        if (wave < 2)
+            copy4((wave ? work.delta : work.lse2) + head * a.q_tokens + q0 + min(i + lane, nq - 1), s_stats[buffer][wave]);
+    };
+
+    f32x16 dk[kD / 32], dv[kD / 32];
+    for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll
+        for (int n = 0; n < kD / 32; ++n) dk[n] = dv[n] = f32x16{};
+        int head = kv * group, i = i_start;
+        if (tiles > 0) load(0, head, i);
+        for (int t = 0; t < tiles; ++t) {
+            char *s_q = s_mem + (t & 1) * 2 * Rows::kBytes, *s_g = s_q + Rows::kBytes;
+            const int i_tile = i;
+            wait_copies();
+            __syncthreads();     // tile t is there, tile t - 1 is no longer read
+            i += kTileRows;
+            if (i >= i_end) {
+                i = i_start;
+                ++head;
+            }
+            if (t + 1 < tiles) load((t + 1) & 1, head, i);
+            if (pass) {
+                if (threadIdx.x < kTileRows) s_bad[threadIdx.x] = 0;
+                __syncthreads();
+                clear_bad_rows<T, kD>(s_q, s_bad);
+                clear_bad_rows<T, kD>(s_g, s_bad);
+                __syncthreads();
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int p0 = i_tile + 32 * b + back;       // position of the first of these 32 queries
+                if (p0 + 31 < key_first || p0 >= hi_any) continue;
+                if (kFar && (b != (wave & 1) || p0 + 31 < i_first + back)) continue;
+                f32x16 x = {}, y = {};
+#pragma unroll
+                for (int n = 0; n < kD / 16; ++n) {
+                    x = mma32(Rows::along(s_q, 32 * b + c, 2 * n + half), k[n], x);
+                    y = mma32(Rows::along(s_g, 32 * b + c, 2 * n + half), v[n], y);
+                }
+                const bool whole = p0 >= key_last && p0 + 31 < hi_all && !kFar && !pass;
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    const int in = 32 * b + 8 * f + 4 * half;
+                    const f32x4 lse2 = *reinterpret_cast<const f32x4 *>(&s_stats[t & 1][0][in]);
+                    const f32x4 delta = *reinterpret_cast<const f32x4 *>(&s_stats[t & 1][1][in]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int r = 4 * f + e;
+                        if constexpr (kNarrow<T>) {
+                            x[r] = fast_exp2(__builtin_fmaf(x[r], factor, kWeightShift - lse2[e]));
+                            y[r] = x[r] * __builtin_fmaf(y[r], small, -small * delta[e]);
+                        } else {
+                            x[r] = fast_exp2(__builtin_fmaf(x[r], factor, -lse2[e]));
+                            y[r] = x[r] * (y[r] - delta[e]);
+                        }
+                    }
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const int in = 8 * (r >> 2) + 4 * half + (r & 3), p = p0 + in;
+                        bool sees = p >= key && p < hi;
+                        if (kFar) sees = sees && p - back >= i_first && p - back < i_end;
+                        if (pass && s_bad[32 * b + in]) x[r] = y[r] = __builtin_nanf("");
+                        x[r] = sees ? x[r] : 0.0f;
+                        y[r] = sees ? y[r] : 0.0f;
+                    }
+                }
+                vec8<T> w[2], d[2];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    w[r >> 3][r & 7] = static_cast<T>(x[r]);
+                    d[r >> 3][r & 7] = static_cast<T>(y[r]);
+                }
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int n = 0; n < kD / 32; ++n) {
+                        dv[n] = mma32(Rows::across(s_g, n, 2 * b + s), w[s], dv[n]);
+                        dk[n] = mma32(Rows::across(s_q, n, 2 * b + s), d[s], dk[n]);
+                    }
+            }
+        }
+        bool odd = false;
+#pragma unroll
+        for (int n = 0; n < kD / 32; ++n)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) odd = odd || not_finite(dk[n][r]) || not_finite(dv[n][r]);
+        if (!__syncthreads_or(odd)) break;     // and the tiles are no longer read
+    }
+    if (key >= nk) return;
+    if (kFar || (work.split && key < a.sinks)) {
+        if (key >= a.sinks) return;
+        const int64_t which = kFar ? (static_cast<int64_t>(slot) * a.kv_heads + kv) * 2 + (wave & 1)
+                                   : static_cast<int64_t>(clip) * a.kv_heads + kv;
+        float *to = (kFar ? work.far : work.near) + (which * a.sinks + key) * 2 * kD;
+#pragma unroll
+        for (int n = 0; n < kD / 32; ++n)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int d0 = 32 * n + 8 * r + 4 * half;
+                *reinterpret_cast<f32x4 *>(to + d0) = f32x4{dk[n][4 * r], dk[n][4 * r + 1], dk[n][4 * r + 2], dk[n][4 * r + 3]} * unit_k;
+                *reinterpret_cast<f32x4 *>(to + kD + d0) = f32x4{dv[n][4 * r], dv[n][4 * r + 1], dv[n][4 * r + 2], dv[n][4 * r + 3]} * unit_v;
+            }
+        return;
+    }
+    T *out_k = static_cast<T *>(a.dk.data) + (k0 + static_cast<int64_t>(key)) * a.dk.token + kv * a.dk.head;
+    T *out_v = static_cast<T *>(a.dv.data) + (k0 + static_cast<int64_t>(key)) * a.dv.token + kv * a.dv.head;
+#pragma unroll
+    for (int n = 0; n < kD / 32; ++n)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            T e[4], f[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                e[x] = static_cast<T>(dk[n][4 * r + x] * (a.scale * unit_k));
+                f[x] = static_cast<T>(dv[n][4 * r + x] * unit_v);
+            }
+            store4(out_k + 32 * n + 8 * r + 4 * half, e);
+            store4(out_v + 32 * n + 8 * r + 4 * half, f);
+        }
+}
+
+// The sinks' gradients: the part within the first keys' window, then the pieces beyond it in order.
+template <typename T, int kD>
+__global__ __launch_bounds__(2 * kD)
+void join_sinks(AttentionArgs a, Work work)
+{
+    const int key = blockIdx.x, kv = blockIdx.y, d = threadIdx.x;      // d < kD: dk, others dv
+    for (int clip = blockIdx.z; clip < a.n_clips; clip += gridDim.z) {
+        int q0, nq, k0, nk;
+        clip_range(a.cu_q, clip, a.q_tokens, q0, nq);
+        clip_range(a.cu_k, clip, a.k_tokens, k0, nk);
+        if (key >= nk) continue;
+        float sum = work.near[((static_cast<int64_t>(clip) * a.kv_heads + kv) * a.sinks + key) * 2 * kD + d];
+        const int64_t base = q0 / kFarRows + clip;
+        for (int piece = 0; piece * static_cast<int64_t>(kFarRows) < nq; ++piece)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                sum += work.far[((((base + piece) * a.kv_heads + kv) * 2 + h) * a.sinks + key) * 2 * kD + d];
+        const int64_t row = k0 + key;
+        if (d < kD)
+            (static_cast<T *>(a.dk.data) + row * a.dk.token + kv * a.dk.head)[d] = static_cast<T>(sum * a.scale);
+        else
+            (static_cast<T *>(a.dv.data) + row * a.dv.token + kv * a.dv.head)[d - kD] = static_cast<T>(sum);
+    }
+}
 
 template <typename T, int kD>
 hipError_t backward(const AttentionArgs &a, hipStream_t stream)
 {
+    const Work work = work_of(a);
+    const float factor = fmaxf(a.scale * kLog2e, FLT_MIN);     // as in the forward pass
+    const int64_t q_slots = a.q_tokens / kRows + a.n_clips + 1, k_slots = a.k_tokens / kRows + a.n_clips + 1;
+    const int64_t lanes = a.q_tokens * a.q_heads * (kD / 8);
+    if (q_slots * a.q_heads > INT_MAX || k_slots * a.kv_heads > INT_MAX || lanes / kThreads >= INT_MAX)
+        return hipErrorInvalidConfiguration;
     if (a.q_tokens > 0) {
-        delta_rows<T, kD><<<dim3(blocks(a.q_tokens), a.q_heads), 64 * kRowsPerBlock, 0, stream>>>(a);
-        dq_rows<T, kD><<<dim3(blocks(a.q_tokens), a.q_heads), 64 * kRowsPerBlock, 0, stream>>>(a);
+        if (kNarrow<T>) clear_largest<<<1, 1, 0, stream>>>(work);
+        row_statistics<T, kD><<<static_cast<unsigned>((lanes + kThreads - 1) / kThreads), kThreads, 0, stream>>>(a, work);
+        dq_tiles<T, kD><<<static_cast<unsigned>(q_slots * a.q_heads), kThreads, 0, stream>>>(a, work, factor, static_cast<int>(q_slots));
     }
-    if (a.k_tokens > 0)
-        dkv_rows<T, kD><<<dim3(blocks(a.k_tokens), a.kv_heads), 64 * kRowsPerBlock, 0, stream>>>(a);
+    if (a.k_tokens > 0) {
+        if (work.split)
+            dkv_tiles<T, kD, true><<<static_cast<unsigned>(far_slots(a.q_tokens, a.n_clips) * a.kv_heads), kThreads, 0, stream>>>(
+                a, work, factor);
+        dkv_tiles<T, kD, false><<<static_cast<unsigned>(k_slots * a.kv_heads), kThreads, 0, stream>>>(a, work, factor);
+        if (work.split)
+            join_sinks<T, kD><<<dim3(a.sinks, a.kv_heads, a.n_clips < 1024 ? a.n_clips : 1024), 2 * kD, 0, stream>>>(a, work);
+    }
     return hipGetLastError();
 }
 
@@ -160,7 +525,7 @@ hipError_t backward(const AttentionArgs &a, hipStream_t stream)
 int64_t window_attention_backward_bytes(int64_t q_tokens, int64_t k_tokens, int n_clips, int q_heads, int kv_heads,
                                         int dim, int sinks)
 {
-    return q_tokens * q_heads * 4;
+    return work_floats(q_tokens, n_clips, q_heads, kv_heads, dim, sinks) * 4;
 }
 
 hipError_t launch_window_attention_backward(const AttentionArgs &a, hipStream_t stream)

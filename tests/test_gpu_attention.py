@@ -319,3 +319,43 @@ def test_nothing_to_do():
     _, k, v, _ = make(torch.bfloat16, 64, 4, 2, [0], [70])
     dq, dk, dv = m.rvq_window_attention_backward(dout, q, k, v, out, lse, ints([0, 0]), ints([0, 70]))
     assert (dk == 0).all() and (dv == 0).all()
+
+
+@pytest.mark.parametrize("typ", list(TYPES))
+def test_gradients_of_frames_apart_from_one_that_is_not_finite(typ):
+    """Frame j is not finite: queries that do not see it, and keys that no query with it sees, keep their gradients."""
+    m = rvq()
+    n, window, sinks = 300, 40, 2
+    q, k, v, dout = make(TYPES[typ], 64, 2, 1, [n], [n])
+    cu = ints([0, n])
+    out, lse = m.rvq_window_attention(q, k, v, cu, window=window, sinks=sinks)
+    clean = m.rvq_window_attention_backward(dout, q, k, v, out, lse, cu, window=window, sinks=sinks)
+    sees = oracle.sees(n, n, window, sinks).to(DEV)
+    for j in (37, 100, 160, 299):
+        for bad in (math.nan, math.inf):
+            for which in ("k", "v", "q", "dout"):
+                args = dict(q=q, k=k, v=v, dout=dout)
+                args[which] = args[which].clone()
+                args[which][j, 0, 7] = bad
+                x = [args[name] for name in ("dout", "q", "k", "v")]
+                o, s = m.rvq_window_attention(*x[1:], cu, window=window, sinks=sinks)
+                dq, dk, dv = m.rvq_window_attention_backward(*x, o, s, cu, window=window, sinks=sinks)
+                hurt = sees[:, j] if which in "kv" else torch.arange(n, device=DEV) == j     # queries
+                blind = ~(sees & hurt[:, None]).any(0)                                       # keys none of them sees
+                assert torch.equal(dq[~hurt], clean[0][~hurt]), (j, bad, which)
+                assert torch.equal(dk[blind], clean[1][blind]) and torch.equal(dv[blind], clean[2][blind]), (j, bad, which)
+                assert not torch.isfinite(dq[hurt][:, 0]).all(-1).any()
+
+
+def test_float16_gradients_of_small_and_large_size():
+    """dout of 2^-12 and of 2^9: the same relative error as at 1, to float16's own range."""
+    m = rvq()
+    lens = [500]
+    q, k, v, dout = make(torch.float16, 64, 2, 1, lens, lens)
+    cu = ints(offsets(lens))
+    out, lse = m.rvq_window_attention(q, k, v, cu)
+    for power in (-12, 9):
+        g = dout * 2.0 ** power
+        want = oracle.attention(q, k, v, offsets(lens), offsets(lens), None, 0, 1 / 8, g)
+        for name, x in zip(("dq", "dk", "dv"), m.rvq_window_attention_backward(g, q, k, v, out, lse, cu)):
+            close(name, x, want[name])
