@@ -43,7 +43,8 @@ typedef enum rvq_dtype {
 /*
  * A packed array of heads: element (t, h, d) is at
  * data[t * token_stride + h * head_stride + d], strides in elements. data and
- * both strides must be multiples of 16 bytes; rows may be slices of a wider
+ * both strides must be multiples of 16 bytes, token_stride below 2^23 - 16
+ * elements; rows may be slices of a wider
  * array (a fused projection's output). Output rows must not overlap.
  */
 typedef struct rvq_heads {

@@ -75,6 +75,7 @@ void forward_tiles(AttentionArgs a, float factor, int slots)
 #pragma unroll
         for (int t = 0; t < kD / 16; ++t) q[t] = load8(at + 16 * t + 8 * half);
     }
+    const typename Rows::Loader load_k(a.k.token), load_v(a.v.token);
     const T *keys = static_cast<const T *>(a.k.data) + static_cast<int64_t>(k0) * a.k.token + kv * a.k.head;
     const T *values = static_cast<const T *>(a.v.data) + static_cast<int64_t>(k0) * a.v.token + kv * a.v.head;
 
@@ -87,8 +88,8 @@ void forward_tiles(AttentionArgs a, float factor, int slots)
         m = -INFINITY;
         l = 0.0f;
         if (range.tiles > 0) {
-            Rows::load(s_mem, keys, a.k.token, range.start(0), nk);
-            Rows::load(s_mem + Rows::kBytes, values, a.v.token, range.start(0), nk);
+            load_k.load(s_mem, keys, range.start(0), nk);
+            load_v.load(s_mem + Rows::kBytes, values, range.start(0), nk);
         }
         for (int t = 0; t < range.tiles; ++t) {
             char *s_k = s_mem + (t & 1) * 2 * Rows::kBytes, *s_v = s_k + Rows::kBytes;
@@ -96,8 +97,8 @@ void forward_tiles(AttentionArgs a, float factor, int slots)
             __syncthreads();     // tile t is there, tile t - 1 is no longer read
             if (t + 1 < range.tiles) {
                 char *s_next = s_mem + ((t + 1) & 1) * 2 * Rows::kBytes;
-                Rows::load(s_next, keys, a.k.token, range.start(t + 1), nk);
-                Rows::load(s_next + Rows::kBytes, values, a.v.token, range.start(t + 1), nk);
+                load_k.load(s_next, keys, range.start(t + 1), nk);
+                load_v.load(s_next + Rows::kBytes, values, range.start(t + 1), nk);
             }
             if (pass != kPlain) {
                 Rows::only_finite(s_v, pass == kMarkers);
@@ -138,10 +139,14 @@ void forward_tiles(AttentionArgs a, float factor, int slots)
                 vec8<T> w[2];
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    float e = fast_exp2(__builtin_fmaf(x[r], factor, -safe));
+                    const float e = fast_exp2(__builtin_fmaf(x[r], factor, -safe));
                     l += e;
-                    if (pass == kMarkers) e = x[r] == -INFINITY ? 0.0f : 1.0f;
                     w[r >> 3][r & 7] = static_cast<T>(e);
+                }
+                if (pass == kMarkers) {
+                    asm volatile("");     // keeps this a branch, not 16 selects on the usual way
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) w[r >> 3][r & 7] = static_cast<T>(x[r] == -INFINITY ? 0.0f : 1.0f);
                 }
 #pragma unroll
                 for (int s = 0; s < 2; ++s)

@@ -19,12 +19,16 @@ rvq_status from_hip(hipError_t e) { return e == hipSuccess ? RVQ_OK : RVQ_ERR_DE
 
 int element_bytes(int32_t dtype) { return dtype == RVQ_F32 ? 4 : 2; }
 
+// 64 rows span less than 2^31 bytes
+constexpr int64_t kMaxTokenStride = (1 << 23) - 16;
+
 bool known_dtype(int32_t dtype) { return dtype == RVQ_F32 || dtype == RVQ_F16 || dtype == RVQ_BF16; }
 
 bool good_heads(const rvq_heads *h, int32_t dtype)
 {
     const int64_t row = 16 / element_bytes(dtype);
     return h && h->data && aligned(h->data, 16) && h->token_stride >= 0 && h->head_stride >= 0 &&
+           h->token_stride <= kMaxTokenStride &&
            h->token_stride % row == 0 && h->head_stride % row == 0;
 }
 

@@ -39,14 +39,16 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kRows = 32 * kWaves;      // queries (dq) or keys (dk, dv) a workgroup
-constexpr int kFarRows = 1024;          // queries of a piece beyond the window
+constexpr int kFarRows = 256;           // queries of a piece beyond the window
+constexpr int kLongClip = 2048;         // average clip from which the sinks are split off
 constexpr int kMaxSplitSinks = 64;
 
 // Workspace: lse in powers of two (+inf for rows that see nothing, so that their weights are 0) and delta a query
 // and head, then the float32 parts of the sinks' gradients, { dk, dv } [sinks][dim] each.
 struct Work {
     float *lse2, *delta;     // [q_heads][q_tokens]
-    uint32_t *largest;       // bits of the largest finite |dout| (float16 only)
+    float *largest;          // [largest_parts] largest finite |dout| of each workgroup of row_statistics (float16 only)
+    int largest_parts;
     float *near;             // [n_clips][kv_heads]
     float *far;              // [far slots][kv_heads][2]
     bool split;
@@ -60,12 +62,21 @@ int64_t far_slots(int64_t q_tokens, int n_clips) { return q_tokens / kFarRows + 
 // longer than the rest.
 bool split_sinks(int64_t q_tokens, int n_clips, int sinks)
 {
-    return sinks > 0 && sinks <= kMaxSplitSinks && q_tokens / 2 >= static_cast<int64_t>(n_clips) * kFarRows;
+    return sinks > 0 && sinks <= kMaxSplitSinks && q_tokens >= static_cast<int64_t>(n_clips) * kLongClip;
+}
+
+// Workgroups of row_statistics: they go over the rows in turn, so that there are at most kStatisticsGroups maxima.
+constexpr int kStatisticsGroups = 2048;
+
+int statistics_groups(int64_t q_tokens, int q_heads, int dim)
+{
+    const int64_t n = (q_tokens * q_heads * (dim / 8) + kThreads - 1) / kThreads;
+    return static_cast<int>(n < kStatisticsGroups ? n : kStatisticsGroups);
 }
 
 int64_t work_floats(int64_t q_tokens, int n_clips, int q_heads, int kv_heads, int dim, int sinks)
 {
-    int64_t n = 2 * rounded(q_tokens * q_heads) + 4;
+    int64_t n = 2 * rounded(q_tokens * q_heads) + kStatisticsGroups;
     if (split_sinks(q_tokens, n_clips, sinks))
         n += (n_clips + 2 * far_slots(q_tokens, n_clips)) * kv_heads * sinks * dim * 2;
     return n;
@@ -76,8 +87,9 @@ Work work_of(const AttentionArgs &a)
     Work w;
     w.lse2 = static_cast<float *>(a.workspace);
     w.delta = w.lse2 + rounded(a.q_tokens * a.q_heads);
-    w.largest = reinterpret_cast<uint32_t *>(w.delta + rounded(a.q_tokens * a.q_heads));
-    w.near = reinterpret_cast<float *>(w.largest) + 4;
+    w.largest = w.delta + rounded(a.q_tokens * a.q_heads);
+    w.largest_parts = statistics_groups(a.q_tokens, a.q_heads, a.dim);
+    w.near = w.largest + kStatisticsGroups;
     w.far = w.near + static_cast<int64_t>(a.n_clips) * a.kv_heads * a.sinks * a.dim * 2;
     w.split = a.window != INT_MAX && split_sinks(a.q_tokens, a.n_clips, a.sinks);
     return w;
@@ -92,40 +104,46 @@ __device__ inline bool not_finite(float x) { return !(fabsf(x) <= FLT_MAX); }
 // e with 2^(e - 1) <= x < 2^e, 0 for x = 0 and values that are not finite.
 __device__ inline int exponent_of(float x) { return x == 0.0f || not_finite(x) ? 0 : __builtin_amdgcn_frexp_expf(x); }
 
-__global__ void clear_largest(Work work) { *work.largest = 0; }
-
 // lse2 and delta; kD / 8 lanes a row. Bound by HBM (out and dout once).
 template <typename T, int kD>
 __global__ __launch_bounds__(kThreads)
 void row_statistics(AttentionArgs a, Work work)
 {
     constexpr int kLanes = kD / 8;
-    const int64_t at = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / kLanes;
     const int part = threadIdx.x % kLanes;
-    if (at >= a.q_tokens * a.q_heads) return;
-    const int64_t row = at / a.q_heads;
-    const int head = static_cast<int>(at - row * a.q_heads);
-    const vec8<T> g = load8(static_cast<const T *>(a.dout.data) + row * a.dout.token + head * a.dout.head + 8 * part);
-    const vec8<T> o = load8(static_cast<const T *>(a.out.data) + row * a.out.token + head * a.out.head + 8 * part);
-    float s = 0.0f;
+    float top = 0.0f;
+    for (int64_t at = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / kLanes; at < a.q_tokens * a.q_heads;
+         at += static_cast<int64_t>(gridDim.x) * (kThreads / kLanes)) {
+        const int64_t row = at / a.q_heads;
+        const int head = static_cast<int>(at - row * a.q_heads);
+        const vec8<T> g = load8(static_cast<const T *>(a.dout.data) + row * a.dout.token + head * a.dout.head + 8 * part);
+        const vec8<T> o = load8(static_cast<const T *>(a.out.data) + row * a.out.token + head * a.out.head + 8 * part);
+        float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s += to_float(g[i]) * to_float(o[i]);
+        for (int i = 0; i < 8; ++i) s += to_float(g[i]) * to_float(o[i]);
 #pragma unroll
-    for (int m = kLanes / 2; m > 0; m >>= 1) s += __shfl_xor(s, m);
-    if (part == 0) {
-        const int64_t to = head * a.q_tokens + row;
-        const float lse = a.lse[to];
-        work.delta[to] = s;
-        work.lse2[to] = lse == -INFINITY ? INFINITY : lse * kLog2e;
+        for (int m = kLanes / 2; m > 0; m >>= 1) s += __shfl_xor(s, m);
+        if (part == 0) {
+            const int64_t to = head * a.q_tokens + row;
+            const float lse = a.lse[to];
+            work.delta[to] = s;
+            work.lse2[to] = lse == -INFINITY ? INFINITY : lse * kLog2e;
+        }
+        if constexpr (kNarrow<T>) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, not_finite(to_float(g[i])) ? 0.0f : fabsf(to_float(g[i])));
+        }
     }
     if constexpr (kNarrow<T>) {
-        float top = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, not_finite(to_float(g[i])) ? 0.0f : fabsf(to_float(g[i])));
+        __shared__ float s_top[kWaves];
 #pragma unroll
         for (int m = 32; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
-        // a maximum does not depend on the order in which it is taken
-        if ((threadIdx.x & 63) == 0 && top > 0.0f) atomicMax(work.largest, __float_as_uint(top));
+        if ((threadIdx.x & 63) == 0) s_top[threadIdx.x >> 6] = top;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < kWaves; ++w) top = fmaxf(top, s_top[w]);
+            work.largest[blockIdx.x] = top;
+        }
     }
 }
 
@@ -194,6 +212,7 @@ void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
         lse2 -= shift;
         unit *= fast_exp2(-shift);
     }
+    const typename Rows::Loader load_k(a.k.token), load_v(a.v.token);
     const T *keys = static_cast<const T *>(a.k.data) + static_cast<int64_t>(k0) * a.k.token + kv * a.k.head;
     const T *values = static_cast<const T *>(a.v.data) + static_cast<int64_t>(k0) * a.v.token + kv * a.v.head;
 
@@ -202,8 +221,8 @@ void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
 #pragma unroll
         for (int n = 0; n < kD / 32; ++n) dq[n] = f32x16{};
         if (range.tiles > 0) {
-            Rows::load(s_mem, keys, a.k.token, range.start(0), nk);
-            Rows::load(s_mem + Rows::kBytes, values, a.v.token, range.start(0), nk);
+            load_k.load(s_mem, keys, range.start(0), nk);
+            load_v.load(s_mem + Rows::kBytes, values, range.start(0), nk);
         }
         for (int t = 0; t < range.tiles; ++t) {
             char *s_k = s_mem + (t & 1) * 2 * Rows::kBytes, *s_v = s_k + Rows::kBytes;
@@ -211,8 +230,8 @@ void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
             __syncthreads();     // tile t is there, tile t - 1 is no longer read
             if (t + 1 < range.tiles) {
                 char *s_next = s_mem + ((t + 1) & 1) * 2 * Rows::kBytes;
-                Rows::load(s_next, keys, a.k.token, range.start(t + 1), nk);
-                Rows::load(s_next + Rows::kBytes, values, a.v.token, range.start(t + 1), nk);
+                load_k.load(s_next, keys, range.start(t + 1), nk);
+                load_v.load(s_next + Rows::kBytes, values, range.start(t + 1), nk);
             }
             if (pass) {
                 if (threadIdx.x < kTileRows) s_bad[threadIdx.x] = 0;
@@ -235,11 +254,16 @@ void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
                     x[r] = fast_exp2(__builtin_fmaf(x[r], factor, -lse2));
                     y[r] = x[r] * (y[r] - delta);
                 }
-                if (pass || !(j0 + 31 <= w_first && (j0 > w_high || j0 + 31 < a.sinks))) {
+                if (pass) {
+                    asm volatile("");     // keeps this a branch
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (s_bad[32 * b + 8 * (r >> 2) + 4 * half + (r & 3)]) y[r] = __builtin_nanf("");
+                }
+                if (!(j0 + 31 <= w_first && (j0 > w_high || j0 + 31 < a.sinks))) {
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
-                        const int in = 8 * (r >> 2) + 4 * half + (r & 3), j = j0 + in;
-                        if (pass && s_bad[32 * b + in]) y[r] = __builtin_nanf("");
+                        const int j = j0 + 8 * (r >> 2) + 4 * half + (r & 3);
                         y[r] = j <= p && (j > p_low || j < a.sinks) ? y[r] : 0.0f;
                     }
                 }
@@ -328,7 +352,11 @@ void dkv_tiles(AttentionArgs a, Work work, float factor)
     // float16: dw and delta times `small`, weights times 2^kWeightShift
     float small = 1.0f, unit_k = 1.0f, unit_v = 1.0f;
     if constexpr (kNarrow<T>) {
-        const int e = exponent_of(__uint_as_float(*work.largest));
+        float top = 0.0f;
+        for (int n = lane; n < work.largest_parts; n += 64) top = fmaxf(top, work.largest[n]);
+#pragma unroll
+        for (int m = 32; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
+        const int e = exponent_of(top);
         small = fast_exp2(static_cast<float>(-e));
         unit_v = fast_exp2(-kWeightShift);
         unit_k = fast_exp2(static_cast<float>(e) - kWeightShift);
@@ -342,13 +370,14 @@ void dkv_tiles(AttentionArgs a, Work work, float factor)
             v[t] = load8(static_cast<const T *>(a.v.data) + row * a.v.token + kv * a.v.head + 16 * t + 8 * half);
         }
     }
+    const typename Rows::Loader load_q(a.q.token), load_g(a.dout.token);
     auto load = [&](int buffer, int head, int i) {
         char *s = s_mem + buffer * 2 * Rows::kBytes;
-        Rows::load(s, static_cast<const T *>(a.q.data) + static_cast<int64_t>(q0) * a.q.token + head * a.q.head, a.q.token, i, nq);
-        Rows::load(s + Rows::kBytes, static_cast<const T *>(a.dout.data) + static_cast<int64_t>(q0) * a.dout.token + head * a.dout.head,
-                   a.dout.token, i, nq);
+        load_q.load(s, static_cast<const T *>(a.q.data) + static_cast<int64_t>(q0) * a.q.token + head * a.q.head, i, nq);
+        load_g.load(s + Rows::kBytes, static_cast<const T *>(a.dout.data) + static_cast<int64_t>(q0) * a.dout.token + head * a.dout.head,
+                    i, nq);
         if (wave < 2)
-            copy4((wave ? work.delta : work.lse2) + head * a.q_tokens + q0 + min(i + lane, nq - 1), s_stats[buffer][wave]);
+            copy4((wave ? work.delta : work.lse2) + head * a.q_tokens + q0 + i, 4 * min(lane, nq - 1 - i), s_stats[buffer][wave]);
     };
 
     f32x16 dk[kD / 32], dv[kD / 32];
@@ -386,7 +415,7 @@ void dkv_tiles(AttentionArgs a, Work work, float factor)
                     x = mma32(Rows::along(s_q, 32 * b + c, 2 * n + half), k[n], x);
                     y = mma32(Rows::along(s_g, 32 * b + c, 2 * n + half), v[n], y);
                 }
-                const bool whole = p0 >= key_last && p0 + 31 < hi_all && !kFar && !pass;
+                const bool whole = p0 >= key_last && p0 + 31 < hi_all && !kFar;
 #pragma unroll
                 for (int f = 0; f < 4; ++f) {
                     const int in = 32 * b + 8 * f + 4 * half;
@@ -404,13 +433,18 @@ void dkv_tiles(AttentionArgs a, Work work, float factor)
                         }
                     }
                 }
+                if (pass) {
+                    asm volatile("");     // keeps this a branch
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (s_bad[32 * b + 8 * (r >> 2) + 4 * half + (r & 3)]) x[r] = y[r] = __builtin_nanf("");
+                }
                 if (!whole) {
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
-                        const int in = 8 * (r >> 2) + 4 * half + (r & 3), p = p0 + in;
+                        const int p = p0 + 8 * (r >> 2) + 4 * half + (r & 3);
                         bool sees = p >= key && p < hi;
                         if (kFar) sees = sees && p - back >= i_first && p - back < i_end;
-                        if (pass && s_bad[32 * b + in]) x[r] = y[r] = __builtin_nanf("");
                         x[r] = sees ? x[r] : 0.0f;
                         y[r] = sees ? y[r] : 0.0f;
                     }
@@ -501,12 +535,10 @@ hipError_t backward(const AttentionArgs &a, hipStream_t stream)
     const Work work = work_of(a);
     const float factor = fmaxf(a.scale * kLog2e, FLT_MIN);     // as in the forward pass
     const int64_t q_slots = a.q_tokens / kRows + a.n_clips + 1, k_slots = a.k_tokens / kRows + a.n_clips + 1;
-    const int64_t lanes = a.q_tokens * a.q_heads * (kD / 8);
-    if (q_slots * a.q_heads > INT_MAX || k_slots * a.kv_heads > INT_MAX || lanes / kThreads >= INT_MAX)
+    if (q_slots * a.q_heads > INT_MAX || k_slots * a.kv_heads > INT_MAX)
         return hipErrorInvalidConfiguration;
     if (a.q_tokens > 0) {
-        if (kNarrow<T>) clear_largest<<<1, 1, 0, stream>>>(work);
-        row_statistics<T, kD><<<static_cast<unsigned>((lanes + kThreads - 1) / kThreads), kThreads, 0, stream>>>(a, work);
+        row_statistics<T, kD><<<work.largest_parts, kThreads, 0, stream>>>(a, work);
         dq_tiles<T, kD><<<static_cast<unsigned>(q_slots * a.q_heads), kThreads, 0, stream>>>(a, work, factor, static_cast<int>(q_slots));
     }
     if (a.k_tokens > 0) {

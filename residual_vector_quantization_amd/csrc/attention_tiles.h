@@ -35,18 +35,20 @@ __device__ inline void store4(T *p, const T (&x)[4])
 
 typedef __attribute__((address_space(3))) void lds_void;
 
-// One wavefront-wide copy from global memory into the LDS: lane i's 16 (4) bytes at src go to dst + 16 i (4 i), dst
-// the same for all lanes. Issued as inline assembly so that the compiler does not order every LDS read behind it;
-// the caller waits with wait_copies and a barrier.
-__device__ inline void copy16(const void *src, void *dst)
+// One wavefront-wide copy from global memory into the LDS: lane i's 16 (4) bytes at src + offset (offset in the lane,
+// src the same for all) go to dst + 16 i (4 i), dst the same for all lanes. Issued as inline assembly so that the
+// compiler does not order every LDS read behind it; the caller waits with wait_copies and a barrier. The instruction
+// needs 1 wait state after a scalar write of m0 and 5 after a vector instruction's write of a scalar register that it
+// reads (src brought back from a spill), which the compiler does not see to inside inline assembly.
+__device__ inline void copy16(const void *src, uint32_t offset, void *dst)
 {
     const unsigned m0 = static_cast<unsigned>(reinterpret_cast<size_t>((lds_void *)dst));
-    asm volatile("global_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(m0) : "memory");
+    asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(src), "{m0}"(m0) : "memory");
 }
-__device__ inline void copy4(const void *src, void *dst)
+__device__ inline void copy4(const void *src, uint32_t offset, void *dst)
 {
     const unsigned m0 = static_cast<unsigned>(reinterpret_cast<size_t>((lds_void *)dst));
-    asm volatile("global_load_lds_dword %0, off" ::"v"(src), "{m0}"(m0) : "memory");
+    asm volatile("s_nop 4\n\tglobal_load_lds_dword %0, %1" ::"v"(offset), "s"(src), "{m0}"(m0) : "memory");
 }
 __device__ inline void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
@@ -90,17 +92,40 @@ struct Tile {
         return piece ^ (kRowPieces >= 16 ? (row & 3) << 2 | ((row >> 2) & 3) : ((row >> 1) & 1) << 2 | ((row >> 2) & 3));
     }
 
-    // Rows first .. first + 63 of `rows` into the tile, the last one (end - 1) again for rows past the end.
-    __device__ static void load(char *s, const T *rows, int64_t stride, int first, int end)
-    {
-        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // What a lane needs to bring tiles of rows `stride` values apart into the LDS: the offset of each of its pieces
+    // from the tile's first row. 64 rows span less than 2^31 bytes.
+    struct Loader {
+        uint32_t offset[kCopies];
+        uint32_t step;      // bytes from row to row
+
+        __device__ Loader(int64_t stride)
+        {
+            const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+            step = static_cast<uint32_t>(stride) * static_cast<uint32_t>(sizeof(T));
 #pragma unroll
-        for (int n = 0; n < kCopies; ++n) {
-            const int at = (n * kWaves + wave) * 64 + lane, row = at / kRowPieces;
-            const int piece = place(row, at % kRowPieces);
-            copy16(rows + min(first + row, end - 1) * stride + piece * kPiece, s + (n * kWaves + wave) * 1024);
+            for (int n = 0; n < kCopies; ++n) {
+                const int at = (n * kWaves + wave) * 64 + lane, row = at / kRowPieces;
+                offset[n] = row * step + place(row, at % kRowPieces) * 16;
+            }
         }
-    }
+        // Rows first .. first + 63 of `rows` into the tile s, the last one (end - 1) again for rows past the end.
+        __device__ void load(char *s, const T *rows, int first, int end) const
+        {
+            const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+            const char *from = reinterpret_cast<const char *>(rows) + static_cast<int64_t>(first) * step;
+            if (first + kTileRows <= end) {
+#pragma unroll
+                for (int n = 0; n < kCopies; ++n) copy16(from, offset[n], s + (n * kWaves + wave) * 1024);
+            } else {
+                const int last = end - 1 - first;
+#pragma unroll
+                for (int n = 0; n < kCopies; ++n) {
+                    const int row = ((n * kWaves + static_cast<int>(threadIdx.x >> 6)) * 64 + static_cast<int>(threadIdx.x & 63)) / kRowPieces;
+                    copy16(from, offset[n] - (row > last ? row - last : 0) * step, s + (n * kWaves + wave) * 1024);
+                }
+            }
+        }
+    };
 
     // Operand along the rows: values 8 k8 .. 8 k8 + 7 of a row.
     __device__ static vec8<T> along(const char *s, int row, int k8)

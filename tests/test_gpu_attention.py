@@ -110,6 +110,14 @@ def test_many_sink_rows_far_from_their_queries(typ):
     check(typ, 64, 4, 1, [1100, 700], window=100, sinks=4)
 
 
+@pytest.mark.parametrize("typ,dim,q_lens,k_lens,window,sinks", [
+    ("bf16", 64, [4500], None, 100, 4), ("fp32", 64, [4700, 90, 1500], None, 300, 64), ("fp16", 128, [4200], [4400], 129, 33),
+    ("fp32", 128, [4300], [4300], 0, 5)])
+def test_sinks_of_long_clips(typ, dim, q_lens, k_lens, window, sinks):
+    """Clips long enough for the sinks' gradients to be added up from pieces."""
+    check(typ, dim, 2, 1, q_lens, k_lens, window=window, sinks=sinks)
+
+
 def test_large_scores_and_other_scales():
     check("bf16", 64, 2, 1, [140], scale=3.0, train=False)
     check("fp32", 64, 2, 1, [140], scale=0.0)
