@@ -33,11 +33,7 @@ constexpr int kThreads = 64 * kWaves;
 constexpr int kRows = 32 * kWaves;     // queries a workgroup
 constexpr float kSlack = 8.0f;         // how far (powers of two) a score may exceed the running maximum
 
-// The passes of a workgroup over its keys. Weights of unseen keys are 0, but 0 times a value that is not finite is
-// not 0. So when a result is not finite, a second pass counts, for every result, the keys seen that have such a value
-// there, and a third computes the results with these values taken as 0: results with a count are NaN, the others are
-// what they would be without the values that are not seen.
-enum Pass { kPlain, kMarkers, kFinite };
+template <int kN> struct Constant { static constexpr int value = kN; };
 
 template <typename T, int kD>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
@@ -80,9 +76,76 @@ void forward_tiles(AttentionArgs a, float factor, int slots)
     const T *values = static_cast<const T *>(a.v.data) + static_cast<int64_t>(k0) * a.v.token + kv * a.v.head;
 
     f32x16 o[kD / 32];
-    uint32_t marked[kD / 64] = {};
-    float m = -INFINITY, l = 0.0f;
-    for (int pass = kPlain; pass <= kFinite; ++pass) {
+    float m, l;
+
+    // One tile of keys. The buffer's number is a constant, so that LDS addresses are; markers and clean (the values
+    // of a tile are to be rewritten) make the later passes.
+    auto tile = [&](int t, auto buffer, auto markers, bool clean) {
+        char *s_k = s_mem + buffer.value * 2 * Rows::kBytes, *s_v = s_k + Rows::kBytes;
+        wait_copies();
+        __syncthreads();     // tile t is there, tile t - 1 is no longer read
+        if (t + 1 < range.tiles) {
+            char *s_next = s_mem + (1 - buffer.value) * 2 * Rows::kBytes;
+            load_k.load(s_next, keys, range.start(t + 1), nk);
+            load_v.load(s_next + Rows::kBytes, values, range.start(t + 1), nk);
+        }
+        if (clean) {
+            Rows::only_finite(s_v, markers.value);
+            __syncthreads();
+        }
+        const int j0 = range.start(t);
+        // nothing of these keys is seen by this wavefront
+        if (j0 > w_last || (j0 + kTileRows - 1 <= w_low && j0 >= a.sinks)) return;
+        f32x16 x[2] = {};
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int n = 0; n < kD / 16; ++n) x[b] = mma32(Rows::along(s_k, 32 * b + c, 2 * n + half), q[n], x[b]);
+        if (!(j0 + kTileRows - 1 <= w_first && (j0 > w_high || j0 + kTileRows - 1 < a.sinks))) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int j = j0 + 32 * b + 8 * (r >> 2) + 4 * half + (r & 3);
+                    x[b][r] = j <= p && (j > p_low || j < a.sinks) ? x[b][r] : -INFINITY;
+                }
+        }
+        float top = x[0][0];
+#pragma unroll
+        for (int r = 1; r < 32; ++r) top = fmaxf(top, x[r >> 4][r & 15]);
+        top *= factor;
+        if (__any(top > m + kSlack)) {
+            top = fmaxf(top, __shfl_xor(top, 32));
+            if (top > m + kSlack) {
+                const float keep = fast_exp2(m - top);
+                m = top;
+                l *= keep;
+                if (!markers.value) {
+#pragma unroll
+                    for (int n = 0; n < kD / 32; ++n) o[n] *= keep;
+                }
+            }
+        }
+        const float safe = m == -INFINITY ? 0.0f : m;
+        float sum[4] = {};
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            vec8<T> w[2];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                float e = fast_exp2(__builtin_fmaf(x[b][r], factor, -safe));
+                sum[r & 3] += e;
+                if (markers.value) e = x[b][r] == -INFINITY ? 0.0f : 1.0f;
+                w[r >> 3][r & 7] = static_cast<T>(e);
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int n = 0; n < kD / 32; ++n) o[n] = mma32(Rows::across(s_v, n, 2 * b + s), w[s], o[n]);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    };
+    auto pass = [&](auto markers, bool clean) {
 #pragma unroll
         for (int n = 0; n < kD / 32; ++n) o[n] = f32x16{};
         m = -INFINITY;
@@ -91,89 +154,36 @@ void forward_tiles(AttentionArgs a, float factor, int slots)
             load_k.load(s_mem, keys, range.start(0), nk);
             load_v.load(s_mem + Rows::kBytes, values, range.start(0), nk);
         }
-        for (int t = 0; t < range.tiles; ++t) {
-            char *s_k = s_mem + (t & 1) * 2 * Rows::kBytes, *s_v = s_k + Rows::kBytes;
-            wait_copies();
-            __syncthreads();     // tile t is there, tile t - 1 is no longer read
-            if (t + 1 < range.tiles) {
-                char *s_next = s_mem + ((t + 1) & 1) * 2 * Rows::kBytes;
-                load_k.load(s_next, keys, range.start(t + 1), nk);
-                load_v.load(s_next + Rows::kBytes, values, range.start(t + 1), nk);
-            }
-            if (pass != kPlain) {
-                Rows::only_finite(s_v, pass == kMarkers);
-                __syncthreads();
-            }
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int j0 = range.start(t) + 32 * b;
-                // nothing of these keys is seen by this wavefront
-                if (j0 > w_last || (j0 + 31 <= w_low && j0 >= a.sinks)) continue;
-                f32x16 x = {};
-#pragma unroll
-                for (int n = 0; n < kD / 16; ++n) x = mma32(Rows::along(s_k, 32 * b + c, 2 * n + half), q[n], x);
-                if (!(j0 + 31 <= w_first && (j0 > w_high || j0 + 31 < a.sinks))) {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const int j = j0 + 8 * (r >> 2) + 4 * half + (r & 3);
-                        x[r] = j <= p && (j > p_low || j < a.sinks) ? x[r] : -INFINITY;
-                    }
-                }
-                float top = x[0];
-#pragma unroll
-                for (int r = 1; r < 16; ++r) top = fmaxf(top, x[r]);
-                top *= factor;
-                if (__any(top > m + kSlack)) {
-                    top = fmaxf(top, __shfl_xor(top, 32));
-                    if (top > m + kSlack) {
-                        const float keep = fast_exp2(m - top);
-                        m = top;
-                        l *= keep;
-                        if (pass != kMarkers) {
-#pragma unroll
-                            for (int n = 0; n < kD / 32; ++n) o[n] *= keep;
-                        }
-                    }
-                }
-                const float safe = m == -INFINITY ? 0.0f : m;
-                vec8<T> w[2];
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const float e = fast_exp2(__builtin_fmaf(x[r], factor, -safe));
-                    l += e;
-                    w[r >> 3][r & 7] = static_cast<T>(e);
-                }
-                if (pass == kMarkers) {
-                    asm volatile("");     // keeps this a branch, not 16 selects on the usual way
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) w[r >> 3][r & 7] = static_cast<T>(x[r] == -INFINITY ? 0.0f : 1.0f);
-                }
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-#pragma unroll
-                    for (int n = 0; n < kD / 32; ++n) o[n] = mma32(Rows::across(s_v, n, 2 * b + s), w[s], o[n]);
-            }
+        for (int t = 0; t < range.tiles; t += 2) {
+            tile(t, Constant<0>{}, markers, clean);
+            if (t + 1 < range.tiles) tile(t + 1, Constant<1>{}, markers, clean);
         }
+    };
+
+    pass(Constant<0>{}, false);
+    bool odd = false;
+#pragma unroll
+    for (int n = 0; n < kD / 32; ++n)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) odd = odd || !(fabsf(o[n][r]) <= FLT_MAX);
+    // Weights of unseen keys are 0, but 0 times a value that is not finite is not 0. So when a result is not finite, a
+    // second pass counts, for every result, the keys seen that have such a value there, and a third computes the
+    // results with these values taken as 0: results with a count are NaN, the others are what they would be without
+    // the values that are not seen.
+    if (__syncthreads_or(odd)) {
+        pass(Constant<1>{}, true);
+        uint32_t marked[kD / 64] = {};
+#pragma unroll
+        for (int n = 0; n < kD / 32; ++n)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) marked[n >> 1] |= static_cast<uint32_t>(o[n][r] > 0.0f) << (16 * (n & 1) + r);
         __syncthreads();     // the tiles are no longer read
-        if (pass == kPlain) {
-            bool odd = false;
+        pass(Constant<0>{}, true);
 #pragma unroll
-            for (int n = 0; n < kD / 32; ++n)
+        for (int n = 0; n < kD / 32; ++n)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) odd = odd || !(fabsf(o[n][r]) <= FLT_MAX);
-            if (!__syncthreads_or(odd)) break;
-        } else if (pass == kMarkers) {
-#pragma unroll
-            for (int n = 0; n < kD / 32; ++n)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) marked[n >> 1] |= static_cast<uint32_t>(o[n][r] > 0.0f) << (16 * (n & 1) + r);
-        } else {
-#pragma unroll
-            for (int n = 0; n < kD / 32; ++n)
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (marked[n >> 1] >> (16 * (n & 1) + r) & 1) o[n][r] = __builtin_nanf("");
-        }
+            for (int r = 0; r < 16; ++r)
+                if (marked[n >> 1] >> (16 * (n & 1) + r) & 1) o[n][r] = __builtin_nanf("");
     }
     if (!real) return;
     l += __shfl_xor(l, 32);
