@@ -33,15 +33,13 @@ constexpr int kThreads = 64 * kWaves;
 constexpr int kRows = 32 * kWaves;     // queries a workgroup
 constexpr float kSlack = 8.0f;         // how far (powers of two) a score may exceed the running maximum
 
-template <int kN> struct Constant { static constexpr int value = kN; };
-
 template <typename T, int kD>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
 void forward_tiles(AttentionArgs a, float factor, int slots)
 {
     typedef Tile<T, kD, kWaves> Rows;
     __shared__ __attribute__((aligned(16))) char s_mem[4 * Rows::kBytes];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 31, half = lane >> 5;
     // heads change fastest: with 8 of them or more, one chiplet sees the same heads' keys again and again; the
     // last queries of a clip, which see most, start first

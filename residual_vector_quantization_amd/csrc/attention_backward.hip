@@ -174,7 +174,7 @@ void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
     typedef Tile<T, kD, kWaves> Rows;
     __shared__ __attribute__((aligned(16))) char s_mem[4 * Rows::kBytes];
     __shared__ int s_bad[kTileRows];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 31, half = lane >> 5;
     const int slot = slots - 1 - static_cast<int>(blockIdx.x / a.q_heads), head = blockIdx.x % a.q_heads;
     const int kv = head / (a.q_heads / a.kv_heads);
@@ -217,72 +217,73 @@ void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
     const T *values = static_cast<const T *>(a.v.data) + static_cast<int64_t>(k0) * a.v.token + kv * a.v.head;
 
     f32x16 dq[kD / 32];
-    for (int pass = 0; pass < 2; ++pass) {
+    // One tile of keys; buffer and pass are constants.
+    auto tile = [&](int t, auto buffer, auto second) {
+        char *s_k = s_mem + buffer.value * 2 * Rows::kBytes, *s_v = s_k + Rows::kBytes;
+        wait_copies();
+        __syncthreads();     // tile t is there, tile t - 1 is no longer read
+        if (t + 1 < range.tiles) {
+            char *s_next = s_mem + (1 - buffer.value) * 2 * Rows::kBytes;
+            load_k.load(s_next, keys, range.start(t + 1), nk);
+            load_v.load(s_next + Rows::kBytes, values, range.start(t + 1), nk);
+        }
+        if (second.value) {
+            if (threadIdx.x < kTileRows) s_bad[threadIdx.x] = 0;
+            __syncthreads();
+            clear_bad_rows<T, kD>(s_k, s_bad);
+            __syncthreads();
+        }
+        const int j0 = range.start(t);
+        if (j0 > w_last || (j0 + kTileRows - 1 <= w_low && j0 >= a.sinks)) return;
+        const bool whole = j0 + kTileRows - 1 <= w_first && (j0 > w_high || j0 + kTileRows - 1 < a.sinks);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            f32x16 x = {}, y = {};
+#pragma unroll
+            for (int n = 0; n < kD / 16; ++n) {
+                x = mma32(Rows::along(s_k, 32 * b + c, 2 * n + half), q[n], x);
+                y = mma32(Rows::along(s_v, 32 * b + c, 2 * n + half), g[n], y);
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                y[r] = fast_exp2(__builtin_fmaf(x[r], factor, -lse2)) * (y[r] - delta);
+                if (second.value && s_bad[32 * b + 8 * (r >> 2) + 4 * half + (r & 3)]) y[r] = __builtin_nanf("");
+            }
+            if (!whole) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int j = j0 + 32 * b + 8 * (r >> 2) + 4 * half + (r & 3);
+                    y[r] = j <= p && (j > p_low || j < a.sinks) ? y[r] : 0.0f;
+                }
+            }
+            vec8<T> w[2];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) w[r >> 3][r & 7] = static_cast<T>(y[r]);
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int n = 0; n < kD / 32; ++n) dq[n] = mma32(Rows::across(s_k, n, 2 * b + s), w[s], dq[n]);
+        }
+    };
+    auto pass = [&](auto second) {
 #pragma unroll
         for (int n = 0; n < kD / 32; ++n) dq[n] = f32x16{};
         if (range.tiles > 0) {
             load_k.load(s_mem, keys, range.start(0), nk);
             load_v.load(s_mem + Rows::kBytes, values, range.start(0), nk);
         }
-        for (int t = 0; t < range.tiles; ++t) {
-            char *s_k = s_mem + (t & 1) * 2 * Rows::kBytes, *s_v = s_k + Rows::kBytes;
-            wait_copies();
-            __syncthreads();     // tile t is there, tile t - 1 is no longer read
-            if (t + 1 < range.tiles) {
-                char *s_next = s_mem + ((t + 1) & 1) * 2 * Rows::kBytes;
-                load_k.load(s_next, keys, range.start(t + 1), nk);
-                load_v.load(s_next + Rows::kBytes, values, range.start(t + 1), nk);
-            }
-            if (pass) {
-                if (threadIdx.x < kTileRows) s_bad[threadIdx.x] = 0;
-                __syncthreads();
-                clear_bad_rows<T, kD>(s_k, s_bad);
-                __syncthreads();
-            }
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int j0 = range.start(t) + 32 * b;
-                if (j0 > w_last || (j0 + 31 <= w_low && j0 >= a.sinks)) continue;
-                f32x16 x = {}, y = {};
-#pragma unroll
-                for (int n = 0; n < kD / 16; ++n) {
-                    x = mma32(Rows::along(s_k, 32 * b + c, 2 * n + half), q[n], x);
-                    y = mma32(Rows::along(s_v, 32 * b + c, 2 * n + half), g[n], y);
-                }
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    x[r] = fast_exp2(__builtin_fmaf(x[r], factor, -lse2));
-                    y[r] = x[r] * (y[r] - delta);
-                }
-                if (pass) {
-                    asm volatile("");     // keeps this a branch
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (s_bad[32 * b + 8 * (r >> 2) + 4 * half + (r & 3)]) y[r] = __builtin_nanf("");
-                }
-                if (!(j0 + 31 <= w_first && (j0 > w_high || j0 + 31 < a.sinks))) {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const int j = j0 + 8 * (r >> 2) + 4 * half + (r & 3);
-                        y[r] = j <= p && (j > p_low || j < a.sinks) ? y[r] : 0.0f;
-                    }
-                }
-                vec8<T> w[2];
-#pragma unroll
-                for (int r = 0; r < 16; ++r) w[r >> 3][r & 7] = static_cast<T>(y[r]);
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-#pragma unroll
-                    for (int n = 0; n < kD / 32; ++n) dq[n] = mma32(Rows::across(s_k, n, 2 * b + s), w[s], dq[n]);
-            }
+        for (int t = 0; t < range.tiles; t += 2) {
+            tile(t, Constant<0>{}, second);
+            if (t + 1 < range.tiles) tile(t + 1, Constant<1>{}, second);
         }
-        bool odd = false;
+    };
+    pass(Constant<0>{});
+    bool odd = false;
 #pragma unroll
-        for (int n = 0; n < kD / 32; ++n)
+    for (int n = 0; n < kD / 32; ++n)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) odd = odd || not_finite(dq[n][r]);
-        if (!__syncthreads_or(odd)) break;     // and the tiles are no longer read
-    }
+        for (int r = 0; r < 16; ++r) odd = odd || not_finite(dq[n][r]);
+    if (__syncthreads_or(odd)) pass(Constant<1>{});
     if (row >= nq) return;
     T *out = static_cast<T *>(a.dq.data) + at * a.dq.token + head * a.dq.head;
 #pragma unroll
@@ -348,6 +349,8 @@ void dkv_tiles(AttentionArgs a, Work work, float factor)
         hi_all = min(hi_all, __shfl_xor(hi_all, m));
         hi_any = max(hi_any, __shfl_xor(hi_any, m));
     }
+    hi_all = __builtin_amdgcn_readfirstlane(hi_all);     // the same in both halves of the wavefront
+    hi_any = __builtin_amdgcn_readfirstlane(hi_any);
 
     // float16: dw and delta times `small`, weights times 2^kWeightShift
     float small = 1.0f, unit_k = 1.0f, unit_v = 1.0f;
@@ -381,96 +384,101 @@ void dkv_tiles(AttentionArgs a, Work work, float factor)
     };
 
     f32x16 dk[kD / 32], dv[kD / 32];
-    for (int pass = 0; pass < 2; ++pass) {
+    int head, i;     // of the next tile to load
+    // One tile of queries; buffer and pass are constants.
+    auto tile = [&](int t, int i_tile, auto buffer, auto second) {
+        char *s_q = s_mem + buffer.value * 2 * Rows::kBytes, *s_g = s_q + Rows::kBytes;
+        wait_copies();
+        __syncthreads();     // tile t is there, tile t - 1 is no longer read
+        if (t + 1 < tiles) load(1 - buffer.value, head, i);
+        if (second.value) {
+            if (threadIdx.x < kTileRows) s_bad[threadIdx.x] = 0;
+            __syncthreads();
+            clear_bad_rows<T, kD>(s_q, s_bad);
+            clear_bad_rows<T, kD>(s_g, s_bad);
+            __syncthreads();
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const int p0 = i_tile + 32 * b + back;       // position of the first of these 32 queries
+            if (p0 + 31 < key_first || p0 >= hi_any) continue;
+            if (kFar && (b != (wave & 1) || p0 + 31 < i_first + back)) continue;
+            f32x16 x = {}, y = {};
+#pragma unroll
+            for (int n = 0; n < kD / 16; ++n) {
+                x = mma32(Rows::along(s_q, 32 * b + c, 2 * n + half), k[n], x);
+                y = mma32(Rows::along(s_g, 32 * b + c, 2 * n + half), v[n], y);
+            }
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                const int in = 32 * b + 8 * f + 4 * half;
+                const f32x4 lse2 = *reinterpret_cast<const f32x4 *>(&s_stats[buffer.value][0][in]);
+                const f32x4 delta = *reinterpret_cast<const f32x4 *>(&s_stats[buffer.value][1][in]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = 4 * f + e;
+                    if constexpr (kNarrow<T>) {
+                        x[r] = fast_exp2(__builtin_fmaf(x[r], factor, kWeightShift - lse2[e]));
+                        y[r] = x[r] * __builtin_fmaf(y[r], small, -small * delta[e]);
+                    } else {
+                        x[r] = fast_exp2(__builtin_fmaf(x[r], factor, -lse2[e]));
+                        y[r] = x[r] * (y[r] - delta[e]);
+                    }
+                    if (second.value && s_bad[in + e]) x[r] = y[r] = __builtin_nanf("");
+                }
+            }
+            if (kFar || !(p0 >= key_last && p0 + 31 < hi_all)) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int p = p0 + 8 * (r >> 2) + 4 * half + (r & 3);
+                    bool sees = p >= key && p < hi;
+                    if (kFar) sees = sees && p - back >= i_first && p - back < i_end;
+                    x[r] = sees ? x[r] : 0.0f;
+                    y[r] = sees ? y[r] : 0.0f;
+                }
+            }
+            vec8<T> w[2], d[2];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                w[r >> 3][r & 7] = static_cast<T>(x[r]);
+                d[r >> 3][r & 7] = static_cast<T>(y[r]);
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int n = 0; n < kD / 32; ++n) {
+                    dv[n] = mma32(Rows::across(s_g, n, 2 * b + s), w[s], dv[n]);
+                    dk[n] = mma32(Rows::across(s_q, n, 2 * b + s), d[s], dk[n]);
+                }
+        }
+    };
+    auto pass = [&](auto second) {
 #pragma unroll
         for (int n = 0; n < kD / 32; ++n) dk[n] = dv[n] = f32x16{};
-        int head = kv * group, i = i_start;
+        head = kv * group;
+        i = i_start;
         if (tiles > 0) load(0, head, i);
-        for (int t = 0; t < tiles; ++t) {
-            char *s_q = s_mem + (t & 1) * 2 * Rows::kBytes, *s_g = s_q + Rows::kBytes;
-            const int i_tile = i;
-            wait_copies();
-            __syncthreads();     // tile t is there, tile t - 1 is no longer read
+        auto step = [&](int t, auto buffer) {
+            const int now = i;
             i += kTileRows;
             if (i >= i_end) {
                 i = i_start;
                 ++head;
             }
-            if (t + 1 < tiles) load((t + 1) & 1, head, i);
-            if (pass) {
-                if (threadIdx.x < kTileRows) s_bad[threadIdx.x] = 0;
-                __syncthreads();
-                clear_bad_rows<T, kD>(s_q, s_bad);
-                clear_bad_rows<T, kD>(s_g, s_bad);
-                __syncthreads();
-            }
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int p0 = i_tile + 32 * b + back;       // position of the first of these 32 queries
-                if (p0 + 31 < key_first || p0 >= hi_any) continue;
-                if (kFar && (b != (wave & 1) || p0 + 31 < i_first + back)) continue;
-                f32x16 x = {}, y = {};
-#pragma unroll
-                for (int n = 0; n < kD / 16; ++n) {
-                    x = mma32(Rows::along(s_q, 32 * b + c, 2 * n + half), k[n], x);
-                    y = mma32(Rows::along(s_g, 32 * b + c, 2 * n + half), v[n], y);
-                }
-                const bool whole = p0 >= key_last && p0 + 31 < hi_all && !kFar;
-#pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                    const int in = 32 * b + 8 * f + 4 * half;
-                    const f32x4 lse2 = *reinterpret_cast<const f32x4 *>(&s_stats[t & 1][0][in]);
-                    const f32x4 delta = *reinterpret_cast<const f32x4 *>(&s_stats[t & 1][1][in]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int r = 4 * f + e;
-                        if constexpr (kNarrow<T>) {
-                            x[r] = fast_exp2(__builtin_fmaf(x[r], factor, kWeightShift - lse2[e]));
-                            y[r] = x[r] * __builtin_fmaf(y[r], small, -small * delta[e]);
-                        } else {
-                            x[r] = fast_exp2(__builtin_fmaf(x[r], factor, -lse2[e]));
-                            y[r] = x[r] * (y[r] - delta[e]);
-                        }
-                    }
-                }
-                if (pass) {
-                    asm volatile("");     // keeps this a branch
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (s_bad[32 * b + 8 * (r >> 2) + 4 * half + (r & 3)]) x[r] = y[r] = __builtin_nanf("");
-                }
-                if (!whole) {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const int p = p0 + 8 * (r >> 2) + 4 * half + (r & 3);
-                        bool sees = p >= key && p < hi;
-                        if (kFar) sees = sees && p - back >= i_first && p - back < i_end;
-                        x[r] = sees ? x[r] : 0.0f;
-                        y[r] = sees ? y[r] : 0.0f;
-                    }
-                }
-                vec8<T> w[2], d[2];
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    w[r >> 3][r & 7] = static_cast<T>(x[r]);
-                    d[r >> 3][r & 7] = static_cast<T>(y[r]);
-                }
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-#pragma unroll
-                    for (int n = 0; n < kD / 32; ++n) {
-                        dv[n] = mma32(Rows::across(s_g, n, 2 * b + s), w[s], dv[n]);
-                        dk[n] = mma32(Rows::across(s_q, n, 2 * b + s), d[s], dk[n]);
-                    }
-            }
+            tile(t, now, buffer, second);
+        };
+        for (int t = 0; t < tiles; t += 2) {
+            step(t, Constant<0>{});
+            if (t + 1 < tiles) step(t + 1, Constant<1>{});
         }
-        bool odd = false;
+    };
+    pass(Constant<0>{});
+    bool odd = false;
 #pragma unroll
-        for (int n = 0; n < kD / 32; ++n)
+    for (int n = 0; n < kD / 32; ++n)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) odd = odd || not_finite(dk[n][r]) || not_finite(dv[n][r]);
-        if (!__syncthreads_or(odd)) break;     // and the tiles are no longer read
-    }
+        for (int r = 0; r < 16; ++r) odd = odd || not_finite(dk[n][r]) || not_finite(dv[n][r]);
+    if (__syncthreads_or(odd)) pass(Constant<1>{});
     if (key >= nk) return;
     if (kFar || (work.split && key < a.sinks)) {
         if (key >= a.sinks) return;

@@ -17,6 +17,9 @@ typedef _Float16 f16_t;
 template <typename T>
 __device__ inline float to_float(T x) { return static_cast<float>(x); }
 
+// A number known to the compiler, as an argument.
+template <int kN> struct Constant { static constexpr int value = kN; };
+
 // One clip of a packed batch: its queries and keys, ends clamped into the arrays.
 struct Clip {
     int q0, nq;      // first query row, number of queries
