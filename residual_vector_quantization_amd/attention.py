@@ -25,11 +25,12 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from typing import Optional
 
 import torch
 
-from . import RVQError, _check, _ptr, _require, _stream, load, rvq_status_string
+from . import RVQError, _check, _ptr, _require, load, rvq_status_string
 
 EXPORTED_ATTENTION = ("rvq_window_attention", "rvq_window_attention_backward", "rvq_window_attention_backward_bytes",
                       "rvq_cache_append", "rvq_cache_attention", "rvq_cache_attention_bytes",
@@ -56,6 +57,11 @@ class _CacheShape(ctypes.Structure):
                 ("table_ld", ctypes.c_int32)]
 
 
+# The same structures packed by hand: a tenth of the time of a ctypes.Structure, which counts where a call takes 10 us.
+_pack_heads = struct.Struct("=Qqq").pack
+_pack_attention = struct.Struct("=6i3qQQf4x").pack
+_pack_cache = struct.Struct("=7i").pack
+
 _ready = None
 
 
@@ -65,7 +71,7 @@ def _lib() -> ctypes.CDLL:
         return _ready
     lib = load()
     vp, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
-    heads, shape, cache = (ctypes.POINTER(t) for t in (_Heads, _AttentionShape, _CacheShape))
+    heads = shape = cache = vp      # packed bytes or a pointer to the structure
     for name, restype, argtypes in (
             ("rvq_window_attention", ctypes.c_int, [shape, heads, heads, heads, heads, vp, vp]),
             ("rvq_window_attention_backward_bytes", i64, [shape]),
@@ -88,9 +94,14 @@ def _lib() -> ctypes.CDLL:
     return lib
 
 
+def _stream(t: torch.Tensor) -> int:
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
 def _require_heads(t: torch.Tensor, name: str, dtype: torch.dtype, device, heads: Optional[int] = None,
-                   dim: Optional[int] = None, tokens: Optional[int] = None) -> None:
-    """A [tokens, heads, dim] tensor with contiguous rows; the C call checks strides and alignment."""
+                   dim: Optional[int] = None, tokens: Optional[int] = None) -> bytes:
+    """A [tokens, heads, dim] tensor with contiguous rows, as the C structure; the C call checks strides and
+    alignment."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -101,16 +112,14 @@ def _require_heads(t: torch.Tensor, name: str, dtype: torch.dtype, device, heads
         raise ValueError(f"{name} must be a GPU tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.stride(2) != 1:
+    (n, h, d), (n_stride, h_stride, d_stride) = t.shape, t.stride()
+    if d_stride != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    for what, have, want in (("tokens", t.shape[0], tokens), ("heads", t.shape[1], heads), ("dim", t.shape[2], dim)):
-        if want is not None and have != want:
-            raise ValueError(f"{name} {tuple(t.shape)} must have {want} {what}")
-
-
-def _heads(t: torch.Tensor):
+    if (heads is not None and h != heads) or (dim is not None and d != dim) or (tokens is not None and n != tokens):
+        want = ", ".join("*" if x is None else str(x) for x in (tokens, heads, dim))
+        raise ValueError(f"{name} must be [{want}], got {tuple(t.shape)}")
     # the stride of a dimension of one entry says nothing
-    return ctypes.byref(_Heads(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0))
+    return _pack_heads(t.data_ptr(), n_stride if n > 1 else 0, h_stride if h > 1 else 0)
 
 
 def _float_type(t: torch.Tensor, name: str) -> torch.dtype:
@@ -121,10 +130,12 @@ def _float_type(t: torch.Tensor, name: str) -> torch.dtype:
     return t.dtype
 
 
-def _offsets(cu: torch.Tensor, name: str, device, n_clips: Optional[int] = None) -> None:
+def _offsets(cu: torch.Tensor, name: str, device, n_clips: Optional[int] = None) -> int:
     _require(cu, name, torch.int32, 1, device)
-    if cu.shape[0] < 1 or (n_clips is not None and cu.shape[0] != n_clips + 1):
-        raise ValueError(f"{name} must have one entry more than there are clips, got {cu.shape[0]}")
+    n = cu.shape[0] - 1
+    if n < 0 or (n_clips is not None and n != n_clips):
+        raise ValueError(f"{name} must have one entry more than there are clips, got {n + 1}")
+    return n
 
 
 def _window(window: Optional[int]) -> int:
@@ -135,26 +146,28 @@ def _window(window: Optional[int]) -> int:
     return int(window)
 
 
-def _attention_shape(q, k, v, cu_q, cu_k, window, sinks, scale):
-    dtype = _float_type(q, "q")
-    dev = q.device
-    _require_heads(q, "q", dtype, dev)
-    dim = q.shape[2]
-    _require_heads(k, "k", dtype, dev, dim=dim)
-    _require_heads(v, "v", dtype, dev, heads=k.shape[1], dim=dim, tokens=k.shape[0])
-    if k.shape[1] == 0 or q.shape[1] % k.shape[1] != 0:
-        raise ValueError(f"q's heads ({q.shape[1]}) must be a multiple of k's ({k.shape[1]})")
-    _offsets(cu_q, "cu_q", dev)
+def _attention_args(q, k, v, cu_q, cu_k, window, sinks, scale):
+    """The checked call: (shape, q, k, v) as C structures, and q's sizes."""
+    dtype, dev = _float_type(q, "q"), q.device
+    q_heads = _require_heads(q, "q", dtype, dev)
+    tq, hq, dim = q.shape
+    k_heads = _require_heads(k, "k", dtype, dev, dim=dim)
+    tk, hk, _ = k.shape
+    v_heads = _require_heads(v, "v", dtype, dev, hk, dim, tk)
+    if hk == 0 or hq % hk != 0:
+        raise ValueError(f"q's heads ({hq}) must be a multiple of k's ({hk})")
+    n = _offsets(cu_q, "cu_q", dev)
     if cu_k is None:
-        if k.shape[0] != q.shape[0]:
+        if tk != tq:
             raise ValueError("cu_k is needed where k has other tokens than q")
         cu_k = cu_q
-    _offsets(cu_k, "cu_k", dev, cu_q.shape[0] - 1)
+    elif cu_k is not cu_q:
+        _offsets(cu_k, "cu_k", dev, n)
     if sinks < 0:
         raise ValueError(f"sinks={sinks} must not be negative")
-    return _AttentionShape(DTYPES[dtype], cu_q.shape[0] - 1, q.shape[1], k.shape[1], dim, sinks, _window(window),
-                           q.shape[0], k.shape[0], cu_q.data_ptr(), cu_k.data_ptr(),
-                           1.0 / math.sqrt(dim) if scale is None else scale)
+    shape = _pack_attention(DTYPES[dtype], n, hq, hk, dim, sinks, _window(window), tq, tk, cu_q.data_ptr(),
+                            cu_k.data_ptr(), 1.0 / math.sqrt(dim) if scale is None else scale)
+    return shape, q_heads, k_heads, v_heads, (tq, hq, dim)
 
 
 def rvq_window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
@@ -166,46 +179,58 @@ def rvq_window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q
     (``cu_k`` None: the same). A clip's queries stand at the last positions of its keys. Returns
     ``(out [Tq, Hq, D], lse [Hq, Tq] float32)``; ``out`` may be preallocated. Rows outside every clip are not written.
     """
-    shape = _attention_shape(q, k, v, cu_q, cu_k, window, sinks, scale)
+    shape, q_heads, k_heads, v_heads, size = _attention_args(q, k, v, cu_q, cu_k, window, sinks, scale)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    _require_heads(out, "out", q.dtype, q.device, q.shape[1], q.shape[2], q.shape[0])
-    lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
-    st = _lib().rvq_window_attention(ctypes.byref(shape), _heads(q), _heads(k), _heads(v), _heads(out), _ptr(lse),
-                                     _stream(q))
+        out = q.new_empty(size)
+    out_heads = _require_heads(out, "out", q.dtype, q.device, size[1], size[2], size[0])
+    lse = q.new_empty((size[1], size[0]), dtype=torch.float32)
+    st = _lib().rvq_window_attention(shape, q_heads, k_heads, v_heads, out_heads, lse.data_ptr(), _stream(q))
     _check("rvq_window_attention", st)
     return out, lse
 
 
-def rvq_window_attention_backward_bytes(shape: _AttentionShape) -> int:
-    """Workspace of the backward pass for a call's shape."""
-    size = _lib().rvq_window_attention_backward_bytes(ctypes.byref(shape))
+def _backward_bytes(shape: bytes) -> int:
+    size = _lib().rvq_window_attention_backward_bytes(shape)
     if size < 0:
         raise RVQError("rvq_window_attention_backward_bytes", size, rvq_status_string(size))
     return size
 
 
+def rvq_window_attention_backward_bytes(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
+                                        cu_k: Optional[torch.Tensor] = None, window: Optional[int] = None,
+                                        sinks: int = 0) -> int:
+    """Workspace of ``rvq_window_attention_backward`` for these arguments."""
+    return _backward_bytes(_attention_args(q, k, v, cu_q, cu_k, window, sinks, None)[0])
+
+
 def rvq_window_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                                   out: torch.Tensor, lse: torch.Tensor, cu_q: torch.Tensor,
                                   cu_k: Optional[torch.Tensor] = None, window: Optional[int] = None, sinks: int = 0,
-                                  scale: Optional[float] = None, grads=None):
+                                  scale: Optional[float] = None, grads=None,
+                                  workspace: Optional[torch.Tensor] = None):
     """Gradients ``(dq, dk, dv)`` of ``rvq_window_attention``; ``out`` and ``lse`` are its results, the other
-    arguments as it had them. ``grads`` may pass the three outputs preallocated (for example slices of one tensor)."""
-    shape = _attention_shape(q, k, v, cu_q, cu_k, window, sinks, scale)
-    for t, name in ((dout, "dout"), (out, "out")):
-        _require_heads(t, name, q.dtype, q.device, q.shape[1], q.shape[2], q.shape[0])
-    _require(lse, "lse", torch.float32, 2, q.device)
-    if tuple(lse.shape) != (q.shape[1], q.shape[0]):
-        raise ValueError(f"lse must be [{q.shape[1]}, {q.shape[0]}], got {tuple(lse.shape)}")
+    arguments as it had them. ``grads`` may pass the three outputs preallocated (for example slices of one tensor),
+    ``workspace`` a uint8 tensor of ``rvq_window_attention_backward_bytes``."""
+    shape, q_heads, k_heads, v_heads, (tq, hq, dim) = _attention_args(q, k, v, cu_q, cu_k, window, sinks, scale)
+    dtype, dev = q.dtype, q.device
+    dout_heads = _require_heads(dout, "dout", dtype, dev, hq, dim, tq)
+    out_heads = _require_heads(out, "out", dtype, dev, hq, dim, tq)
+    _require(lse, "lse", torch.float32, 2, dev)
+    if lse.shape != (hq, tq):
+        raise ValueError(f"lse must be [{hq}, {tq}], got {tuple(lse.shape)}")
     if grads is None:
-        grads = tuple(torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
+        grads = tuple(t.new_empty(t.shape) for t in (q, k, v))
     dq, dk, dv = grads
-    for t, name, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)):
-        _require_heads(t, name, q.dtype, q.device, like.shape[1], like.shape[2], like.shape[0])
-    work = torch.empty(rvq_window_attention_backward_bytes(shape), dtype=torch.uint8, device=q.device)
-    st = _lib().rvq_window_attention_backward(
-        ctypes.byref(shape), _heads(dout), _heads(q), _heads(k), _heads(v), _heads(out), _ptr(lse), _heads(dq),
-        _heads(dk), _heads(dv), _ptr(work), work.numel(), _stream(q))
+    tk, hk, _ = k.shape
+    dq_heads = _require_heads(dq, "dq", dtype, dev, hq, dim, tq)
+    dk_heads = _require_heads(dk, "dk", dtype, dev, hk, dim, tk)
+    dv_heads = _require_heads(dv, "dv", dtype, dev, hk, dim, tk)
+    if workspace is None:
+        workspace = q.new_empty(_backward_bytes(shape), dtype=torch.uint8)
+    _require(workspace, "workspace", torch.uint8, 1, dev)
+    st = _lib().rvq_window_attention_backward(shape, dout_heads, q_heads, k_heads, v_heads, out_heads, lse.data_ptr(),
+                                              dq_heads, dk_heads, dv_heads, workspace.data_ptr(), workspace.numel(),
+                                              _stream(q))
     _check("rvq_window_attention_backward", st)
     return dq, dk, dv
 
@@ -232,9 +257,9 @@ def _require_table(table: torch.Tensor, lens: Optional[torch.Tensor], device, re
             raise ValueError(f"refs must have one entry per page ({n_pages}), got {refs.shape[0]}")
 
 
-def _cache_shape(pool: torch.Tensor, table: torch.Tensor) -> _CacheShape:
+def _cache_shape(pool: torch.Tensor, n_clips: int, table_ld: int) -> bytes:
     pages, heads, size, dim = pool.shape[-4:]
-    return _CacheShape(DTYPES[pool.dtype], table.shape[0], heads, dim, size, pages, table.shape[1])
+    return _pack_cache(DTYPES[pool.dtype], n_clips, heads, dim, size, pages, table_ld)
 
 
 def rvq_cache_append(k: torch.Tensor, v: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
@@ -243,20 +268,23 @@ def rvq_cache_append(k: torch.Tensor, v: torch.Tensor, k_pool: torch.Tensor, v_p
     and on; None: one frame a clip) goes to position ``lens[b] + i``. Frames without a page are dropped."""
     _require_pools(k_pool, v_pool, (4,))
     dev = k_pool.device
-    _require_heads(k, "k", k_pool.dtype, dev, k_pool.shape[1], k_pool.shape[3])
-    _require_heads(v, "v", k_pool.dtype, dev, k_pool.shape[1], k_pool.shape[3], k.shape[0])
+    _, heads, _, dim = k_pool.shape
+    k_heads = _require_heads(k, "k", k_pool.dtype, dev, heads, dim)
+    n = k.shape[0]
+    v_heads = _require_heads(v, "v", k_pool.dtype, dev, heads, dim, n)
     _require_table(table, lens, dev)
+    clips, cols = table.shape
     if cu is not None:
-        _offsets(cu, "cu", dev, table.shape[0])
-    elif k.shape[0] != table.shape[0]:
+        _offsets(cu, "cu", dev, clips)
+    elif n != clips:
         raise ValueError("without cu, k must have one frame per clip")
-    st = _lib().rvq_cache_append(ctypes.byref(_cache_shape(k_pool, table)), _heads(k), _heads(v), k.shape[0], _ptr(cu),
-                                 _ptr(table), _ptr(lens), _ptr(k_pool), _ptr(v_pool), _stream(k_pool))
+    st = _lib().rvq_cache_append(_cache_shape(k_pool, clips, cols), k_heads, v_heads, n, _ptr(cu), table.data_ptr(),
+                                 lens.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), _stream(k_pool))
     _check("rvq_cache_append", st)
 
 
-def _cache_attention_bytes(shape: _CacheShape, q_heads: int) -> int:
-    size = _lib().rvq_cache_attention_bytes(ctypes.byref(shape), q_heads)
+def _cache_attention_bytes(shape: bytes, q_heads: int) -> int:
+    size = _lib().rvq_cache_attention_bytes(shape, q_heads)
     if size < 0:
         raise RVQError("rvq_cache_attention_bytes", size, rvq_status_string(size))
     return size
@@ -266,7 +294,7 @@ def rvq_cache_attention_bytes(k_pool: torch.Tensor, table: torch.Tensor, q_heads
     """Workspace of ``rvq_cache_attention`` for these pools, this table and ``q_heads`` query heads."""
     _require_pools(k_pool, k_pool, (4,))
     _require(table, "table", torch.int32, 2, k_pool.device)
-    return _cache_attention_bytes(_cache_shape(k_pool, table), q_heads)
+    return _cache_attention_bytes(_cache_shape(k_pool, *table.shape), q_heads)
 
 
 def rvq_cache_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, table: torch.Tensor,
@@ -279,23 +307,25 @@ def rvq_cache_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Ten
     _require_pools(k_pool, v_pool, (4,))
     dev = k_pool.device
     _require_table(table, lens, dev)
-    _require_heads(q, "q", k_pool.dtype, dev, dim=k_pool.shape[3], tokens=table.shape[0])
-    if k_pool.shape[1] == 0 or q.shape[1] % k_pool.shape[1] != 0:
-        raise ValueError(f"q's heads ({q.shape[1]}) must be a multiple of the pools' ({k_pool.shape[1]})")
+    clips, cols = table.shape
+    _, heads, _, dim = k_pool.shape
+    q_heads = _require_heads(q, "q", k_pool.dtype, dev, dim=dim, tokens=clips)
+    hq = q.shape[1]
+    if heads == 0 or hq % heads != 0:
+        raise ValueError(f"q's heads ({hq}) must be a multiple of the pools' ({heads})")
     if sinks < 0:
         raise ValueError(f"sinks={sinks} must not be negative")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    _require_heads(out, "out", q.dtype, dev, q.shape[1], q.shape[2], q.shape[0])
-    shape = _cache_shape(k_pool, table)
-    size = _cache_attention_bytes(shape, q.shape[1])
+        out = q.new_empty((clips, hq, dim))
+    out_heads = _require_heads(out, "out", q.dtype, dev, hq, dim, clips)
+    shape = _cache_shape(k_pool, clips, cols)
     if workspace is None:
-        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        workspace = q.new_empty(_cache_attention_bytes(shape, hq), dtype=torch.uint8)
     _require(workspace, "workspace", torch.uint8, 1, dev)
-    st = _lib().rvq_cache_attention(ctypes.byref(shape), q.shape[1], _heads(q), _ptr(k_pool), _ptr(v_pool),
-                                    _ptr(table), _ptr(lens), _window(window), sinks,
-                                    1.0 / math.sqrt(q.shape[2]) if scale is None else scale, _heads(out),
-                                    _ptr(workspace), workspace.numel(), _stream(k_pool))
+    st = _lib().rvq_cache_attention(shape, hq, q_heads, k_pool.data_ptr(), v_pool.data_ptr(), table.data_ptr(),
+                                    lens.data_ptr(), _window(window), sinks,
+                                    1.0 / math.sqrt(dim) if scale is None else scale, out_heads, workspace.data_ptr(),
+                                    workspace.numel(), _stream(k_pool))
     _check("rvq_cache_attention", st)
     return out
 
@@ -309,7 +339,7 @@ def rvq_cache_scratch_bytes(n_clips: int, n_pages: int) -> int:
 
 
 def _scratch(table: torch.Tensor, refs: torch.Tensor) -> torch.Tensor:
-    return torch.empty(rvq_cache_scratch_bytes(table.shape[0], refs.shape[0]), dtype=torch.uint8, device=table.device)
+    return table.new_empty(rvq_cache_scratch_bytes(table.shape[0], refs.shape[0]), dtype=torch.uint8)
 
 
 def rvq_cache_reserve(table: torch.Tensor, lens: torch.Tensor, new_lens: torch.Tensor, refs: torch.Tensor,
@@ -324,7 +354,7 @@ def rvq_cache_reserve(table: torch.Tensor, lens: torch.Tensor, new_lens: torch.T
     if new_lens.shape != lens.shape:
         raise ValueError("new_lens must match lens")
     table_out, refs_out = torch.empty_like(table), torch.empty_like(refs)
-    missing, work = torch.empty(1, dtype=torch.int32, device=table.device), _scratch(table, refs)
+    missing, work = table.new_empty(1), _scratch(table, refs)
     st = _lib().rvq_cache_reserve(_ptr(table), _ptr(lens), _ptr(new_lens), _ptr(refs), table.shape[0], table.shape[1],
                                   page_size, refs.shape[0], _ptr(table_out), _ptr(refs_out), _ptr(missing),
                                   _ptr(work), work.numel(), _stream(table))
@@ -351,8 +381,8 @@ def rvq_cache_fork(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, 
     if parents.shape != children.shape or children.shape[0] > table.shape[0]:
         raise ValueError("parents and children must match and be no more than there are clips")
     table_out, lens_out, refs_out = torch.empty_like(table), torch.empty_like(lens), torch.empty_like(refs)
-    missing, work = torch.empty(1, dtype=torch.int32, device=dev), _scratch(table, refs)
-    st = _lib().rvq_cache_fork(ctypes.byref(_cache_shape(k_pool, table)), _layers(k_pool), _ptr(table), _ptr(lens),
+    missing, work = table.new_empty(1), _scratch(table, refs)
+    st = _lib().rvq_cache_fork(_cache_shape(k_pool, *table.shape), _layers(k_pool), _ptr(table), _ptr(lens),
                                _ptr(refs), _ptr(parents), _ptr(children), children.shape[0], _ptr(k_pool),
                                _ptr(v_pool), _ptr(table_out), _ptr(lens_out), _ptr(refs_out), _ptr(missing),
                                _ptr(work), work.numel(), _stream(k_pool))
@@ -385,8 +415,8 @@ def rvq_cache_compact(table: torch.Tensor, refs: torch.Tensor, k_pool: torch.Ten
     dev = k_pool.device
     _require_table(table, None, dev, refs, k_pool.shape[-4])
     table_out, refs_out = torch.empty_like(table), torch.empty_like(refs)
-    live, work = torch.empty(1, dtype=torch.int32, device=dev), _scratch(table, refs)
-    st = _lib().rvq_cache_compact(ctypes.byref(_cache_shape(k_pool, table)), _layers(k_pool), _ptr(table), _ptr(refs),
+    live, work = table.new_empty(1), _scratch(table, refs)
+    st = _lib().rvq_cache_compact(_cache_shape(k_pool, *table.shape), _layers(k_pool), _ptr(table), _ptr(refs),
                                   _ptr(k_pool), _ptr(v_pool), _ptr(table_out), _ptr(refs_out), _ptr(live),
                                   _ptr(work), work.numel(), _stream(k_pool))
     _check("rvq_cache_compact", st)
@@ -400,8 +430,6 @@ def rvq_cache_copy(src: torch.Tensor, dst: torch.Tensor, k_pool: torch.Tensor, v
     _require(dst, "dst", torch.int32, 1, k_pool.device)
     if src.shape != dst.shape:
         raise ValueError("src and dst must match")
-    shape = _cache_shape(k_pool, dst[:, None])
-    shape.n_clips, shape.table_ld = 0, 0
-    st = _lib().rvq_cache_copy(ctypes.byref(shape), _layers(k_pool), _ptr(src), _ptr(dst), src.shape[0], _ptr(k_pool),
+    st = _lib().rvq_cache_copy(_cache_shape(k_pool, 0, 0), _layers(k_pool), _ptr(src), _ptr(dst), src.shape[0], _ptr(k_pool),
                                _ptr(v_pool), _stream(k_pool))
     _check("rvq_cache_copy", st)

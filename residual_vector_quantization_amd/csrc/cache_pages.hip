@@ -1,11 +1,13 @@
 // Upkeep of a paged key-value cache: append, reserve, fork, free, compact, copy.
 //
 // Page numbers are handed out lowest first, so free pages are ranked by a
-// prefix count over refs: every chunk of kChunk pages is counted by its own
-// workgroup, then each workgroup adds up the counts before its chunk and
-// ranks its pages. Only integer atomics (reference counts) are used, whose
-// order changes nothing. Page contents move in 16-byte pieces, one read and
-// one write of every byte.
+// prefix count over refs. A workgroup ranks the kChunk pages of its chunk; what
+// precedes them it counts itself in pools of up to kSelfCounted pages (reading
+// them again from the L2 costs less than the launch that would count them), or
+// finds as counts of the chunks in larger ones. Table entries, pages and
+// reference counts are then written by a second launch. Only integer atomics
+// (reference counts) are used, whose order changes nothing. Page contents move
+// in 16-byte pieces, one read and one write of every byte: bound by HBM.
 #include <limits.h>
 #include <stdint.h>
 
@@ -17,10 +19,13 @@
 namespace rvq {
 namespace {
 
+typedef int32_t s32x4 __attribute__((ext_vector_type(4)));
+
 constexpr int kThreads = 256;
 constexpr int kPerThread = 8;
 constexpr int kChunk = kThreads * kPerThread;      // pages a ranking workgroup
 constexpr int kCopyBlocks = 2048;                  // workgroups that copy pages (8 a CU)
+constexpr int kSelfCounted = 1 << 16;              // pages (and clips) up to which a workgroup counts for itself
 
 int64_t chunks(int n) { return (static_cast<int64_t>(n) + kChunk - 1) / kChunk; }
 
@@ -84,15 +89,6 @@ __device__ inline int block_exclusive(int x, int &total, int *s_wave)
     return before + inclusive - x;
 }
 
-// Sum of counts[0 .. n) by the whole workgroup.
-__device__ inline int block_total(const int32_t *counts, int n, int *s_wave)
-{
-    int sum = 0, total;
-    for (int i = threadIdx.x; i < n; i += kThreads) sum += counts[i];
-    block_exclusive(sum, total, s_wave);
-    return total;
-}
-
 __device__ inline int pages_for(int len, int page_size) { return len <= 0 ? 0 : (len - 1) / page_size + 1; }
 
 // counts[c] = pages in use in chunk c.
@@ -111,38 +107,29 @@ void count_used(const int32_t *__restrict__ refs, int n_pages, int32_t *__restri
     if (threadIdx.x == 0) counts[blockIdx.x] = total;
 }
 
-// base[b] = pages wanted by the clips before b, base[n_clips] their sum, *beyond = pages wanted past the table's
-// last column; one workgroup.
-__global__ __launch_bounds__(kThreads)
-void wanted_before(const int32_t *__restrict__ lens, const int32_t *__restrict__ new_lens, int n_clips,
-                   int page_size, int table_ld, int32_t *__restrict__ base, int32_t *__restrict__ beyond)
+// Pages in use below number `end`, by the whole workgroup; counts of the chunks, or null to count the pages.
+__device__ inline int used_below(const int32_t *refs, const int32_t *counts, int end, int *s_wave)
 {
-    __shared__ int s_wave[kThreads / 64];
-    int before = 0, past = 0, total;
-    for (int b0 = 0; b0 < n_clips; b0 += kThreads) {
-        const int b = b0 + threadIdx.x;
-        int want = 0;
-        if (b < n_clips) {
-            const int had = pages_for(lens[b], page_size), wanted = pages_for(new_lens[b], page_size);
-            want = max(0, min(wanted, table_ld) - had);
-            past += max(0, wanted - max(had, table_ld));
-        }
-        const int rank = block_exclusive(want, total, s_wave);
-        if (b < n_clips) base[b] = before + rank;
-        before += total;
+    const int whole = counts ? end / kChunk : 0;
+    int sum = 0, total;
+    for (int i = threadIdx.x; i < whole; i += kThreads) sum += counts[i];
+    const int first = whole * kChunk, fours = reinterpret_cast<uintptr_t>(refs) % 16 == 0 ? (end - first) / 4 : 0;
+    const s32x4 *four = reinterpret_cast<const s32x4 *>(refs + first);
+#pragma unroll 8
+    for (int i = threadIdx.x; i < fours; i += kThreads) {
+        const s32x4 x = four[i];
+        sum += (x[0] > 0) + (x[1] > 0) + (x[2] > 0) + (x[3] > 0);
     }
-    block_exclusive(past, total, s_wave);
-    if (threadIdx.x == 0) {
-        base[n_clips] = before;
-        *beyond = total;
-    }
+    for (int p = first + 4 * fours + threadIdx.x; p < end; p += kThreads) sum += refs[p] > 0;
+    block_exclusive(sum, total, s_wave);
+    return total;
 }
 
-// This thread's kPerThread neighbouring pages of chunk blockIdx.x: how many pages in use precede them.
-__device__ inline int used_before(const int32_t *refs, int n_pages, const int32_t *counts, int64_t first,
+// This thread's kPerThread neighbouring pages from `first` on, and how many pages in use precede them.
+__device__ inline int used_before(const int32_t *refs, int n_pages, const int32_t *counts, int chunk, int64_t first,
                                   int (&ref)[kPerThread], int *s_wave)
 {
-    const int before = block_total(counts, blockIdx.x, s_wave);
+    const int before = used_below(refs, counts, chunk * kChunk, s_wave);
     int used = 0, total;
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
@@ -152,16 +139,97 @@ __device__ inline int used_before(const int32_t *refs, int n_pages, const int32_
     return before + block_exclusive(used, total, s_wave);
 }
 
-// Free pages in order -> list (their first `most`), and refs_out with the first `wanted` of them taken.
+// What a fork or a reserve wants of the free pages.
+struct Wanted {
+    const int32_t *lens, *new_lens;             // reserve
+    const int32_t *parents, *children;          // fork (new_lens null)
+    int n, n_clips, table_ld, page_size;        // n: clips (reserve) or children (fork)
+
+    // pages that item i wants; past: those that would lie beyond the table
+    __device__ int of(int i, int &past) const
+    {
+        if (new_lens) {
+            const int had = pages_for(lens[i], page_size), want = pages_for(new_lens[i], page_size);
+            past += max(0, want - max(had, table_ld));
+            return max(0, min(want, table_ld) - had);
+        }
+        const int parent = parents[i], child = children[i];
+        if (static_cast<unsigned>(parent) >= static_cast<unsigned>(n_clips) ||
+            static_cast<unsigned>(child) >= static_cast<unsigned>(n_clips))
+            return 0;
+        const int len = max(lens[parent], 0);
+        return len % page_size != 0 && len / page_size < table_ld;     // a partial page, to be copied
+    }
+};
+
+// All that is wanted, by the whole workgroup.
+__device__ inline int total_wanted(const Wanted &w, int *s_wave)
+{
+    int sum = 0, past = 0, total;
+    for (int i = threadIdx.x; i < w.n; i += kThreads) sum += w.of(i, past);
+    block_exclusive(sum, total, s_wave);
+    return total;
+}
+
+// Scratch totals: pages wanted in the table, wanted beyond it, free; compact: pages in use, moves.
+enum Total { kInTable = 0, kBeyond = 1, kFree = 2, kLive = 0, kMoves = 1 };
+
+// base[i] = pages wanted before item i, and the totals; one workgroup.
+__device__ inline void rank_wanted(const Wanted &w, int32_t *base, int32_t *totals, int *s_wave)
+{
+    int before = 0, past = 0, total;
+    for (int i0 = 0; i0 < w.n; i0 += kThreads) {
+        const int i = i0 + threadIdx.x;
+        const int rank = block_exclusive(i < w.n ? w.of(i, past) : 0, total, s_wave);
+        if (i < w.n) base[i] = before + rank;
+        before += total;
+    }
+    block_exclusive(past, total, s_wave);
+    if (threadIdx.x == 0) {
+        totals[kInTable] = before;
+        totals[kBeyond] = total;
+    }
+}
+
 __global__ __launch_bounds__(kThreads)
-void take_free(const int32_t *__restrict__ refs, int n_pages, const int32_t *__restrict__ counts,
-               const int32_t *__restrict__ wanted, int32_t *__restrict__ list, int32_t *__restrict__ refs_out)
+void rank_wanted_alone(Wanted w, int32_t *__restrict__ base, int32_t *__restrict__ totals)
 {
     __shared__ int s_wave[kThreads / 64];
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * kChunk + threadIdx.x * kPerThread;
+    rank_wanted(w, base, totals, s_wave);
+}
+
+// First launch of reserve and fork. Workgroups 0 .. n_chunks - 1: free pages in order -> list (as many as are
+// wanted), and refs_out with those taken. The next one ranks what is wanted, unless that has been done (counted).
+// Those that are left copy the n_copies pairs of arrays for fork.
+struct IntCopy {
+    const int32_t *from;
+    int32_t *to;
+    int64_t n;
+};
+
+__global__ __launch_bounds__(kThreads)
+void take_free(const int32_t *__restrict__ refs, int n_pages, int n_chunks, const int32_t *__restrict__ counts,
+               Wanted w, int32_t *__restrict__ base, int32_t *__restrict__ totals, int32_t *__restrict__ list,
+               int32_t *__restrict__ refs_out, IntCopy one, IntCopy two)
+{
+    __shared__ int s_wave[kThreads / 64];
+    const int chunk = blockIdx.x;
+    if (chunk > n_chunks) {
+        int64_t i = (chunk - n_chunks - 1) * static_cast<int64_t>(kThreads) + threadIdx.x;
+        if (i < one.n) one.to[i] = one.from[i];
+        else if ((i -= one.n) < two.n) two.to[i] = two.from[i];
+        return;
+    }
+    if (chunk == n_chunks) {
+        if (!counts) rank_wanted(w, base, totals, s_wave);
+        const int used = used_below(refs, counts, n_pages, s_wave);
+        if (threadIdx.x == 0) totals[kFree] = n_pages - used;
+        return;
+    }
+    const int take = counts ? totals[kInTable] : total_wanted(w, s_wave);
+    const int64_t first = static_cast<int64_t>(chunk) * kChunk + threadIdx.x * kPerThread;
     int ref[kPerThread];
-    int used = used_before(refs, n_pages, counts, first, ref, s_wave);
-    const int take = *wanted;
+    int used = used_before(refs, n_pages, counts, chunk, first, ref, s_wave);
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
         const int64_t p = first + i;
@@ -174,69 +242,113 @@ void take_free(const int32_t *__restrict__ refs, int n_pages, const int32_t *__r
     }
 }
 
-__device__ inline int free_pages(const int32_t *counts, int n_chunks, int n_pages, int *s_wave)
+__device__ inline void write_missing(const int32_t *totals, int32_t *missing)
 {
-    return n_pages - block_total(counts, n_chunks, s_wave);
+    *missing = max(0, totals[kInTable] - totals[kFree]) + totals[kBeyond];
 }
 
-// table_out = table with the wanted entries filled from the list of free pages; one thread an entry.
+// reserve, second launch: table_out = table with the wanted entries filled from the list of free pages; one thread an
+// entry.
 __global__ __launch_bounds__(kThreads)
 void fill_table(const int32_t *__restrict__ table, const int32_t *__restrict__ lens,
-                const int32_t *__restrict__ new_lens, int n_clips, int table_ld, int page_size, int n_pages,
-                const int32_t *__restrict__ counts, int n_chunks, const int32_t *__restrict__ base,
-                const int32_t *__restrict__ list, int32_t *__restrict__ table_out)
+                const int32_t *__restrict__ new_lens, int n_clips, int table_ld, int page_size,
+                const int32_t *__restrict__ totals, const int32_t *__restrict__ base,
+                const int32_t *__restrict__ list, int32_t *__restrict__ table_out, int32_t *__restrict__ missing)
 {
-    __shared__ int s_wave[kThreads / 64];
-    const int n_free = free_pages(counts, n_chunks, n_pages, s_wave);
     const int64_t at = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    if (at == 0) write_missing(totals, missing);
     if (at >= static_cast<int64_t>(n_clips) * table_ld) return;
     const int b = static_cast<int>(at / table_ld), e = static_cast<int>(at - static_cast<int64_t>(b) * table_ld);
     const int had = pages_for(lens[b], page_size), want = pages_for(new_lens[b], page_size);
     int page = table[at];
     if (e >= had && e < want) {
         const int rank = base[b] + e - had;
-        if (rank < n_free) page = list[rank];
+        if (rank < totals[kFree]) page = list[rank];
     }
     table_out[at] = page;
 }
 
-// missing = wanted pages that there are not (and those past the table), one workgroup.
-__global__ __launch_bounds__(kThreads)
-void count_missing(const int32_t *__restrict__ counts, int n_chunks, int n_pages,
-                   const int32_t *__restrict__ wanted, const int32_t *__restrict__ beyond,
-                   int32_t *__restrict__ missing)
+// Copies one page of one layer of one pool; the whole workgroup.
+__device__ inline void copy_page(char *pool, int source, int target, int64_t page_bytes)
 {
-    __shared__ int s_wave[kThreads / 64];
-    const int n_free = free_pages(counts, n_chunks, n_pages, s_wave);
-    if (threadIdx.x == 0) *missing = max(0, *wanted - n_free) + (beyond ? *beyond : 0);
+    const u32x4 *from = reinterpret_cast<const u32x4 *>(pool + source * page_bytes);
+    u32x4 *to = reinterpret_cast<u32x4 *>(pool + target * page_bytes);
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < page_bytes / 16; i += kThreads) to[i] = from[i];
 }
 
-// fork, first step: which children want a page of their own for a partial page, in order; one workgroup.
-__device__ inline bool wants_part(const int32_t *lens, int parent, int child, int n_clips, int table_ld, int page_size)
-{
-    if (static_cast<unsigned>(parent) >= static_cast<unsigned>(n_clips) ||
-        static_cast<unsigned>(child) >= static_cast<unsigned>(n_clips))
-        return false;
-    const int n = max(lens[parent], 0);
-    return n % page_size != 0 && n / page_size < table_ld;
-}
+struct Pools {
+    char *k, *v;
+    int n_pages, n_layers;
+    int64_t page_bytes;
 
-__global__ __launch_bounds__(kThreads)
-void wanted_parts(const int32_t *__restrict__ lens, const int32_t *__restrict__ parents,
-                  const int32_t *__restrict__ children, int n_children, int n_clips, int table_ld, int page_size,
-                  int32_t *__restrict__ base)
-{
-    __shared__ int s_wave[kThreads / 64];
-    int before = 0;
-    for (int c0 = 0; c0 < n_children; c0 += kThreads) {
-        const int c = c0 + threadIdx.x;
-        int total;
-        const int want = c < n_children && wants_part(lens, parents[c], children[c], n_clips, table_ld, page_size);
-        const int rank = block_exclusive(want, total, s_wave);
-        if (c < n_children) base[c] = before + rank;
-        before += total;
+    // job = (pair * n_layers + layer) * 2 + pool
+    __device__ void copy(int64_t job, int64_t pair, int source, int target) const
+    {
+        if (static_cast<unsigned>(source) >= static_cast<unsigned>(n_pages) ||
+            static_cast<unsigned>(target) >= static_cast<unsigned>(n_pages))
+            return;
+        const int rest = static_cast<int>(job - pair * 2 * n_layers), layer = rest >> 1;
+        copy_page(((rest & 1) ? v : k) + static_cast<int64_t>(layer) * n_pages * page_bytes, source, target, page_bytes);
     }
-    if (threadIdx.x == 0) base[n_clips] = before;
+};
+
+// fork, second launch: a workgroup a child rewrites its row and counts references; those that are left copy the
+// partial pages, whole (page, layer, pool) jobs in turn.
+__global__ __launch_bounds__(kThreads)
+void fork_rows(Wanted w, const int32_t *__restrict__ table, const int32_t *__restrict__ totals,
+               const int32_t *__restrict__ base, const int32_t *__restrict__ list, int32_t *__restrict__ table_out,
+               int32_t *__restrict__ lens_out, int32_t *__restrict__ refs_out, int32_t *__restrict__ missing, Pools pools)
+{
+    const int n_free = totals[kFree];
+    // the child's page for the parent's partial one: its column, and the page
+    auto part_of = [&](int c, int &column) {
+        int past = 0;
+        const bool part = w.of(c, past) != 0;
+        column = part ? w.lens[w.parents[c]] / w.page_size : -1;
+        return part && base[c] < n_free ? list[base[c]] : -1;
+    };
+    if (blockIdx.x >= static_cast<unsigned>(w.n)) {
+        const int64_t jobs = static_cast<int64_t>(w.n) * pools.n_layers * 2, step = gridDim.x - w.n;
+        for (int64_t job = blockIdx.x - w.n; job < jobs; job += step) {
+            const int64_t pair = job / (2 * pools.n_layers);
+            int column;
+            const int target = part_of(static_cast<int>(pair), column);
+            if (target >= 0)
+                pools.copy(job, pair, table[static_cast<int64_t>(w.parents[pair]) * w.table_ld + column], target);
+        }
+        return;
+    }
+    const int c = blockIdx.x, parent = w.parents[c], child = w.children[c];
+    if (c == 0 && threadIdx.x == 0) write_missing(totals, missing);
+    if (static_cast<unsigned>(parent) >= static_cast<unsigned>(w.n_clips) ||
+        static_cast<unsigned>(child) >= static_cast<unsigned>(w.n_clips))
+        return;
+    int own;
+    const int fresh = part_of(c, own);
+    const int32_t *from = table + static_cast<int64_t>(parent) * w.table_ld;
+    const int32_t *was = table + static_cast<int64_t>(child) * w.table_ld;
+    int32_t *to = table_out + static_cast<int64_t>(child) * w.table_ld;
+    for (int e = threadIdx.x; e < w.table_ld; e += kThreads) {
+        const int left = was[e];
+        int page = from[e];
+        if (static_cast<unsigned>(left) < static_cast<unsigned>(pools.n_pages)) atomicSub(&refs_out[left], 1);
+        if (e == own) page = fresh;
+        else if (static_cast<unsigned>(page) < static_cast<unsigned>(pools.n_pages)) atomicAdd(&refs_out[page], 1);
+        to[e] = page;
+    }
+    if (threadIdx.x == 0) lens_out[child] = w.lens[parent];
+}
+
+// copy: page sources[i] to targets[i].
+__global__ __launch_bounds__(kThreads)
+void copy_pages(const int32_t *__restrict__ sources, const int32_t *__restrict__ targets, int n, Pools pools)
+{
+    const int64_t jobs = static_cast<int64_t>(n) * pools.n_layers * 2;
+    for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
+        const int64_t pair = job / (2 * pools.n_layers);
+        pools.copy(job, pair, sources[pair], targets[pair]);
+    }
 }
 
 __global__ __launch_bounds__(kThreads)
@@ -244,74 +356,6 @@ void copy_ints(const int32_t *__restrict__ from, int32_t *__restrict__ to, int64
 {
     const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
     if (i < n) to[i] = from[i];
-}
-
-// fork, second step: one wavefront a child rewrites its row, counts references and lists its page copy.
-__global__ __launch_bounds__(64)
-void fork_rows(const int32_t *__restrict__ table, const int32_t *__restrict__ lens,
-               const int32_t *__restrict__ parents, const int32_t *__restrict__ children, int n_clips, int table_ld,
-               int page_size, int n_pages, const int32_t *__restrict__ counts, int n_chunks,
-               const int32_t *__restrict__ base, const int32_t *__restrict__ list, int32_t *__restrict__ table_out,
-               int32_t *__restrict__ lens_out, int32_t *__restrict__ refs_out, int32_t *__restrict__ sources,
-               int32_t *__restrict__ targets)
-{
-    const int c = blockIdx.x, lane = threadIdx.x;
-    const int parent = parents[c], child = children[c];
-    int free_count = 0;
-    for (int i = lane; i < n_chunks; i += 64) free_count += counts[i];
-#pragma unroll
-    for (int m = 32; m > 0; m >>= 1) free_count += __shfl_xor(free_count, m);
-    free_count = n_pages - free_count;
-    int source = -1, target = -1;
-    if (static_cast<unsigned>(parent) < static_cast<unsigned>(n_clips) &&
-        static_cast<unsigned>(child) < static_cast<unsigned>(n_clips)) {
-        const bool part = wants_part(lens, parent, child, n_clips, table_ld, page_size);
-        const int n = lens[parent], own = part ? n / page_size : -1;
-        const int fresh = part && base[c] < free_count ? list[base[c]] : -1;
-        const int32_t *from = table + static_cast<int64_t>(parent) * table_ld;
-        const int32_t *was = table + static_cast<int64_t>(child) * table_ld;
-        int32_t *to = table_out + static_cast<int64_t>(child) * table_ld;
-        for (int e = lane; e < table_ld; e += 64) {
-            const int left = was[e];
-            int page = from[e];
-            if (static_cast<unsigned>(left) < static_cast<unsigned>(n_pages)) atomicSub(&refs_out[left], 1);
-            if (e == own) page = fresh;
-            else if (static_cast<unsigned>(page) < static_cast<unsigned>(n_pages)) atomicAdd(&refs_out[page], 1);
-            to[e] = page;
-        }
-        if (lane == 0) lens_out[child] = n;
-        if (fresh >= 0) {
-            source = from[own];
-            target = fresh;
-        }
-    }
-    if (lane == 0) {
-        sources[c] = source;
-        targets[c] = target;
-    }
-}
-
-// Copies page sources[i] to targets[i] for i < *count (or n), every layer of both pools; pairs with a number
-// outside the pool are skipped. A workgroup takes whole (pair, layer, pool) pages in turn.
-__global__ __launch_bounds__(kThreads)
-void copy_pages(const int32_t *__restrict__ sources, const int32_t *__restrict__ targets, int n,
-                const int32_t *__restrict__ count, int n_pages, int n_layers, int64_t page_bytes, char *k_pool,
-                char *v_pool)
-{
-    if (count) n = min(n, *count);
-    const int64_t jobs = static_cast<int64_t>(n) * n_layers * 2;
-    for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
-        const int64_t pair = job / (2 * n_layers);
-        const int rest = static_cast<int>(job - pair * 2 * n_layers), layer = rest >> 1;
-        const int s = sources[pair], d = targets[pair];
-        if (static_cast<unsigned>(s) >= static_cast<unsigned>(n_pages) ||
-            static_cast<unsigned>(d) >= static_cast<unsigned>(n_pages))
-            continue;
-        char *pool = ((rest & 1) ? v_pool : k_pool) + static_cast<int64_t>(layer) * n_pages * page_bytes;
-        const u32x4 *from = reinterpret_cast<const u32x4 *>(pool + s * page_bytes);
-        u32x4 *to = reinterpret_cast<u32x4 *>(pool + d * page_bytes);
-        for (int64_t i = threadIdx.x; i < page_bytes / 16; i += kThreads) to[i] = from[i];
-    }
 }
 
 // free: what leaves the table, reference counts go down.
@@ -336,24 +380,19 @@ void free_entries(const int32_t *__restrict__ table, const int32_t *__restrict__
     table_out[at] = page;
 }
 
-// compact: pages in use numbered live and more are sources, free pages below live are targets, both in order.
+// compact, first launch: pages in use numbered live and more are sources, free pages below live are targets, both in
+// order.
 __global__ __launch_bounds__(kThreads)
-void list_moves(const int32_t *__restrict__ refs, int n_pages, const int32_t *__restrict__ counts, int n_chunks,
+void list_moves(const int32_t *__restrict__ refs, int n_pages, const int32_t *__restrict__ counts,
                 int32_t *__restrict__ totals, int32_t *__restrict__ sources, int32_t *__restrict__ targets,
                 int32_t *__restrict__ rank, int32_t *__restrict__ live_out)
 {
     __shared__ int s_wave[kThreads / 64];
-    const int live = block_total(counts, n_chunks, s_wave);
-    // pages in use below number live
-    const int border = live / kChunk;
-    int below = block_total(counts, border, s_wave);
-    int more = 0, total;
-    for (int64_t p = static_cast<int64_t>(border) * kChunk + threadIdx.x; p < live; p += kThreads) more += refs[p] > 0;
-    block_exclusive(more, total, s_wave);
-    below += total;
+    const int live = used_below(refs, counts, n_pages, s_wave);
+    const int below = used_below(refs, counts, live, s_wave);
     const int64_t first = static_cast<int64_t>(blockIdx.x) * kChunk + threadIdx.x * kPerThread;
     int ref[kPerThread];
-    int used = used_before(refs, n_pages, counts, first, ref, s_wave);
+    int used = used_before(refs, n_pages, counts, blockIdx.x, first, ref, s_wave);
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
         const int64_t p = first + i;
@@ -367,26 +406,35 @@ void list_moves(const int32_t *__restrict__ refs, int n_pages, const int32_t *__
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         *live_out = live;
-        totals[0] = live;
-        totals[1] = live - below;    // moves
+        totals[kLive] = live;
+        totals[kMoves] = live - below;
     }
 }
 
-// compact: new numbers in the table, reference counts at the new numbers.
+// compact, second launch: workgroups 0 .. n_renumber - 1 put new numbers into the table and reference counts at the
+// new numbers, those that are left move the pages.
 __global__ __launch_bounds__(kThreads)
-void renumber(const int32_t *__restrict__ table, int64_t entries, const int32_t *__restrict__ refs, int n_pages,
-              const int32_t *__restrict__ totals, const int32_t *__restrict__ sources,
-              const int32_t *__restrict__ targets, const int32_t *__restrict__ rank, int32_t *__restrict__ table_out,
-              int32_t *__restrict__ refs_out)
+void move_pages(int n_renumber, const int32_t *__restrict__ table, int64_t entries, const int32_t *__restrict__ refs,
+                const int32_t *__restrict__ totals, const int32_t *__restrict__ sources,
+                const int32_t *__restrict__ targets, const int32_t *__restrict__ rank, int32_t *__restrict__ table_out,
+                int32_t *__restrict__ refs_out, Pools pools)
 {
+    const int live = totals[kLive], moves = totals[kMoves];
+    if (blockIdx.x >= static_cast<unsigned>(n_renumber)) {
+        const int64_t jobs = static_cast<int64_t>(moves) * pools.n_layers * 2, step = gridDim.x - n_renumber;
+        for (int64_t job = blockIdx.x - n_renumber; job < jobs; job += step) {
+            const int64_t pair = job / (2 * pools.n_layers);
+            pools.copy(job, pair, sources[pair], targets[pair]);
+        }
+        return;
+    }
     const int64_t at = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    const int live = totals[0], moves = totals[1];
     if (at < entries) {
         int page = table[at];
-        if (page >= live && page < n_pages) page = refs[page] > 0 ? targets[rank[page]] : -1;
+        if (page >= live && page < pools.n_pages) page = refs[page] > 0 ? targets[rank[page]] : -1;
         table_out[at] = page;
     }
-    if (at < n_pages) {
+    if (at < pools.n_pages) {
         const int ref = refs[at];
         if (at >= live) refs_out[at] = 0;
         else if (ref > 0) refs_out[at] = ref;
@@ -394,51 +442,68 @@ void renumber(const int32_t *__restrict__ table, int64_t entries, const int32_t 
     if (at < moves) refs_out[targets[at]] = refs[sources[at]];
 }
 
-// append: a thread a 16-byte piece of a new frame's key and value rows.
+// append: a workgroup takes kAppendTokens new frames, finds their places, then moves their rows, a thread 16 bytes of
+// a key row and of the value row beside it.
+constexpr int kAppendTokens = 8;
+
 __global__ __launch_bounds__(kThreads)
 void append_rows(Heads k, Heads v, int64_t n_tokens, const int32_t *__restrict__ cu, int n_clips, int kv_heads,
                  int pieces, int element_bytes, int page_size, int n_pages, int table_ld,
                  const int32_t *__restrict__ table, const int32_t *__restrict__ lens, char *__restrict__ k_pool,
                  char *__restrict__ v_pool)
 {
-    const int64_t at = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    const int piece = static_cast<int>(at % pieces);
-    const int64_t row = at / pieces;
-    const int head = static_cast<int>(row % kv_heads);
-    const int64_t token = row / kv_heads;
-    if (token >= n_tokens) return;
-    int clip = static_cast<int>(token), nth = 0;
-    if (cu) {
-        clip = clip_of_row(cu, n_clips, static_cast<int>(token));
-        nth = static_cast<int>(token) - cu[clip];
-        if (nth < 0 || token >= cu[clip + 1]) return;    // outside every clip
+    __shared__ int64_t s_row[kAppendTokens];       // the frame's row at head 0 in the pools, -1 for none
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kAppendTokens;
+    if (threadIdx.x < kAppendTokens) {
+        const int64_t token = first + threadIdx.x;
+        int64_t row = -1;
+        int clip = static_cast<int>(token), nth = 0;
+        bool there = token < n_tokens;
+        if (there && cu) {
+            clip = clip_of_row(cu, n_clips, static_cast<int>(token));
+            nth = static_cast<int>(token) - cu[clip];
+            there = nth >= 0 && token < cu[clip + 1];      // not outside every clip
+        }
+        if (there) {
+            const int64_t position = static_cast<int64_t>(lens[clip]) + nth;
+            if (position >= 0 && position < static_cast<int64_t>(table_ld) * page_size) {
+                const int e = static_cast<int>(position) / page_size, slot = static_cast<int>(position) - e * page_size;
+                const int page = table[static_cast<int64_t>(clip) * table_ld + e];
+                if (static_cast<unsigned>(page) < static_cast<unsigned>(n_pages))
+                    row = static_cast<int64_t>(page) * kv_heads * page_size + slot;
+            }
+        }
+        s_row[threadIdx.x] = row;
     }
-    const int64_t position = static_cast<int64_t>(lens[clip]) + nth;
-    if (position < 0 || position >= static_cast<int64_t>(table_ld) * page_size) return;
-    const int e = static_cast<int>(position) / page_size, slot = static_cast<int>(position) - e * page_size;
-    const int page = table[static_cast<int64_t>(clip) * table_ld + e];
-    if (static_cast<unsigned>(page) >= static_cast<unsigned>(n_pages)) return;
-    const int64_t to = (((static_cast<int64_t>(page) * kv_heads + head) * page_size + slot) * pieces + piece) * 16;
-    const char *from_k = static_cast<const char *>(k.data) + (token * k.token + head * k.head) * element_bytes;
-    const char *from_v = static_cast<const char *>(v.data) + (token * v.token + head * v.head) * element_bytes;
-    *reinterpret_cast<u32x4 *>(k_pool + to) = *reinterpret_cast<const u32x4 *>(from_k + piece * 16);
-    *reinterpret_cast<u32x4 *>(v_pool + to) = *reinterpret_cast<const u32x4 *>(from_v + piece * 16);
+    __syncthreads();
+    const int per_token = kv_heads * pieces;
+#pragma unroll 4
+    for (int at = threadIdx.x; at < kAppendTokens * per_token; at += kThreads) {
+        const int n = at / per_token, rest = at - n * per_token, head = rest / pieces, piece = rest - head * pieces;
+        const int64_t row = s_row[n], token = first + n;
+        if (row < 0) continue;
+        const int64_t to = ((row + static_cast<int64_t>(head) * page_size) * pieces + piece) * 16;
+        const char *from_k = static_cast<const char *>(k.data) + (token * k.token + head * k.head) * element_bytes;
+        const char *from_v = static_cast<const char *>(v.data) + (token * v.token + head * v.head) * element_bytes;
+        *reinterpret_cast<u32x4 *>(k_pool + to) = *reinterpret_cast<const u32x4 *>(from_k + piece * 16);
+        *reinterpret_cast<u32x4 *>(v_pool + to) = *reinterpret_cast<const u32x4 *>(from_v + piece * 16);
+    }
 }
 
-hipError_t launch_copy(const int32_t *sources, const int32_t *targets, int64_t most, const int32_t *count, int n_pages,
-                       int n_layers, int64_t page_bytes, void *k_pool, void *v_pool, hipStream_t stream)
-{
-    const int64_t jobs = most * n_layers * 2;
-    if (jobs == 0) return hipSuccess;
-    copy_pages<<<static_cast<unsigned>(jobs < kCopyBlocks ? jobs : kCopyBlocks), kThreads, 0, stream>>>(
-        sources, targets, static_cast<int>(most), count, n_pages, n_layers, page_bytes, static_cast<char *>(k_pool),
-        static_cast<char *>(v_pool));
-    return hipGetLastError();
-}
+unsigned copy_blocks(int64_t jobs) { return static_cast<unsigned>(jobs < kCopyBlocks ? jobs : kCopyBlocks); }
 
-void launch_copy_ints(const int32_t *from, int32_t *to, int64_t n, hipStream_t stream)
+// First launch of reserve and fork (and before it, in large pools or with many clips, the counting ones).
+void launch_take_free(const int32_t *refs, int n_pages, const Wanted &w, const Scratch &s, int32_t *list,
+                      int32_t *refs_out, const IntCopy &one, const IntCopy &two, hipStream_t stream)
 {
-    if (n > 0) copy_ints<<<ceil_div(n, kThreads), kThreads, 0, stream>>>(from, to, n);
+    const int n_chunks = static_cast<int>(chunks(n_pages));
+    const bool counted = n_pages > kSelfCounted || w.n > kSelfCounted / 16;
+    if (counted) {
+        if (n_chunks) count_used<<<n_chunks, kThreads, 0, stream>>>(refs, n_pages, s.counts);
+        rank_wanted_alone<<<1, kThreads, 0, stream>>>(w, s.base, s.totals);
+    }
+    take_free<<<n_chunks + 1 + ceil_div(one.n + two.n, kThreads), kThreads, 0, stream>>>(
+        refs, n_pages, n_chunks, counted ? s.counts : nullptr, w, s.base, s.totals, list, refs_out, one, two);
 }
 
 }  // namespace
@@ -451,7 +516,7 @@ hipError_t launch_cache_append(const Heads &k, const Heads &v, int64_t n_tokens,
                                hipStream_t stream)
 {
     const int pieces = dim * element_bytes / 16;
-    append_rows<<<ceil_div(n_tokens * kv_heads * pieces, kThreads), kThreads, 0, stream>>>(
+    append_rows<<<ceil_div(n_tokens, kAppendTokens), kThreads, 0, stream>>>(
         k, v, n_tokens, cu, n_clips, kv_heads, pieces, element_bytes, page_size, n_pages, table_ld, table, lens,
         static_cast<char *>(k_pool), static_cast<char *>(v_pool));
     return hipGetLastError();
@@ -463,18 +528,11 @@ hipError_t launch_cache_reserve(const int32_t *table, const int32_t *lens, const
                                 hipStream_t stream)
 {
     const Scratch s = scratch(workspace, n_clips, n_pages);
-    const int n_chunks = static_cast<int>(chunks(n_pages));
-    if (n_chunks) count_used<<<n_chunks, kThreads, 0, stream>>>(refs, n_pages, s.counts);
-    wanted_before<<<1, kThreads, 0, stream>>>(lens, new_lens, n_clips, page_size, table_ld, s.base,
-                                             s.totals);
-    if (n_chunks)
-        take_free<<<n_chunks, kThreads, 0, stream>>>(refs, n_pages, s.counts, s.base + n_clips, s.sources, refs_out);
+    const Wanted w = {lens, new_lens, nullptr, nullptr, n_clips, n_clips, table_ld, page_size};
+    launch_take_free(refs, n_pages, w, s, s.sources, refs_out, IntCopy{}, IntCopy{}, stream);
     const int64_t entries = static_cast<int64_t>(n_clips) * table_ld;
-    if (entries)
-        fill_table<<<ceil_div(entries, kThreads), kThreads, 0, stream>>>(table, lens, new_lens, n_clips, table_ld,
-                                                                         page_size, n_pages, s.counts, n_chunks,
-                                                                         s.base, s.sources, table_out);
-    count_missing<<<1, kThreads, 0, stream>>>(s.counts, n_chunks, n_pages, s.base + n_clips, s.totals, missing);
+    fill_table<<<entries ? ceil_div(entries, kThreads) : 1, kThreads, 0, stream>>>(
+        table, lens, new_lens, n_clips, table_ld, page_size, s.totals, s.base, s.sources, table_out, missing);
     return hipGetLastError();
 }
 
@@ -485,28 +543,28 @@ hipError_t launch_cache_fork(const int32_t *table, const int32_t *lens, const in
                              void *workspace, hipStream_t stream)
 {
     const Scratch s = scratch(workspace, n_clips, n_pages);
-    const int n_chunks = static_cast<int>(chunks(n_pages));
-    if (n_chunks) count_used<<<n_chunks, kThreads, 0, stream>>>(refs, n_pages, s.counts);
-    wanted_parts<<<1, kThreads, 0, stream>>>(lens, parents, children, n_children, n_clips, table_ld, page_size, s.base);
-    launch_copy_ints(table, table_out, static_cast<int64_t>(n_clips) * table_ld, stream);
-    launch_copy_ints(lens, lens_out, n_clips, stream);
-    if (n_chunks)
-        take_free<<<n_chunks, kThreads, 0, stream>>>(refs, n_pages, s.counts, s.base + n_clips, s.rank, refs_out);
-    if (n_children)
-        fork_rows<<<n_children, 64, 0, stream>>>(table, lens, parents, children, n_clips, table_ld, page_size, n_pages,
-                                                 s.counts, n_chunks, s.base, s.rank, table_out, lens_out, refs_out,
-                                                 s.sources, s.targets);
-    count_missing<<<1, kThreads, 0, stream>>>(s.counts, n_chunks, n_pages, s.base + n_clips, nullptr, missing);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || n_pages == 0) return e;
-    return launch_copy(s.sources, s.targets, n_children, nullptr, n_pages, n_layers, page_bytes, k_pool, v_pool, stream);
+    // new_lens null makes it a fork; a fork of no children still copies the arrays and reports nothing missing
+    const Wanted w = {lens, nullptr, parents, children, n_children, n_clips, table_ld, page_size};
+    const Pools pools = {static_cast<char *>(k_pool), static_cast<char *>(v_pool), n_pages, n_layers, page_bytes};
+    launch_take_free(refs, n_pages, w, s, s.sources, refs_out,
+                     IntCopy{table, table_out, static_cast<int64_t>(n_clips) * table_ld}, IntCopy{lens, lens_out, n_clips},
+                     stream);
+    if (n_children == 0) {
+        fill_table<<<1, kThreads, 0, stream>>>(nullptr, nullptr, nullptr, 0, 0, 1, s.totals, s.base, s.sources, nullptr,
+                                               missing);
+        return hipGetLastError();
+    }
+    const int64_t jobs = static_cast<int64_t>(n_children) * n_layers * 2;
+    fork_rows<<<n_children + copy_blocks(jobs), kThreads, 0, stream>>>(w, table, s.totals, s.base, s.sources, table_out,
+                                                                       lens_out, refs_out, missing, pools);
+    return hipGetLastError();
 }
 
 hipError_t launch_cache_free(const int32_t *table, const int32_t *lens, const int32_t *refs, const int32_t *drop,
                              int n_clips, int table_ld, int page_size, int n_pages, int64_t window, int sinks,
                              int32_t *table_out, int32_t *lens_out, int32_t *refs_out, hipStream_t stream)
 {
-    launch_copy_ints(refs, refs_out, n_pages, stream);
+    if (n_pages > 0) copy_ints<<<ceil_div(n_pages, kThreads), kThreads, 0, stream>>>(refs, refs_out, n_pages);
     const int64_t entries = static_cast<int64_t>(n_clips) * (table_ld > 0 ? table_ld : 1);
     if (entries)
         free_entries<<<ceil_div(entries, kThreads), kThreads, 0, stream>>>(table, lens, drop, n_clips, table_ld,
@@ -520,24 +578,27 @@ hipError_t launch_cache_compact(const int32_t *table, const int32_t *refs, int n
                                 int32_t *refs_out, int32_t *live, void *workspace, hipStream_t stream)
 {
     const Scratch s = scratch(workspace, n_clips, n_pages);
+    const Pools pools = {static_cast<char *>(k_pool), static_cast<char *>(v_pool), n_pages, n_layers, page_bytes};
     const int n_chunks = static_cast<int>(chunks(n_pages));
-    if (n_chunks) count_used<<<n_chunks, kThreads, 0, stream>>>(refs, n_pages, s.counts);
-    list_moves<<<n_chunks ? n_chunks : 1, kThreads, 0, stream>>>(refs, n_pages, s.counts, n_chunks, s.totals,
+    const bool counted = n_pages > kSelfCounted;
+    if (counted) count_used<<<n_chunks, kThreads, 0, stream>>>(refs, n_pages, s.counts);
+    list_moves<<<n_chunks ? n_chunks : 1, kThreads, 0, stream>>>(refs, n_pages, counted ? s.counts : nullptr, s.totals,
                                                                  s.sources, s.targets, s.rank, live);
     const int64_t entries = static_cast<int64_t>(n_clips) * table_ld, most = entries > n_pages ? entries : n_pages;
-    if (most)
-        renumber<<<ceil_div(most, kThreads), kThreads, 0, stream>>>(table, entries, refs, n_pages, s.totals, s.sources,
-                                                                    s.targets, s.rank, table_out, refs_out);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || n_pages == 0) return e;
-    return launch_copy(s.sources, s.targets, n_pages / 2, s.totals + 1, n_pages, n_layers, page_bytes, k_pool, v_pool,
-                       stream);
+    const unsigned renumber = ceil_div(most, kThreads);
+    const unsigned movers = copy_blocks(static_cast<int64_t>(n_pages / 2) * n_layers * 2);
+    if (renumber + movers)
+        move_pages<<<renumber + movers, kThreads, 0, stream>>>(static_cast<int>(renumber), table, entries, refs, s.totals,
+                                                               s.sources, s.targets, s.rank, table_out, refs_out, pools);
+    return hipGetLastError();
 }
 
 hipError_t launch_cache_copy(const int32_t *src, const int32_t *dst, int n_copies, int n_pages, int n_layers,
                              int64_t page_bytes, void *k_pool, void *v_pool, hipStream_t stream)
 {
-    return launch_copy(src, dst, n_copies, nullptr, n_pages, n_layers, page_bytes, k_pool, v_pool, stream);
+    const Pools pools = {static_cast<char *>(k_pool), static_cast<char *>(v_pool), n_pages, n_layers, page_bytes};
+    copy_pages<<<copy_blocks(static_cast<int64_t>(n_copies) * n_layers * 2), kThreads, 0, stream>>>(src, dst, n_copies, pools);
+    return hipGetLastError();
 }
 
 }  // namespace rvq

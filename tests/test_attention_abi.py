@@ -36,6 +36,14 @@ def test_header_binding_and_library_agree(lib):
         assert hasattr(lib, name) and callable(getattr(rvq, name))
 
 
+def test_packed_structures_are_the_structures():
+    from residual_vector_quantization_amd import attention as a
+    assert bytes(a._Heads(1, 2, 3)) == a._pack_heads(1, 2, 3)
+    assert bytes(a._CacheShape(1, 2, 3, 4, 5, 6, 7)) == a._pack_cache(1, 2, 3, 4, 5, 6, 7)
+    fields = (1, 2, 3, 4, 5, 6, -7, 2 ** 40, 9, 2 ** 47, 11, 0.5)
+    assert bytes(a._AttentionShape(*fields)) == a._pack_attention(*fields)
+
+
 def test_header_is_c99(tmp_path):
     src = tmp_path / "use.c"
     src.write_text('#include "rvq_attention.h"\nint main(void) { rvq_heads h = {0, 0, 0}; rvq_cache_shape s = '
