@@ -68,6 +68,8 @@ void forward_tiles(AttentionArgs a, float factor, int slots)
         const T *at = static_cast<const T *>(a.q.data) + static_cast<int64_t>(q0 + min(row, nq - 1)) * a.q.token + head * a.q.head;
 #pragma unroll
         for (int t = 0; t < kD / 16; ++t) q[t] = load8(at + 16 * t + 8 * half);
+#pragma unroll
+        for (int t = 0; t < kD / 16; ++t) arrive(q[t]);
     }
     const typename Rows::Loader load_k(a.k.token), load_v(a.v.token);
     const T *keys = static_cast<const T *>(a.k.data) + static_cast<int64_t>(k0) * a.k.token + kv * a.k.head;

@@ -51,10 +51,10 @@ constexpr int kFarRows = 256;           // queries of a piece beyond the window
 constexpr int kLongClip = 2048;         // average clip from which the sinks are split off
 constexpr int kMaxSplitSinks = 64;
 
-// Workspace: lse in powers of two (+inf for rows that see nothing, so that their weights are 0) and delta a query
-// and head, then the float32 parts of the sinks' gradients, { dk, dv } [sinks][dim] each.
+// Workspace: lse in powers of two (less kWeightShift in float16; +inf for rows that see nothing, so that their weights
+// are 0) and -delta a query and head, then the float32 parts of the sinks' gradients, { dk, dv } [sinks][dim] each.
 struct Work {
-    float *lse2, *delta;     // [q_heads][q_tokens]
+    float *lse2, *minus_delta;     // [q_heads][q_tokens]
     float *largest;          // [largest_parts] largest finite |dout| of each workgroup of row_statistics (float16 only)
     int largest_parts;
     float *near;             // [n_clips][kv_heads]
@@ -94,8 +94,8 @@ Work work_of(const AttentionArgs &a)
 {
     Work w;
     w.lse2 = static_cast<float *>(a.workspace);
-    w.delta = w.lse2 + rounded(a.q_tokens * a.q_heads);
-    w.largest = w.delta + rounded(a.q_tokens * a.q_heads);
+    w.minus_delta = w.lse2 + rounded(a.q_tokens * a.q_heads);
+    w.largest = w.minus_delta + rounded(a.q_tokens * a.q_heads);
     w.largest_parts = statistics_groups(a.q_tokens, a.q_heads, a.dim);
     w.near = w.largest + kStatisticsGroups;
     w.far = w.near + static_cast<int64_t>(a.n_clips) * a.kv_heads * a.sinks * a.dim * 2;
@@ -134,8 +134,8 @@ void row_statistics(AttentionArgs a, Work work)
         if (part == 0) {
             const int64_t to = head * a.q_tokens + row;
             const float lse = a.lse[to];
-            work.delta[to] = s;
-            work.lse2[to] = lse == -INFINITY ? INFINITY : lse * kLog2e;
+            work.minus_delta[to] = -s;
+            work.lse2[to] = lse == -INFINITY ? INFINITY : lse * kLog2e - (kNarrow<T> ? kWeightShift : 0.0f);
         }
         if constexpr (kNarrow<T>) {
 #pragma unroll
@@ -202,7 +202,7 @@ void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
     const int w_high = below_window(w_last, a.window);
     const int64_t at = q0 + min(row, nq - 1);
     float lse2 = work.lse2[head * a.q_tokens + at], unshift = 1.0f;
-    float delta = work.delta[head * a.q_tokens + at];
+    float minus_delta = work.minus_delta[head * a.q_tokens + at];
 
     vec8<T> q[kD / 16], g[kD / 16];
 #pragma unroll
@@ -210,15 +210,22 @@ void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
         q[t] = load8(static_cast<const T *>(a.q.data) + at * a.q.token + head * a.q.head + 16 * t + 8 * half);
         g[t] = load8(static_cast<const T *>(a.dout.data) + at * a.dout.token + head * a.dout.head + 16 * t + 8 * half);
     }
+#pragma unroll
+    for (int t = 0; t < kD / 16; ++t) {
+        arrive(q[t]);
+        arrive(g[t]);
+    }
+    arrive(lse2);
+    arrive(minus_delta);
     if constexpr (kNarrow<T>) {
         float top = 0.0f;
 #pragma unroll
         for (int t = 0; t < kD / 16; ++t)
 #pragma unroll
             for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(to_float(g[t][i])));
-        const float shift = kWeightShift - exponent_of(fmaxf(top, __shfl_xor(top, 32)));
-        lse2 -= shift;
-        unshift = fast_exp2(-shift);
+        const float e = static_cast<float>(exponent_of(fmaxf(top, __shfl_xor(top, 32))));
+        lse2 += e;
+        unshift = fast_exp2(e - kWeightShift);
     }
     const typename Rows::Loader load_k(a.k.token), load_v(a.v.token);
     const T *keys = static_cast<const T *>(a.k.data) + static_cast<int64_t>(k0) * a.k.token + kv * a.k.head;
@@ -257,7 +264,7 @@ void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
             }
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                y[r] = fast_exp2(__builtin_fmaf(x[r], factor, -lse2)) * (y[r] - delta);
+                y[r] = fast_exp2(__builtin_fmaf(x[r], factor, -lse2)) * (y[r] + minus_delta);
                 if (second && s_bad[32 * b + 8 * (r >> 2) + 4 * half + (r & 3)]) y[r] = __builtin_nanf("");
             }
             if (!whole) {
@@ -296,8 +303,8 @@ void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
     if (sizeof(T) == 2 && min(static_cast<int64_t>(a.window) + a.sinks, static_cast<int64_t>(min(i0 + kRows, nq) + back)) <= kFewKeys) {
         pass(Constant<2>{});
         lack += __shfl_xor(lack, 32);
-        delta += lack * unshift;
-        if (half == 0 && row < nq) work.delta[head * a.q_tokens + at] = delta;
+        minus_delta -= lack * unshift;
+        if (half == 0 && row < nq) work.minus_delta[head * a.q_tokens + at] = minus_delta;
         __syncthreads();     // the tiles are no longer read
     }
     pass(Constant<0>{});
@@ -329,7 +336,7 @@ void dkv_tiles(AttentionArgs a, Work work, float factor)
 {
     typedef Tile<T, kD, kWaves> Rows;
     __shared__ __attribute__((aligned(16))) char s_mem[4 * Rows::kBytes];
-    __shared__ __attribute__((aligned(16))) float s_stats[2][2][kTileRows];     // [buffer][lse2, delta][query]
+    __shared__ __attribute__((aligned(16))) float s_stats[2][2][kTileRows];     // [buffer][lse2, -delta][query]
     __shared__ int s_bad[kTileRows];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 31, half = lane >> 5;
@@ -375,7 +382,7 @@ void dkv_tiles(AttentionArgs a, Work work, float factor)
     hi_all = __builtin_amdgcn_readfirstlane(hi_all);     // the same in both halves of the wavefront
     hi_any = __builtin_amdgcn_readfirstlane(hi_any);
 
-    // float16: dw and delta times `small`, weights times 2^kWeightShift
+    // float16: dw - delta times `small`, weights times 2^kWeightShift
     float small = 1.0f, unit_k = 1.0f, unit_v = 1.0f;
     if constexpr (kNarrow<T>) {
         float top = 0.0f;
@@ -395,6 +402,11 @@ void dkv_tiles(AttentionArgs a, Work work, float factor)
             k[t] = load8(static_cast<const T *>(a.k.data) + row * a.k.token + kv * a.k.head + 16 * t + 8 * half);
             v[t] = load8(static_cast<const T *>(a.v.data) + row * a.v.token + kv * a.v.head + 16 * t + 8 * half);
         }
+#pragma unroll
+        for (int t = 0; t < kD / 16; ++t) {
+            arrive(k[t]);
+            arrive(v[t]);
+        }
     }
     const typename Rows::Loader load_q(a.q.token), load_g(a.dout.token);
     auto load = [&](int buffer, int head, int i) {
@@ -403,7 +415,7 @@ void dkv_tiles(AttentionArgs a, Work work, float factor)
         load_g.load(s + Rows::kBytes, static_cast<const T *>(a.dout.data) + static_cast<int64_t>(q0) * a.dout.token + head * a.dout.head,
                     i, nq);
         if (wave < 2)
-            copy4((wave ? work.delta : work.lse2) + head * a.q_tokens + q0 + i, 4 * min(lane, nq - 1 - i), s_stats[buffer][wave]);
+            copy4((wave ? work.minus_delta : work.lse2) + head * a.q_tokens + q0 + i, 4 * min(lane, nq - 1 - i), s_stats[buffer][wave]);
     };
 
     f32x16 dk[kD / 32], dv[kD / 32];
@@ -426,29 +438,26 @@ void dkv_tiles(AttentionArgs a, Work work, float factor)
             const int p0 = i_tile + 32 * b + back;       // position of the first of these 32 queries
             if (p0 + 31 < key_first || p0 >= hi_any) continue;
             if (kFar && (b != (wave & 1) || p0 + 31 < i_first + back)) continue;
-            f32x16 x = {}, y = {};
+            f32x16 x = {}, y;
+            f32x4 lse2[4];
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                const int in = 32 * b + 8 * f + 4 * half;
+                lse2[f] = *reinterpret_cast<const f32x4 *>(&s_stats[buffer.value][0][in]);
+                const f32x4 minus_delta = *reinterpret_cast<const f32x4 *>(&s_stats[buffer.value][1][in]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[4 * f + e] = minus_delta[e];     // dw - delta comes out of the product
+            }
 #pragma unroll
             for (int n = 0; n < kD / 16; ++n) {
                 x = mma32(Rows::along(s_q, 32 * b + c, 2 * n + half), k[n], x);
                 y = mma32(Rows::along(s_g, 32 * b + c, 2 * n + half), v[n], y);
             }
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
-                const int in = 32 * b + 8 * f + 4 * half;
-                const f32x4 lse2 = *reinterpret_cast<const f32x4 *>(&s_stats[buffer.value][0][in]);
-                const f32x4 delta = *reinterpret_cast<const f32x4 *>(&s_stats[buffer.value][1][in]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int r = 4 * f + e;
-                    if constexpr (kNarrow<T>) {
-                        x[r] = fast_exp2(__builtin_fmaf(x[r], factor, kWeightShift - lse2[e]));
-                        y[r] = x[r] * __builtin_fmaf(y[r], small, -small * delta[e]);
-                    } else {
-                        x[r] = fast_exp2(__builtin_fmaf(x[r], factor, -lse2[e]));
-                        y[r] = x[r] * (y[r] - delta[e]);
-                    }
-                    if (second.value && s_bad[in + e]) x[r] = y[r] = __builtin_nanf("");
-                }
+            for (int r = 0; r < 16; ++r) {
+                x[r] = fast_exp2(__builtin_fmaf(x[r], factor, -lse2[r >> 2][r & 3]));
+                y[r] = x[r] * (kNarrow<T> ? y[r] * small : y[r]);
+                if (second.value && s_bad[32 * b + 8 * (r >> 2) + 4 * half + (r & 3)]) x[r] = y[r] = __builtin_nanf("");
             }
             if (kFar || !(p0 >= key_last && p0 + 31 < hi_all)) {
 #pragma unroll

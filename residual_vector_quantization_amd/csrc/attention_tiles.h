@@ -50,6 +50,13 @@ __device__ inline void copy4(const void *src, uint32_t offset, void *dst)
     const unsigned m0 = static_cast<unsigned>(reinterpret_cast<size_t>((lds_void *)dst));
     asm volatile("s_nop 4\n\tglobal_load_lds_dword %0, %1" ::"v"(offset), "s"(src), "{m0}"(m0) : "memory");
 }
+// Makes the compiler wait for a loaded operand here. Otherwise it waits where a loop first uses it, in every turn, and
+// its count of outstanding loads, which knows nothing of the copies above, then waits for those as well.
+template <typename V>
+__device__ inline void arrive(V &x)
+{
+    asm volatile("" : "+v"(x));
+}
 __device__ inline void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // The 64-key tiles that the queries at positions p_first .. p_last see some of: the sinks', then the window's.
