@@ -4,8 +4,8 @@
 //   dw_ij = dout_i . v_j,  dx_ij = w_ij (dw_ij - delta_i)
 //   dq_i = scale sum_j dx_ij k_j,  dk_j = scale sum_i dx_ij q_i,  dv_j = sum_i w_ij dout_i
 //
-// Three launches and no atomics, so the sums' order is fixed: row statistics,
-// dq (queries in registers, keys go by), dk and dv (keys in registers, queries
+// Two launches and no atomics, so the sums' order is fixed: dq and the rows'
+// delta (queries in registers, keys go by), dk and dv (keys in registers, queries
 // go by, all query heads of a key head one after another). Scores and dw are
 // made twice, 14 dim flops a pair with the forward pass' 4 make 18 where 14
 // would do; in exchange no partial dq goes through memory.
@@ -29,7 +29,7 @@
 // The first sinks of a clip are seen by all of its later queries, hundreds of
 // tiles where other keys have a window's. When that matters (see split_sinks)
 // the queries beyond the window go in pieces of kFarRows to workgroups of their
-// own, and a last launch adds the float32 parts in order.
+// own, and a third launch adds the float32 parts in order.
 #include <float.h>
 #include <limits.h>
 #include <stdint.h>
@@ -55,7 +55,7 @@ constexpr int kMaxSplitSinks = 64;
 // are 0) and -delta a query and head, then the float32 parts of the sinks' gradients, { dk, dv } [sinks][dim] each.
 struct Work {
     float *lse2, *minus_delta;     // [q_heads][q_tokens]
-    float *largest;          // [largest_parts] largest finite |dout| of each workgroup of row_statistics (float16 only)
+    float *largest;          // [largest_parts] largest finite |dout| of each workgroup of dq_tiles (float16 only)
     int largest_parts;
     float *near;             // [n_clips][kv_heads]
     float *far;              // [far slots][kv_heads][2]
@@ -73,18 +73,11 @@ bool split_sinks(int64_t q_tokens, int n_clips, int sinks)
     return sinks > 0 && sinks <= kMaxSplitSinks && q_tokens >= static_cast<int64_t>(n_clips) * kLongClip;
 }
 
-// Workgroups of row_statistics: they go over the rows in turn, so that there are at most kStatisticsGroups maxima.
-constexpr int kStatisticsGroups = 2048;
-
-int statistics_groups(int64_t q_tokens, int q_heads, int dim)
-{
-    const int64_t n = (q_tokens * q_heads * (dim / 8) + kThreads - 1) / kThreads;
-    return static_cast<int>(n < kStatisticsGroups ? n : kStatisticsGroups);
-}
+int64_t q_slots(int64_t q_tokens, int n_clips) { return q_tokens / kRows + n_clips + 1; }
 
 int64_t work_floats(int64_t q_tokens, int n_clips, int q_heads, int kv_heads, int dim, int sinks)
 {
-    int64_t n = 2 * rounded(q_tokens * q_heads) + kStatisticsGroups;
+    int64_t n = 2 * rounded(q_tokens * q_heads) + rounded(q_slots(q_tokens, n_clips) * q_heads);
     if (split_sinks(q_tokens, n_clips, sinks))
         n += (n_clips + 2 * far_slots(q_tokens, n_clips)) * kv_heads * sinks * dim * 2;
     return n;
@@ -96,8 +89,9 @@ Work work_of(const AttentionArgs &a)
     w.lse2 = static_cast<float *>(a.workspace);
     w.minus_delta = w.lse2 + rounded(a.q_tokens * a.q_heads);
     w.largest = w.minus_delta + rounded(a.q_tokens * a.q_heads);
-    w.largest_parts = statistics_groups(a.q_tokens, a.q_heads, a.dim);
-    w.near = w.largest + kStatisticsGroups;
+    const int64_t parts = q_slots(a.q_tokens, a.n_clips) * a.q_heads;
+    w.largest_parts = a.q_tokens > 0 ? static_cast<int>(parts) : 0;
+    w.near = w.largest + rounded(parts);
     w.far = w.near + static_cast<int64_t>(a.n_clips) * a.kv_heads * a.sinks * a.dim * 2;
     w.split = a.window != INT_MAX && split_sinks(a.q_tokens, a.n_clips, a.sinks);
     return w;
@@ -111,49 +105,6 @@ __device__ inline bool not_finite(float x) { return !(fabsf(x) <= FLT_MAX); }
 
 // e with 2^(e - 1) <= x < 2^e, 0 for x = 0 and values that are not finite.
 __device__ inline int exponent_of(float x) { return x == 0.0f || not_finite(x) ? 0 : __builtin_amdgcn_frexp_expf(x); }
-
-// lse2 and delta; kD / 8 lanes a row. Bound by HBM (out and dout once).
-template <typename T, int kD>
-__global__ __launch_bounds__(kThreads)
-void row_statistics(AttentionArgs a, Work work)
-{
-    constexpr int kLanes = kD / 8;
-    const int part = threadIdx.x % kLanes;
-    float top = 0.0f;
-    for (int64_t at = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / kLanes; at < a.q_tokens * a.q_heads;
-         at += static_cast<int64_t>(gridDim.x) * (kThreads / kLanes)) {
-        const int64_t row = at / a.q_heads;
-        const int head = static_cast<int>(at - row * a.q_heads);
-        const vec8<T> g = load8(static_cast<const T *>(a.dout.data) + row * a.dout.token + head * a.dout.head + 8 * part);
-        const vec8<T> o = load8(static_cast<const T *>(a.out.data) + row * a.out.token + head * a.out.head + 8 * part);
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s += to_float(g[i]) * to_float(o[i]);
-#pragma unroll
-        for (int m = kLanes / 2; m > 0; m >>= 1) s += __shfl_xor(s, m);
-        if (part == 0) {
-            const int64_t to = head * a.q_tokens + row;
-            const float lse = a.lse[to];
-            work.minus_delta[to] = -s;
-            work.lse2[to] = lse == -INFINITY ? INFINITY : lse * kLog2e - (kNarrow<T> ? kWeightShift : 0.0f);
-        }
-        if constexpr (kNarrow<T>) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, not_finite(to_float(g[i])) ? 0.0f : fabsf(to_float(g[i])));
-        }
-    }
-    if constexpr (kNarrow<T>) {
-        __shared__ float s_top[kWaves];
-#pragma unroll
-        for (int m = 32; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
-        if ((threadIdx.x & 63) == 0) s_top[threadIdx.x >> 6] = top;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            for (int w = 1; w < kWaves; ++w) top = fmaxf(top, s_top[w]);
-            work.largest[blockIdx.x] = top;
-        }
-    }
-}
 
 // Rows of a tile with a value that is not finite: their flag is set and they become zeros. Barriers are the caller's.
 template <typename T, int kD>
@@ -172,11 +123,11 @@ __device__ inline void clear_bad_rows(char *s, int *flags)
     }
 }
 
-// dq. As in the forward pass a workgroup takes 128 queries and goes over the tiles of keys they see. If a result is
+// dq, and lse2 and delta of the rows. As in the forward pass a workgroup takes 128 queries and goes over the tiles of keys they see. If a result is
 // not finite, a second pass takes rows of K that are not finite as zeros and the weights of the queries that do see
 // them as NaN, so that only those get it.
 template <typename T, int kD>
-__global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? (kD == 64 ? 3 : 2) : 1)
 void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
 {
     typedef Tile<T, kD, kWaves> Rows;
@@ -191,7 +142,10 @@ void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
     clip_range(a.cu_q, clip, a.q_tokens, q0, nq);
     clip_range(a.cu_k, clip, a.k_tokens, k0, nk);
     const int i0 = (slot - (a.cu_q[clip] / kRows + clip)) * kRows;
-    if (i0 < 0 || i0 >= nq) return;
+    if (i0 < 0 || i0 >= nq) {
+        if (kNarrow<T> && threadIdx.x == 0) work.largest[blockIdx.x] = 0.0f;
+        return;
+    }
 
     const int back = nk - nq;
     const int row = i0 + 32 * wave + c;
@@ -201,31 +155,47 @@ void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
     const int p_low = below_window(p, a.window), w_low = below_window(w_first, a.window);
     const int w_high = below_window(w_last, a.window);
     const int64_t at = q0 + min(row, nq - 1);
-    float lse2 = work.lse2[head * a.q_tokens + at], unshift = 1.0f;
-    float minus_delta = work.minus_delta[head * a.q_tokens + at];
 
     vec8<T> q[kD / 16], g[kD / 16];
+    float lse2 = a.lse[head * a.q_tokens + at], minus_delta = 0.0f, unshift = 1.0f;
+    lse2 = lse2 == -INFINITY ? INFINITY : lse2 * kLog2e - (kNarrow<T> ? kWeightShift : 0.0f);
+    {
+        vec8<T> o[kD / 16];
 #pragma unroll
-    for (int t = 0; t < kD / 16; ++t) {
-        q[t] = load8(static_cast<const T *>(a.q.data) + at * a.q.token + head * a.q.head + 16 * t + 8 * half);
-        g[t] = load8(static_cast<const T *>(a.dout.data) + at * a.dout.token + head * a.dout.head + 16 * t + 8 * half);
-    }
+        for (int t = 0; t < kD / 16; ++t) {
+            q[t] = load8(static_cast<const T *>(a.q.data) + at * a.q.token + head * a.q.head + 16 * t + 8 * half);
+            g[t] = load8(static_cast<const T *>(a.dout.data) + at * a.dout.token + head * a.dout.head + 16 * t + 8 * half);
+            o[t] = load8(static_cast<const T *>(a.out.data) + at * a.out.token + head * a.out.head + 16 * t + 8 * half);
+        }
 #pragma unroll
-    for (int t = 0; t < kD / 16; ++t) {
-        arrive(q[t]);
-        arrive(g[t]);
+        for (int t = 0; t < kD / 16; ++t) {
+            arrive(q[t]);
+            arrive(g[t]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) minus_delta -= to_float(g[t][i]) * to_float(o[t][i]);
+        }
     }
-    arrive(lse2);
-    arrive(minus_delta);
+    minus_delta += __shfl_xor(minus_delta, 32);
+    if (half == 0 && row < nq) work.lse2[head * a.q_tokens + at] = lse2;
     if constexpr (kNarrow<T>) {
-        float top = 0.0f;
+        __shared__ float s_top[kWaves];
+        float top = 0.0f, finite = 0.0f;
 #pragma unroll
         for (int t = 0; t < kD / 16; ++t)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(to_float(g[t][i])));
+            for (int i = 0; i < 8; ++i) {
+                const float x = fabsf(to_float(g[t][i]));
+                top = fmaxf(top, x);
+                finite = fmaxf(finite, not_finite(x) ? 0.0f : x);
+            }
         const float e = static_cast<float>(exponent_of(fmaxf(top, __shfl_xor(top, 32))));
         lse2 += e;
         unshift = fast_exp2(e - kWeightShift);
+#pragma unroll
+        for (int m = 32; m > 0; m >>= 1) finite = fmaxf(finite, __shfl_xor(finite, m));
+        s_top[wave] = finite;
+        __syncthreads();
+        if (threadIdx.x == 0) work.largest[blockIdx.x] = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
     }
     const typename Rows::Loader load_k(a.k.token), load_v(a.v.token);
     const T *keys = static_cast<const T *>(a.k.data) + static_cast<int64_t>(k0) * a.k.token + kv * a.k.head;
@@ -304,9 +274,9 @@ void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
         pass(Constant<2>{});
         lack += __shfl_xor(lack, 32);
         minus_delta -= lack * unshift;
-        if (half == 0 && row < nq) work.minus_delta[head * a.q_tokens + at] = minus_delta;
         __syncthreads();     // the tiles are no longer read
     }
+    if (half == 0 && row < nq) work.minus_delta[head * a.q_tokens + at] = minus_delta;
     pass(Constant<0>{});
     bool odd = false;
 #pragma unroll
@@ -331,16 +301,13 @@ void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
 // query head after another. kFar: the sinks with the queries beyond the first keys' window, kFarRows of them; the
 // wavefronts share the sinks (32 each) and take half of a tile's queries each.
 template <typename T, int kD, bool kFar>
-__global__ __launch_bounds__(kThreads, sizeof(T) == 2 && kD == 64 ? 2 : 1)
-void dkv_tiles(AttentionArgs a, Work work, float factor)
+__device__ inline void dkv_group(const AttentionArgs &a, const Work &work, float factor, int block, char *s_mem,
+                                 float (&s_stats)[2][2][kTileRows], int *s_bad)
 {
     typedef Tile<T, kD, kWaves> Rows;
-    __shared__ __attribute__((aligned(16))) char s_mem[4 * Rows::kBytes];
-    __shared__ __attribute__((aligned(16))) float s_stats[2][2][kTileRows];     // [buffer][lse2, -delta][query]
-    __shared__ int s_bad[kTileRows];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 31, half = lane >> 5;
-    const int slot = blockIdx.x / a.kv_heads, kv = blockIdx.x % a.kv_heads, group = a.q_heads / a.kv_heads;
+    const int slot = block / a.kv_heads, kv = block % a.kv_heads, group = a.q_heads / a.kv_heads;
     const int32_t *cu = kFar ? a.cu_q : a.cu_k;
     constexpr int kPer = kFar ? kFarRows : kRows;
     const int clip = clip_of_slot(cu, a.n_clips, slot, kPer);
@@ -394,19 +361,22 @@ void dkv_tiles(AttentionArgs a, Work work, float factor)
         unit_v = fast_exp2(-kWeightShift);
         unit_k = fast_exp2(static_cast<float>(e) - kWeightShift);
     }
-    vec8<T> k[kD / 16], v[kD / 16];
-    {
-        const int64_t row = k0 + min(key, nk - 1);
+    // The keys' and values' operands stay in registers. Float32 rows of 128 take 128 registers each way, beside as many
+    // of accumulators: there the values come from the caches in every tile (the compiler would else put some of the
+    // operands into scratch memory and fetch them from there).
+    constexpr bool kKeep = sizeof(T) == 2 || kD == 64;
+    vec8<T> k[kD / 16], v[kKeep ? kD / 16 : 1];
+    const int64_t own = k0 + min(key, nk - 1);
+    const T *own_v = static_cast<const T *>(a.v.data) + own * a.v.token + kv * a.v.head + 8 * half;
 #pragma unroll
-        for (int t = 0; t < kD / 16; ++t) {
-            k[t] = load8(static_cast<const T *>(a.k.data) + row * a.k.token + kv * a.k.head + 16 * t + 8 * half);
-            v[t] = load8(static_cast<const T *>(a.v.data) + row * a.v.token + kv * a.v.head + 16 * t + 8 * half);
-        }
+    for (int t = 0; t < kD / 16; ++t) {
+        k[t] = load8(static_cast<const T *>(a.k.data) + own * a.k.token + kv * a.k.head + 16 * t + 8 * half);
+        if constexpr (kKeep) v[t] = load8(own_v + 16 * t);
+    }
 #pragma unroll
-        for (int t = 0; t < kD / 16; ++t) {
-            arrive(k[t]);
-            arrive(v[t]);
-        }
+    for (int t = 0; t < kD / 16; ++t) {
+        arrive(k[t]);
+        if constexpr (kKeep) arrive(v[t]);
     }
     const typename Rows::Loader load_q(a.q.token), load_g(a.dout.token);
     auto load = [&](int buffer, int head, int i) {
@@ -451,7 +421,8 @@ void dkv_tiles(AttentionArgs a, Work work, float factor)
 #pragma unroll
             for (int n = 0; n < kD / 16; ++n) {
                 x = mma32(Rows::along(s_q, 32 * b + c, 2 * n + half), k[n], x);
-                y = mma32(Rows::along(s_g, 32 * b + c, 2 * n + half), v[n], y);
+                if constexpr (kKeep) y = mma32(Rows::along(s_g, 32 * b + c, 2 * n + half), v[n], y);
+                else y = mma32(Rows::along(s_g, 32 * b + c, 2 * n + half), load8(own_v + 16 * n), y);
             }
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
@@ -544,6 +515,19 @@ void dkv_tiles(AttentionArgs a, Work work, float factor)
         }
 }
 
+// The pieces of queries beyond the window come last: they are shorter than the others and fill up their last round.
+template <typename T, int kD>
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 && kD == 64 ? 2 : 1)
+void dkv_tiles(AttentionArgs a, Work work, float factor, int near_groups)
+{
+    __shared__ __attribute__((aligned(16))) char s_mem[4 * Tile<T, kD, kWaves>::kBytes];
+    __shared__ __attribute__((aligned(16))) float s_stats[2][2][kTileRows];     // [buffer][lse2, -delta][query]
+    __shared__ int s_bad[kTileRows];
+    const int block = blockIdx.x;
+    if (block < near_groups) dkv_group<T, kD, false>(a, work, factor, block, s_mem, s_stats, s_bad);
+    else dkv_group<T, kD, true>(a, work, factor, block - near_groups, s_mem, s_stats, s_bad);
+}
+
 // The sinks' gradients: the part within the first keys' window, then the pieces beyond it in order.
 template <typename T, int kD>
 __global__ __launch_bounds__(2 * kD)
@@ -557,7 +541,8 @@ void join_sinks(AttentionArgs a, Work work)
         if (key >= nk) continue;
         float sum = work.near[((static_cast<int64_t>(clip) * a.kv_heads + kv) * a.sinks + key) * 2 * kD + d];
         const int64_t base = q0 / kFarRows + clip;
-        for (int piece = 0; piece * static_cast<int64_t>(kFarRows) < nq; ++piece)
+#pragma unroll 8
+        for (int piece = 0; piece < (nq + kFarRows - 1) / kFarRows; ++piece)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 sum += work.far[((((base + piece) * a.kv_heads + kv) * 2 + h) * a.sinks + key) * 2 * kD + d];
@@ -574,18 +559,16 @@ hipError_t backward(const AttentionArgs &a, hipStream_t stream)
 {
     const Work work = work_of(a);
     const float factor = fmaxf(a.scale * kLog2e, FLT_MIN);     // as in the forward pass
-    const int64_t q_slots = a.q_tokens / kRows + a.n_clips + 1, k_slots = a.k_tokens / kRows + a.n_clips + 1;
-    if (q_slots * a.q_heads > INT_MAX || k_slots * a.kv_heads > INT_MAX)
-        return hipErrorInvalidConfiguration;
-    if (a.q_tokens > 0) {
-        row_statistics<T, kD><<<work.largest_parts, kThreads, 0, stream>>>(a, work);
-        dq_tiles<T, kD><<<static_cast<unsigned>(q_slots * a.q_heads), kThreads, 0, stream>>>(a, work, factor, static_cast<int>(q_slots));
-    }
+    const int64_t q_groups = q_slots(a.q_tokens, a.n_clips) * a.q_heads;
+    const int64_t far_groups = work.split ? far_slots(a.q_tokens, a.n_clips) * a.kv_heads : 0;
+    const int64_t near_groups = (a.k_tokens / kRows + a.n_clips + 1) * a.kv_heads;
+    if (q_groups > INT_MAX || near_groups + far_groups > INT_MAX) return hipErrorInvalidConfiguration;
+    if (a.q_tokens > 0)
+        dq_tiles<T, kD><<<static_cast<unsigned>(q_groups), kThreads, 0, stream>>>(
+            a, work, factor, static_cast<int>(q_slots(a.q_tokens, a.n_clips)));
     if (a.k_tokens > 0) {
-        if (work.split)
-            dkv_tiles<T, kD, true><<<static_cast<unsigned>(far_slots(a.q_tokens, a.n_clips) * a.kv_heads), kThreads, 0, stream>>>(
-                a, work, factor);
-        dkv_tiles<T, kD, false><<<static_cast<unsigned>(k_slots * a.kv_heads), kThreads, 0, stream>>>(a, work, factor);
+        dkv_tiles<T, kD><<<static_cast<unsigned>(near_groups + far_groups), kThreads, 0, stream>>>(
+            a, work, factor, static_cast<int>(near_groups));
         if (work.split)
             join_sinks<T, kD><<<dim3(a.sinks, a.kv_heads, a.n_clips < 1024 ? a.n_clips : 1024), 2 * kD, 0, stream>>>(a, work);
     }
