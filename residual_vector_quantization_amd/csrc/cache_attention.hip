@@ -17,9 +17,11 @@
 // A wavefront takes tiles of 32 seen frames; its running maximum moves only
 // when a score exceeds it by more than 2^8, so most tiles need neither an
 // exchange between lanes nor a rescale (weights stay below 2^8, sums are
-// float32). A clip's frames are split over workgroups when clips and heads
-// alone do not fill the chip; each split leaves its maximum, sum and
-// accumulator in the workspace and a second launch joins them in order.
+// float32). When clips and heads alone do not fill the chip, a clip's frames go
+// to 8 wavefronts of a workgroup instead of 4, and where that leaves each more
+// than kManyTiles tiles they are split over workgroups: each split leaves its
+// maximum, sum and accumulator in the workspace and a second launch joins them
+// in order.
 #include <float.h>
 #include <limits.h>
 #include <stdint.h>
@@ -34,17 +36,21 @@
 namespace rvq {
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 4;            // wavefronts of a workgroup; kWideWaves in a few workgroups with few frames
+constexpr int kWideWaves = 8;
+constexpr int kManyTiles = 2;
 constexpr int kTile = 32;            // frames a wavefront takes at a time
 constexpr int kQueries = 16;         // columns of the products
 constexpr float kSlack = 8.0f;       // how far (powers of two) a score may exceed the running maximum
 constexpr int kWantedGroups = 2048;  // workgroups that fill the chip evenly (8 a CU)
 constexpr int kMaxSplits = 256;
+constexpr int kCus = 256;
 
 struct Params {
     CacheAttentionArgs a;
     Divisor page;
     int group, chunks, splits;       // query heads a key head, 16-wide chunks of them, splits of a clip's frames
+    bool wide;                       // kWideWaves wavefronts a workgroup
     float factor;                    // scale in powers of two
 };
 
@@ -91,7 +97,7 @@ __device__ inline float over_groups_sum(float x)
     return x + __shfl_xor(x, 32);
 }
 
-template <typename T, int kD>
+template <typename T, int kD, int kWaves>
 __global__ __launch_bounds__(64 * kWaves)
 void newest_frame(Params p, Partials part)
 {
@@ -287,7 +293,8 @@ int splits_for(int n_clips, int kv_heads, int group, int64_t capacity)
     const int64_t base = static_cast<int64_t>(n_clips) * kv_heads * ((group + kQueries - 1) / kQueries);
     const int64_t tiles = (capacity + kTile - 1) / kTile;
     int64_t n = base > 0 ? kWantedGroups / base : 1;
-    const int64_t most = tiles / kWaves;
+    // the second launch costs about 3 us, as much as a tile of a wavefront that nothing hides
+    const int64_t most = tiles <= kWideWaves * kManyTiles ? 1 : tiles / kWaves;
     if (n > most) n = most;
     if (n > kMaxSplits) n = kMaxSplits;
     return n < 1 ? 1 : static_cast<int>(n);
@@ -306,7 +313,8 @@ hipError_t run(const Params &p, hipStream_t stream)
     }
     const int64_t groups = static_cast<int64_t>(a.n_clips) * p.splits * a.kv_heads * p.chunks;
     if (groups > INT_MAX) return hipErrorInvalidConfiguration;
-    newest_frame<T, kD><<<static_cast<unsigned>(groups), 64 * kWaves, 0, stream>>>(p, part);
+    if (p.wide) newest_frame<T, kD, kWideWaves><<<static_cast<unsigned>(groups), 64 * kWideWaves, 0, stream>>>(p, part);
+    else newest_frame<T, kD, kWaves><<<static_cast<unsigned>(groups), 64 * kWaves, 0, stream>>>(p, part);
     if (p.splits > 1) join_splits<T, kD><<<dim3(a.n_clips, a.q_heads), 64, 0, stream>>>(p, part);
     return hipGetLastError();
 }
@@ -331,7 +339,9 @@ hipError_t launch_cache_attention(const CacheAttentionArgs &a, hipStream_t strea
     // no more frames than the window and the sinks hold; the workspace is sized for the table's capacity
     const int64_t capacity = static_cast<int64_t>(a.table_ld) * a.page_size;
     const int64_t seen = static_cast<int64_t>(a.window) + a.sinks;
-    p.splits = splits_for(a.n_clips, a.kv_heads, p.group, seen < capacity ? seen : capacity);
+    const int64_t frames = seen < capacity ? seen : capacity;
+    p.splits = splits_for(a.n_clips, a.kv_heads, p.group, frames);
+    p.wide = p.splits == 1 && frames > kWaves * kTile && static_cast<int64_t>(a.n_clips) * a.kv_heads * p.chunks <= kCus;
     p.factor = fmaxf(a.scale * kLog2e, FLT_MIN);   // scale 0: equal weights, and 0 times -inf does not arise
     if (a.dtype == RVQ_F32) return a.dim == 64 ? run<float, 64>(p, stream) : run<float, 128>(p, stream);
     if (a.dtype == RVQ_F16) return a.dim == 64 ? run<f16_t, 64>(p, stream) : run<f16_t, 128>(p, stream);

@@ -25,6 +25,7 @@ constexpr int kThreads = 256;
 constexpr int kPerThread = 8;
 constexpr int kChunk = kThreads * kPerThread;      // pages a ranking workgroup
 constexpr int kCopyBlocks = 2048;                  // workgroups that copy pages (8 a CU)
+constexpr int kSoonRead = 2048;                    // table entries up to which a free takes one launch (8 a thread: 4 us)
 constexpr int kSelfCounted = 1 << 16;              // pages (and clips) up to which a workgroup counts for itself
 
 int64_t chunks(int n) { return (static_cast<int64_t>(n) + kChunk - 1) / kChunk; }
@@ -358,22 +359,64 @@ void copy_ints(const int32_t *__restrict__ from, int32_t *__restrict__ to, int64
     if (i < n) to[i] = from[i];
 }
 
+// Whether entry e of clip b leaves the table in a free.
+struct Leaves {
+    const int32_t *lens, *drop;
+    int page_size, sinks;
+    int64_t window;
+
+    __device__ bool operator()(int b, int e) const
+    {
+        if (drop && drop[b]) return true;
+        // the next frame stands at position lens[b] and sees the positions above lens[b] - window
+        const int64_t low = static_cast<int64_t>(e) * page_size;
+        return window >= 0 && low >= sinks && low + page_size <= static_cast<int64_t>(lens[b]) - window + 1;
+    }
+};
+
+// free in one launch, for tables that are soon read: workgroups 0 .. n_chunks - 1 go over the whole table and count in
+// the LDS what leaves of their chunk's pages, those that are left write the table and the lengths.
+__global__ __launch_bounds__(kThreads)
+void free_small(const int32_t *__restrict__ table, const int32_t *__restrict__ refs, int n_clips, int table_ld,
+                int n_pages, int n_chunks, Leaves leaves, int32_t *__restrict__ table_out,
+                int32_t *__restrict__ lens_out, int32_t *__restrict__ refs_out)
+{
+    __shared__ int s_gone[kChunk];
+    const int entries = n_clips * table_ld;
+    if (static_cast<int>(blockIdx.x) >= n_chunks) {
+        const int at = (static_cast<int>(blockIdx.x) - n_chunks) * kThreads + threadIdx.x;
+        if (at < n_clips) lens_out[at] = leaves.drop && leaves.drop[at] ? 0 : leaves.lens[at];
+        if (at >= entries) return;
+        const int b = at / table_ld;
+        table_out[at] = leaves(b, at - b * table_ld) ? -1 : table[at];
+        return;
+    }
+    const int first = blockIdx.x * kChunk;
+    for (int i = threadIdx.x; i < kChunk; i += kThreads) s_gone[i] = 0;
+    __syncthreads();
+#pragma unroll 4
+    for (int at = threadIdx.x; at < entries; at += kThreads) {
+        const uint32_t page = static_cast<uint32_t>(table[at]) - static_cast<uint32_t>(first);
+        if (page < static_cast<uint32_t>(kChunk)) {
+            const int b = at / table_ld;
+            if (leaves(b, at - b * table_ld)) atomicAdd(&s_gone[page], 1);
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < kChunk && first + i < n_pages; i += kThreads) refs_out[first + i] = refs[first + i] - s_gone[i];
+}
+
 // free: what leaves the table, reference counts go down.
 __global__ __launch_bounds__(kThreads)
-void free_entries(const int32_t *__restrict__ table, const int32_t *__restrict__ lens,
-                  const int32_t *__restrict__ drop, int n_clips, int table_ld, int page_size, int n_pages,
-                  int64_t window, int sinks, int32_t *__restrict__ table_out, int32_t *__restrict__ lens_out,
-                  int32_t *__restrict__ refs_out)
+void free_entries(const int32_t *__restrict__ table, int n_clips, int table_ld, int n_pages, Leaves leaves,
+                  int32_t *__restrict__ table_out, int32_t *__restrict__ lens_out, int32_t *__restrict__ refs_out)
 {
     const int64_t at = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    if (at < n_clips) lens_out[at] = drop && drop[at] ? 0 : lens[at];
+    if (at < n_clips) lens_out[at] = leaves.drop && leaves.drop[at] ? 0 : leaves.lens[at];
     if (at >= static_cast<int64_t>(n_clips) * table_ld) return;
     const int b = static_cast<int>(at / table_ld), e = static_cast<int>(at - static_cast<int64_t>(b) * table_ld);
-    const int64_t low = static_cast<int64_t>(e) * page_size;
     int page = table[at];
-    // the next frame stands at position lens[b] and sees the positions above lens[b] - window
-    const bool behind = window >= 0 && low >= sinks && low + page_size <= static_cast<int64_t>(lens[b]) - window + 1;
-    if ((drop && drop[b]) || behind) {
+    if (leaves(b, e)) {
         if (static_cast<unsigned>(page) < static_cast<unsigned>(n_pages)) atomicSub(&refs_out[page], 1);
         page = -1;
     }
@@ -564,12 +607,20 @@ hipError_t launch_cache_free(const int32_t *table, const int32_t *lens, const in
                              int n_clips, int table_ld, int page_size, int n_pages, int64_t window, int sinks,
                              int32_t *table_out, int32_t *lens_out, int32_t *refs_out, hipStream_t stream)
 {
+    const Leaves leaves = {lens, drop, page_size, sinks, window};
+    const int64_t entries = static_cast<int64_t>(n_clips) * table_ld, items = entries > n_clips ? entries : n_clips;
+    const int64_t n_chunks = chunks(n_pages);
+    if (entries <= kSoonRead && n_pages <= kSelfCounted) {
+        const int64_t groups = n_chunks + ceil_div(items, kThreads);
+        if (groups)
+            free_small<<<static_cast<unsigned>(groups), kThreads, 0, stream>>>(table, refs, n_clips, table_ld, n_pages,
+                                                                               static_cast<int>(n_chunks), leaves,
+                                                                               table_out, lens_out, refs_out);
+        return hipGetLastError();
+    }
     if (n_pages > 0) copy_ints<<<ceil_div(n_pages, kThreads), kThreads, 0, stream>>>(refs, refs_out, n_pages);
-    const int64_t entries = static_cast<int64_t>(n_clips) * (table_ld > 0 ? table_ld : 1);
-    if (entries)
-        free_entries<<<ceil_div(entries, kThreads), kThreads, 0, stream>>>(table, lens, drop, n_clips, table_ld,
-                                                                           page_size, n_pages, window, sinks,
-                                                                           table_out, lens_out, refs_out);
+    free_entries<<<ceil_div(items, kThreads), kThreads, 0, stream>>>(table, n_clips, table_ld, n_pages, leaves, table_out,
+                                                                     lens_out, refs_out);
     return hipGetLastError();
 }
 
