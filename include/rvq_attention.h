@@ -19,7 +19,8 @@
  * log-sum-exp -inf and gradient 0; so has a frame whose scores are all -inf.
  *
  * Arithmetic. Products run on the matrix cores in the inputs' type with
- * float32 accumulation (float32 inputs: float32 products); scores, softmax
+ * float32 accumulation (float32 inputs: as three bfloat16 parts a value, six
+ * products, or as float32, either way as exact as float32); scores, softmax
  * statistics and accumulators are float32. Attention weights and score
  * gradients are rounded once to the inputs' type where they enter a matrix
  * product of it, outputs once at the end. No sum's order depends on timing:

@@ -63,14 +63,12 @@ void forward_tiles(AttentionArgs a, float factor, int slots)
     const int p_low = below_window(p, a.window), w_low = below_window(w_first, a.window);
     const int w_high = below_window(w_last, a.window);
 
-    vec8<T> q[kD / 16];
-    {
-        const T *at = static_cast<const T *>(a.q.data) + static_cast<int64_t>(q0 + min(row, nq - 1)) * a.q.token + head * a.q.head;
+    const T *own = static_cast<const T *>(a.q.data) + static_cast<int64_t>(q0 + min(row, nq - 1)) * a.q.token + head * a.q.head;
+    Operand<T> q[kD / 16];
 #pragma unroll
-        for (int t = 0; t < kD / 16; ++t) q[t] = load8(at + 16 * t + 8 * half);
+    for (int t = 0; t < kD / 16; ++t) q[t] = Operand<T>(load8(own + 16 * t + 8 * half));
 #pragma unroll
-        for (int t = 0; t < kD / 16; ++t) arrive(q[t]);
-    }
+    for (int t = 0; t < kD / 16; ++t) arrive(q[t]);
     const typename Rows::Loader load_k(a.k.token), load_v(a.v.token);
     const T *keys = static_cast<const T *>(a.k.data) + static_cast<int64_t>(k0) * a.k.token + kv * a.k.head;
     const T *values = static_cast<const T *>(a.v.data) + static_cast<int64_t>(k0) * a.v.token + kv * a.v.head;
@@ -79,8 +77,9 @@ void forward_tiles(AttentionArgs a, float factor, int slots)
     float m, l;
 
     // One tile of keys. The buffer's number is a constant, so that LDS addresses are; markers and clean (the values
-    // of a tile are to be rewritten) make the later passes.
-    auto tile = [&](int t, auto buffer, auto markers, bool clean) {
+    // of a tile are rewritten) make the later passes.
+    auto tile = [&](int t, auto buffer, auto markers, auto clean) {
+        typedef Operand<T> Op;
         char *s_k = s_mem + buffer.value * 2 * Rows::kBytes, *s_v = s_k + Rows::kBytes;
         wait_copies();
         __syncthreads();     // tile t is there, tile t - 1 is no longer read
@@ -89,7 +88,7 @@ void forward_tiles(AttentionArgs a, float factor, int slots)
             load_k.load(s_next, keys, range.start(t + 1), nk);
             load_v.load(s_next + Rows::kBytes, values, range.start(t + 1), nk);
         }
-        if (clean) {
+        if (clean.value) {
             Rows::only_finite(s_v, markers.value);
             __syncthreads();
         }
@@ -100,7 +99,22 @@ void forward_tiles(AttentionArgs a, float factor, int slots)
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int n = 0; n < kD / 16; ++n) x[b] = mma32(Rows::along(s_k, 32 * b + c, 2 * n + half), q[n], x[b]);
+            for (int n = 0; n < kD / 16; ++n) x[b] = mma32(Op(Rows::along(s_k, 32 * b + c, 2 * n + half)), q[n], x[b]);
+        if constexpr (clean.value && sizeof(T) == 4) {
+            // scores that the split made NaN, again by float32 products: they may be infinite
+            bool odd = false;
+#pragma unroll
+            for (int r = 0; r < 32; ++r) odd = odd || x[r >> 4][r & 15] != x[r >> 4][r & 15];
+            if (__any(odd)) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    f32x16 y = {};
+                    for (int n = 0; n < kD / 16; ++n) y = mma32(Rows::along(s_k, 32 * b + c, 2 * n + half), load8(own + 16 * n + 8 * half), y);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) x[b][r] = x[b][r] != x[b][r] ? y[r] : x[b][r];
+                }
+            }
+        }
         if (!(j0 + kTileRows - 1 <= w_first && (j0 > w_high || j0 + kTileRows - 1 < a.sinks))) {
 #pragma unroll
             for (int b = 0; b < 2; ++b)
@@ -139,28 +153,30 @@ void forward_tiles(AttentionArgs a, float factor, int slots)
                 w[r >> 3][r & 7] = static_cast<T>(e);
             }
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
+            for (int s = 0; s < 2; ++s) {
+                const Op weights(w[s]);
 #pragma unroll
-                for (int n = 0; n < kD / 32; ++n) o[n] = mma32(Rows::across(s_v, n, 2 * b + s), w[s], o[n]);
+                for (int n = 0; n < kD / 32; ++n) o[n] = mma32(Op(Rows::across(s_v, n, 2 * b + s)), weights, o[n]);
+            }
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     };
-    auto pass = [&](auto markers, bool clean) {
-#pragma unroll
-        for (int n = 0; n < kD / 32; ++n) o[n] = f32x16{};
-        m = -INFINITY;
-        l = 0.0f;
+    auto pass = [&](auto markers, auto clean) {
         if (range.tiles > 0) {
             load_k.load(s_mem, keys, range.start(0), nk);
             load_v.load(s_mem + Rows::kBytes, values, range.start(0), nk);
         }
+#pragma unroll
+        for (int n = 0; n < kD / 32; ++n) o[n] = f32x16{};
+        m = -INFINITY;
+        l = 0.0f;
         for (int t = 0; t < range.tiles; t += 2) {
             tile(t, Constant<0>{}, markers, clean);
             if (t + 1 < range.tiles) tile(t + 1, Constant<1>{}, markers, clean);
         }
     };
 
-    pass(Constant<0>{}, false);
+    pass(Constant<0>{}, Constant<0>{});
     bool odd = false;
 #pragma unroll
     for (int n = 0; n < kD / 32; ++n)
@@ -171,14 +187,14 @@ void forward_tiles(AttentionArgs a, float factor, int slots)
     // results with these values taken as 0: results with a count are NaN, the others are what they would be without
     // the values that are not seen.
     if (__syncthreads_or(odd)) {
-        pass(Constant<1>{}, true);
+        pass(Constant<1>{}, Constant<1>{});
         uint32_t marked[kD / 64] = {};
 #pragma unroll
         for (int n = 0; n < kD / 32; ++n)
 #pragma unroll
             for (int r = 0; r < 16; ++r) marked[n >> 1] |= static_cast<uint32_t>(o[n][r] > 0.0f) << (16 * (n & 1) + r);
         __syncthreads();     // the tiles are no longer read
-        pass(Constant<0>{}, true);
+        pass(Constant<0>{}, Constant<1>{});
 #pragma unroll
         for (int n = 0; n < kD / 32; ++n)
 #pragma unroll

@@ -156,38 +156,40 @@ void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
     const int w_high = below_window(w_last, a.window);
     const int64_t at = q0 + min(row, nq - 1);
 
-    vec8<T> q[kD / 16], g[kD / 16];
+    const T *own_q = static_cast<const T *>(a.q.data) + at * a.q.token + head * a.q.head + 8 * half;
+    const T *own_g = static_cast<const T *>(a.dout.data) + at * a.dout.token + head * a.dout.head + 8 * half;
+    const T *own_o = static_cast<const T *>(a.out.data) + at * a.out.token + head * a.out.head + 8 * half;
+    Operand<T> q[kD / 16], g[kD / 16];
     float lse2 = a.lse[head * a.q_tokens + at], minus_delta = 0.0f, unshift = 1.0f;
     lse2 = lse2 == -INFINITY ? INFINITY : lse2 * kLog2e - (kNarrow<T> ? kWeightShift : 0.0f);
-    {
-        vec8<T> o[kD / 16];
+    float top = 0.0f, finite = 0.0f;      // largest |dout| of the row, and of its finite values
+    vec8<T> rows[3][kD / 16];
 #pragma unroll
-        for (int t = 0; t < kD / 16; ++t) {
-            q[t] = load8(static_cast<const T *>(a.q.data) + at * a.q.token + head * a.q.head + 16 * t + 8 * half);
-            g[t] = load8(static_cast<const T *>(a.dout.data) + at * a.dout.token + head * a.dout.head + 16 * t + 8 * half);
-            o[t] = load8(static_cast<const T *>(a.out.data) + at * a.out.token + head * a.out.head + 16 * t + 8 * half);
-        }
+    for (int t = 0; t < kD / 16; ++t) {
+        rows[0][t] = load8(own_q + 16 * t);
+        rows[1][t] = load8(own_g + 16 * t);
+        rows[2][t] = load8(own_o + 16 * t);
+    }
 #pragma unroll
-        for (int t = 0; t < kD / 16; ++t) {
-            arrive(q[t]);
-            arrive(g[t]);
+    for (int t = 0; t < kD / 16; ++t) {
+        q[t] = Operand<T>(rows[0][t]);
+        g[t] = Operand<T>(rows[1][t]);
+        arrive(q[t]);
+        arrive(g[t]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) minus_delta -= to_float(g[t][i]) * to_float(o[t][i]);
+        for (int i = 0; i < 8; ++i) {
+            minus_delta -= to_float(rows[1][t][i]) * to_float(rows[2][t][i]);
+            if constexpr (kNarrow<T>) {
+                const float x = fabsf(to_float(rows[1][t][i]));
+                top = fmaxf(top, x);
+                finite = fmaxf(finite, not_finite(x) ? 0.0f : x);
+            }
         }
     }
     minus_delta += __shfl_xor(minus_delta, 32);
     if (half == 0 && row < nq) work.lse2[head * a.q_tokens + at] = lse2;
     if constexpr (kNarrow<T>) {
         __shared__ float s_top[kWaves];
-        float top = 0.0f, finite = 0.0f;
-#pragma unroll
-        for (int t = 0; t < kD / 16; ++t)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float x = fabsf(to_float(g[t][i]));
-                top = fmaxf(top, x);
-                finite = fmaxf(finite, not_finite(x) ? 0.0f : x);
-            }
         const float e = static_cast<float>(exponent_of(fmaxf(top, __shfl_xor(top, 32))));
         lse2 += e;
         unshift = fast_exp2(e - kWeightShift);
@@ -207,6 +209,7 @@ void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
     // 2 the one that finds what delta lacks.
     auto tile = [&](int t, auto buffer, auto which) {
         constexpr bool second = which.value == 1;
+        typedef Operand<T> Op;
         char *s_k = s_mem + buffer.value * 2 * Rows::kBytes, *s_v = s_k + Rows::kBytes;
         wait_copies();
         __syncthreads();     // tile t is there, tile t - 1 is no longer read
@@ -229,8 +232,8 @@ void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
             f32x16 x = {}, y = {};
 #pragma unroll
             for (int n = 0; n < kD / 16; ++n) {
-                x = mma32(Rows::along(s_k, 32 * b + c, 2 * n + half), q[n], x);
-                y = mma32(Rows::along(s_v, 32 * b + c, 2 * n + half), g[n], y);
+                x = mma32(Op(Rows::along(s_k, 32 * b + c, 2 * n + half)), q[n], x);
+                y = mma32(Op(Rows::along(s_v, 32 * b + c, 2 * n + half)), g[n], y);
             }
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
@@ -253,18 +256,20 @@ void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
 #pragma unroll
             for (int r = 0; r < 16; ++r) w[r >> 3][r & 7] = static_cast<T>(y[r]);
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
+            for (int s = 0; s < 2; ++s) {
+                const Op weights(w[s]);
 #pragma unroll
-                for (int n = 0; n < kD / 32; ++n) dq[n] = mma32(Rows::across(s_k, n, 2 * b + s), w[s], dq[n]);
+                for (int n = 0; n < kD / 32; ++n) dq[n] = mma32(Op(Rows::across(s_k, n, 2 * b + s)), weights, dq[n]);
+            }
         }
     };
     auto pass = [&](auto which) {
-#pragma unroll
-        for (int n = 0; n < kD / 32; ++n) dq[n] = f32x16{};
         if (range.tiles > 0) {
             load_k.load(s_mem, keys, range.start(0), nk);
             load_v.load(s_mem + Rows::kBytes, values, range.start(0), nk);
         }
+#pragma unroll
+        for (int n = 0; n < kD / 32; ++n) dq[n] = f32x16{};
         for (int t = 0; t < range.tiles; t += 2) {
             tile(t, Constant<0>{}, which);
             if (t + 1 < range.tiles) tile(t + 1, Constant<1>{}, which);
@@ -361,23 +366,9 @@ __device__ inline void dkv_group(const AttentionArgs &a, const Work &work, float
         unit_v = fast_exp2(-kWeightShift);
         unit_k = fast_exp2(static_cast<float>(e) - kWeightShift);
     }
-    // The keys' and values' operands stay in registers. Float32 rows of 128 take 128 registers each way, beside as many
-    // of accumulators: there the values come from the caches in every tile (the compiler would else put some of the
-    // operands into scratch memory and fetch them from there).
-    constexpr bool kKeep = sizeof(T) == 2 || kD == 64;
-    vec8<T> k[kD / 16], v[kKeep ? kD / 16 : 1];
     const int64_t own = k0 + min(key, nk - 1);
+    const T *own_k = static_cast<const T *>(a.k.data) + own * a.k.token + kv * a.k.head + 8 * half;
     const T *own_v = static_cast<const T *>(a.v.data) + own * a.v.token + kv * a.v.head + 8 * half;
-#pragma unroll
-    for (int t = 0; t < kD / 16; ++t) {
-        k[t] = load8(static_cast<const T *>(a.k.data) + own * a.k.token + kv * a.k.head + 16 * t + 8 * half);
-        if constexpr (kKeep) v[t] = load8(own_v + 16 * t);
-    }
-#pragma unroll
-    for (int t = 0; t < kD / 16; ++t) {
-        arrive(k[t]);
-        if constexpr (kKeep) arrive(v[t]);
-    }
     const typename Rows::Loader load_q(a.q.token), load_g(a.dout.token);
     auto load = [&](int buffer, int head, int i) {
         char *s = s_mem + buffer * 2 * Rows::kBytes;
@@ -388,10 +379,26 @@ __device__ inline void dkv_group(const AttentionArgs &a, const Work &work, float
             copy4((wave ? work.minus_delta : work.lse2) + head * a.q_tokens + q0 + i, 4 * min(lane, nq - 1 - i), s_stats[buffer][wave]);
     };
 
+    // The keys' and values' operands stay in registers, but for float32 values of dim 128: with as many registers of
+    // accumulators beside them they come from the caches in every tile (the compiler would put some of them into
+    // scratch memory and fetch them from there).
+    constexpr bool kKeep = sizeof(T) == 2 || kD == 64;
+    Operand<T> k[kD / 16], v[kKeep ? kD / 16 : 1];
+#pragma unroll
+    for (int t = 0; t < kD / 16; ++t) {
+        k[t] = Operand<T>(load8(own_k + 16 * t));
+        if constexpr (kKeep) v[t] = Operand<T>(load8(own_v + 16 * t));
+    }
+#pragma unroll
+    for (int t = 0; t < kD / 16; ++t) {
+        arrive(k[t]);
+        if constexpr (kKeep) arrive(v[t]);
+    }
     f32x16 dk[kD / 32], dv[kD / 32];
     int head, i;     // of the next tile to load
     // One tile of queries; buffer and pass are constants.
     auto tile = [&](int t, int i_tile, auto buffer, auto second) {
+        typedef Operand<T> Op;
         char *s_q = s_mem + buffer.value * 2 * Rows::kBytes, *s_g = s_q + Rows::kBytes;
         wait_copies();
         __syncthreads();     // tile t is there, tile t - 1 is no longer read
@@ -420,9 +427,9 @@ __device__ inline void dkv_group(const AttentionArgs &a, const Work &work, float
             }
 #pragma unroll
             for (int n = 0; n < kD / 16; ++n) {
-                x = mma32(Rows::along(s_q, 32 * b + c, 2 * n + half), k[n], x);
-                if constexpr (kKeep) y = mma32(Rows::along(s_g, 32 * b + c, 2 * n + half), v[n], y);
-                else y = mma32(Rows::along(s_g, 32 * b + c, 2 * n + half), load8(own_v + 16 * n), y);
+                x = mma32(Op(Rows::along(s_q, 32 * b + c, 2 * n + half)), k[n], x);
+                if constexpr (kKeep) y = mma32(Op(Rows::along(s_g, 32 * b + c, 2 * n + half)), v[n], y);
+                else y = mma32(Op(Rows::along(s_g, 32 * b + c, 2 * n + half)), Op(load8(own_v + 16 * n)), y);
             }
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
@@ -447,20 +454,22 @@ __device__ inline void dkv_group(const AttentionArgs &a, const Work &work, float
                 d[r >> 3][r & 7] = static_cast<T>(y[r]);
             }
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
+            for (int s = 0; s < 2; ++s) {
+                const Op weights(w[s]), slopes(d[s]);
 #pragma unroll
                 for (int n = 0; n < kD / 32; ++n) {
-                    dv[n] = mma32(Rows::across(s_g, n, 2 * b + s), w[s], dv[n]);
-                    dk[n] = mma32(Rows::across(s_q, n, 2 * b + s), d[s], dk[n]);
+                    dv[n] = mma32(Op(Rows::across(s_g, n, 2 * b + s)), weights, dv[n]);
+                    dk[n] = mma32(Op(Rows::across(s_q, n, 2 * b + s)), slopes, dk[n]);
                 }
+            }
         }
     };
     auto pass = [&](auto second) {
-#pragma unroll
-        for (int n = 0; n < kD / 32; ++n) dk[n] = dv[n] = f32x16{};
         head = kv * group;
         i = i_start;
         if (tiles > 0) load(0, head, i);
+#pragma unroll
+        for (int n = 0; n < kD / 32; ++n) dk[n] = dv[n] = f32x16{};
         auto step = [&](int t, auto buffer) {
             const int now = i;
             i += kTileRows;

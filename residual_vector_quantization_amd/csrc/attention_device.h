@@ -85,6 +85,44 @@ __device__ inline f32x4 mma16(f32x8 a, f32x8 b, f32x4 c)
     return c;
 }
 
+// Eight float32 values as three bfloat16 parts each, x = high + middle + low to 2^-24 of x: high is x cut off after 8
+// bits, what is left is exact in float32, middle its rounding to 8 bits and low that of the exact rest.
+struct Split8 {
+    bf16x8 high, middle, low;
+
+    __device__ Split8() {}
+    __device__ explicit Split8(f32x8 x)
+    {
+        union Pairs { uint32_t pair[4]; bf16x8 whole; } h, m, l;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = x[2 * i], b = x[2 * i + 1];
+            const uint32_t ah = __float_as_uint(a) & 0xffff0000u, bh = __float_as_uint(b) & 0xffff0000u;
+            h.pair[i] = __builtin_amdgcn_perm(bh, ah, 0x07060302u);     // both high halves
+            const float ar = a - __uint_as_float(ah), br = b - __uint_as_float(bh);
+            m.pair[i] = round_pair(ar, br);
+            l.pair[i] = round_pair(ar - __uint_as_float(m.pair[i] << 16), br - __uint_as_float(m.pair[i] & 0xffff0000u));
+        }
+        high = h.whole;
+        middle = m.whole;
+        low = l.whole;
+    }
+    __device__ static uint32_t round_pair(float a, float b)
+    {
+        typedef float two __attribute__((ext_vector_type(2)));
+        typedef bf16_t half_two __attribute__((ext_vector_type(2)));
+        union { half_two x; uint32_t bits; } u;
+        u.x = __builtin_convertvector(two{a, b}, half_two);
+        return u.bits;
+    }
+};
+
+// What a 32-wide product takes for 8 values of type T. Float32 values are split: six bfloat16 products of 32 cycles
+// give what eight float32 products of 64 do, to the 2^-26 of the parts' products left out. Infinities split into NaN.
+template <typename T> struct OperandOf { typedef vec8<T> type; };
+template <> struct OperandOf<float> { typedef Split8 type; };
+template <typename T> using Operand = typename OperandOf<T>::type;
+
 __device__ inline f32x16 mma32(bf16x8 a, bf16x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
 __device__ inline f32x16 mma32(f16x8 a, f16x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
 __device__ inline f32x16 mma32(f32x8 a, f32x8 b, f32x16 c)
@@ -93,7 +131,15 @@ __device__ inline f32x16 mma32(f32x8 a, f32x8 b, f32x16 c)
     for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], c, 0, 0, 0);
     return c;
 }
-
+__device__ inline f32x16 mma32(const Split8 &a, const Split8 &b, f32x16 c)
+{
+    c = mma32(a.low, b.high, c);       // small terms first
+    c = mma32(a.high, b.low, c);
+    c = mma32(a.middle, b.middle, c);
+    c = mma32(a.middle, b.high, c);
+    c = mma32(a.high, b.middle, c);
+    return mma32(a.high, b.high, c);
+}
 __device__ inline float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
 __device__ inline float wave_sum(float x)

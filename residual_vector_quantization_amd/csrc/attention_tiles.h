@@ -57,6 +57,12 @@ __device__ inline void arrive(V &x)
 {
     asm volatile("" : "+v"(x));
 }
+__device__ inline void arrive(Split8 &x)
+{
+    arrive(x.high);
+    arrive(x.middle);
+    arrive(x.low);
+}
 __device__ inline void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // The 64-key tiles that the queries at positions p_first .. p_last see some of: the sinks', then the window's.
