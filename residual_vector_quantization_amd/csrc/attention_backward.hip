@@ -383,6 +383,10 @@ __device__ inline void dkv_group(const AttentionArgs &a, const Work &work, float
     // accumulators beside them they come from the caches in every tile (the compiler would put some of them into
     // scratch memory and fetch them from there).
     constexpr bool kKeep = sizeof(T) == 2 || kD == 64;
+    // 16-bit operands are read from the LDS well ahead of their products: those along the rows all at once, those across
+    // them before the exponentials (dim 128 with 1 wavefront a SIMD 302 -> 282 us, dim 64 with 2 237 -> 221 us). Split
+    // float32 operands would take three times the registers.
+    constexpr bool kAhead = sizeof(T) == 2;
     Operand<T> k[kD / 16], v[kKeep ? kD / 16 : 1];
 #pragma unroll
     for (int t = 0; t < kD / 16; ++t) {
@@ -417,6 +421,7 @@ __device__ inline void dkv_group(const AttentionArgs &a, const Work &work, float
             if (kFar && (b != (wave & 1) || p0 + 31 < i_first + back)) continue;
             f32x16 x = {}, y;
             f32x4 lse2[4];
+            Op tg[2][kAhead ? kD / 32 : 1], tq[2][kAhead ? kD / 32 : 1];
 #pragma unroll
             for (int f = 0; f < 4; ++f) {
                 const int in = 32 * b + 8 * f + 4 * half;
@@ -425,11 +430,34 @@ __device__ inline void dkv_group(const AttentionArgs &a, const Work &work, float
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[4 * f + e] = minus_delta[e];     // dw - delta comes out of the product
             }
+            if constexpr (kAhead) {
+                Op aq[kD / 16], ag[kD / 16];
 #pragma unroll
-            for (int n = 0; n < kD / 16; ++n) {
-                x = mma32(Op(Rows::along(s_q, 32 * b + c, 2 * n + half)), k[n], x);
-                if constexpr (kKeep) y = mma32(Op(Rows::along(s_g, 32 * b + c, 2 * n + half)), v[n], y);
-                else y = mma32(Op(Rows::along(s_g, 32 * b + c, 2 * n + half)), Op(load8(own_v + 16 * n)), y);
+                for (int n = 0; n < kD / 16; ++n) {
+                    aq[n] = Rows::along(s_q, 32 * b + c, 2 * n + half);
+                    ag[n] = Rows::along(s_g, 32 * b + c, 2 * n + half);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int n = 0; n < kD / 16; ++n) {
+                    x = mma32(aq[n], k[n], x);
+                    y = mma32(ag[n], v[n], y);
+                }
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int n = 0; n < kD / 32; ++n) {
+                        tg[s][n] = Rows::across(s_g, n, 2 * b + s);
+                        tq[s][n] = Rows::across(s_q, n, 2 * b + s);
+                    }
+                __builtin_amdgcn_sched_barrier(0);
+            } else {
+#pragma unroll
+                for (int n = 0; n < kD / 16; ++n) {
+                    x = mma32(Op(Rows::along(s_q, 32 * b + c, 2 * n + half)), k[n], x);
+                    if constexpr (kKeep) y = mma32(Op(Rows::along(s_g, 32 * b + c, 2 * n + half)), v[n], y);
+                    else y = mma32(Op(Rows::along(s_g, 32 * b + c, 2 * n + half)), Op(load8(own_v + 16 * n)), y);
+                }
             }
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
@@ -458,8 +486,13 @@ __device__ inline void dkv_group(const AttentionArgs &a, const Work &work, float
                 const Op weights(w[s]), slopes(d[s]);
 #pragma unroll
                 for (int n = 0; n < kD / 32; ++n) {
-                    dv[n] = mma32(Op(Rows::across(s_g, n, 2 * b + s)), weights, dv[n]);
-                    dk[n] = mma32(Op(Rows::across(s_q, n, 2 * b + s)), slopes, dk[n]);
+                    if constexpr (kAhead) {
+                        dv[n] = mma32(tg[s][n], weights, dv[n]);
+                        dk[n] = mma32(tq[s][n], slopes, dk[n]);
+                    } else {
+                        dv[n] = mma32(Op(Rows::across(s_g, n, 2 * b + s)), weights, dv[n]);
+                        dk[n] = mma32(Op(Rows::across(s_q, n, 2 * b + s)), slopes, dk[n]);
+                    }
                 }
             }
         }
