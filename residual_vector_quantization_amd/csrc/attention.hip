@@ -13,8 +13,7 @@
 // so maxima and sums run inside a lane (and once with the lane 32 further), and
 // the scores that a lane holds are, in order, the P^T operand of the second
 // product: the keys of a V^T operand are numbered as the scores come out.
-// K and V lie in the LDS row by row, two tiles of each: while one is worked on,
-// the next is on its way from global memory.
+// While one tile is worked on, the next is on its way from global memory.
 #include <float.h>
 #include <limits.h>
 #include <stdint.h>
@@ -37,8 +36,9 @@ template <typename T, int kD>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
 void forward_tiles(AttentionArgs a, float factor, int slots)
 {
-    typedef Tile<T, kD, kWaves> Rows;
-    __shared__ __attribute__((aligned(16))) char s_mem[4 * Rows::kBytes];
+    typedef Feed<T, kD, kWaves> Keys;
+    typedef typename Keys::Rows Rows;
+    __shared__ __attribute__((aligned(16))) char s_mem[Keys::kBytes];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 31, half = lane >> 5;
     // heads change fastest: with 8 of them or more, one chiplet sees the same heads' keys again and again; the
@@ -69,7 +69,7 @@ void forward_tiles(AttentionArgs a, float factor, int slots)
     for (int t = 0; t < kD / 16; ++t) q[t] = Operand<T>(load8(own + 16 * t + 8 * half));
 #pragma unroll
     for (int t = 0; t < kD / 16; ++t) arrive(q[t]);
-    const typename Rows::Loader load_k(a.k.token), load_v(a.v.token);
+    Keys feed(s_mem, a.k.token, a.v.token);
     const T *keys = static_cast<const T *>(a.k.data) + static_cast<int64_t>(k0) * a.k.token + kv * a.k.head;
     const T *values = static_cast<const T *>(a.v.data) + static_cast<int64_t>(k0) * a.v.token + kv * a.v.head;
 
@@ -79,17 +79,10 @@ void forward_tiles(AttentionArgs a, float factor, int slots)
     // One tile of keys. The buffer's number is a constant, so that LDS addresses are; markers and clean (the values
     // of a tile are rewritten) make the later passes.
     auto tile = [&](int t, auto buffer, auto markers, auto clean) {
-        typedef Operand<T> Op;
-        char *s_k = s_mem + buffer.value * 2 * Rows::kBytes, *s_v = s_k + Rows::kBytes;
-        wait_copies();
-        __syncthreads();     // tile t is there, tile t - 1 is no longer read
-        if (t + 1 < range.tiles) {
-            char *s_next = s_mem + (1 - buffer.value) * 2 * Rows::kBytes;
-            load_k.load(s_next, keys, range.start(t + 1), nk);
-            load_v.load(s_next + Rows::kBytes, values, range.start(t + 1), nk);
-        }
+        char *s_k = feed.tile_one(buffer), *s_v = feed.tile_two(buffer);
+        feed.turn(buffer, t + 1 < range.tiles, keys, values, range.start(t + 1), nk);
         if (clean.value) {
-            Rows::only_finite(s_v, markers.value);
+            only_finite<Rows, kD, kThreads>(s_v, markers.value);
             __syncthreads();
         }
         const int j0 = range.start(t);
@@ -99,7 +92,7 @@ void forward_tiles(AttentionArgs a, float factor, int slots)
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int n = 0; n < kD / 16; ++n) x[b] = mma32(Op(Rows::along(s_k, 32 * b + c, 2 * n + half)), q[n], x[b]);
+            for (int n = 0; n < kD / 16; ++n) x[b] = mma32(Rows::along(s_k, 32 * b + c, 2 * n + half), q[n], x[b]);
         if constexpr (clean.value && sizeof(T) == 4) {
             // scores that the split made NaN, again by float32 products: they may be infinite
             bool odd = false;
@@ -109,7 +102,8 @@ void forward_tiles(AttentionArgs a, float factor, int slots)
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     f32x16 y = {};
-                    for (int n = 0; n < kD / 16; ++n) y = mma32(Rows::along(s_k, 32 * b + c, 2 * n + half), load8(own + 16 * n + 8 * half), y);
+                    const T *key = keys + min(j0 + 32 * b + c, nk - 1) * a.k.token + 8 * half;
+                    for (int n = 0; n < kD / 16; ++n) y = mma32(load8(key + 16 * n), load8(own + 16 * n + 8 * half), y);
 #pragma unroll
                     for (int r = 0; r < 16; ++r) x[b][r] = x[b][r] != x[b][r] ? y[r] : x[b][r];
                 }
@@ -154,18 +148,15 @@ void forward_tiles(AttentionArgs a, float factor, int slots)
             }
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const Op weights(w[s]);
+                const Operand<T> weights(w[s]);
 #pragma unroll
-                for (int n = 0; n < kD / 32; ++n) o[n] = mma32(Op(Rows::across(s_v, n, 2 * b + s)), weights, o[n]);
+                for (int n = 0; n < kD / 32; ++n) o[n] = mma32(Rows::across(s_v, n, 2 * b + s), weights, o[n]);
             }
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     };
     auto pass = [&](auto markers, auto clean) {
-        if (range.tiles > 0) {
-            load_k.load(s_mem, keys, range.start(0), nk);
-            load_v.load(s_mem + Rows::kBytes, values, range.start(0), nk);
-        }
+        if (range.tiles > 0) feed.start(keys, values, range.start(0), nk);
 #pragma unroll
         for (int n = 0; n < kD / 32; ++n) o[n] = f32x16{};
         m = -INFINITY;

@@ -106,23 +106,6 @@ __device__ inline bool not_finite(float x) { return !(fabsf(x) <= FLT_MAX); }
 // e with 2^(e - 1) <= x < 2^e, 0 for x = 0 and values that are not finite.
 __device__ inline int exponent_of(float x) { return x == 0.0f || not_finite(x) ? 0 : __builtin_amdgcn_frexp_expf(x); }
 
-// Rows of a tile with a value that is not finite: their flag is set and they become zeros. Barriers are the caller's.
-template <typename T, int kD>
-__device__ inline void clear_bad_rows(char *s, int *flags)
-{
-    constexpr int kLanes = kThreads / kTileRows;
-    const int row = threadIdx.x / kLanes;
-    T *x = reinterpret_cast<T *>(s) + row * kD;
-    bool bad = false;
-    for (int i = threadIdx.x % kLanes; i < kD; i += kLanes) bad = bad || not_finite(to_float(x[i]));
-#pragma unroll
-    for (int m = 1; m < kLanes; m <<= 1) bad = __shfl_xor(static_cast<int>(bad), m) || bad;
-    if (bad) {
-        flags[row] = 1;
-        for (int i = threadIdx.x % kLanes; i < kD; i += kLanes) x[i] = static_cast<T>(0.0f);
-    }
-}
-
 // dq, and lse2 and delta of the rows. As in the forward pass a workgroup takes 128 queries and goes over the tiles of keys they see. If a result is
 // not finite, a second pass takes rows of K that are not finite as zeros and the weights of the queries that do see
 // them as NaN, so that only those get it.
@@ -130,8 +113,9 @@ template <typename T, int kD>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? (kD == 64 ? 3 : 2) : 1)
 void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
 {
-    typedef Tile<T, kD, kWaves> Rows;
-    __shared__ __attribute__((aligned(16))) char s_mem[4 * Rows::kBytes];
+    typedef Feed<T, kD, kWaves> Keys;
+    typedef typename Keys::Rows Rows;
+    __shared__ __attribute__((aligned(16))) char s_mem[Keys::kBytes];
     __shared__ int s_bad[kTileRows];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 31, half = lane >> 5;
@@ -199,7 +183,7 @@ void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
         __syncthreads();
         if (threadIdx.x == 0) work.largest[blockIdx.x] = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
     }
-    const typename Rows::Loader load_k(a.k.token), load_v(a.v.token);
+    Keys feed(s_mem, a.k.token, a.v.token);
     const T *keys = static_cast<const T *>(a.k.data) + static_cast<int64_t>(k0) * a.k.token + kv * a.k.head;
     const T *values = static_cast<const T *>(a.v.data) + static_cast<int64_t>(k0) * a.v.token + kv * a.v.head;
 
@@ -209,19 +193,12 @@ void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
     // 2 the one that finds what delta lacks.
     auto tile = [&](int t, auto buffer, auto which) {
         constexpr bool second = which.value == 1;
-        typedef Operand<T> Op;
-        char *s_k = s_mem + buffer.value * 2 * Rows::kBytes, *s_v = s_k + Rows::kBytes;
-        wait_copies();
-        __syncthreads();     // tile t is there, tile t - 1 is no longer read
-        if (t + 1 < range.tiles) {
-            char *s_next = s_mem + (1 - buffer.value) * 2 * Rows::kBytes;
-            load_k.load(s_next, keys, range.start(t + 1), nk);
-            load_v.load(s_next + Rows::kBytes, values, range.start(t + 1), nk);
-        }
+        char *s_k = feed.tile_one(buffer), *s_v = feed.tile_two(buffer);
+        feed.turn(buffer, t + 1 < range.tiles, keys, values, range.start(t + 1), nk);
         if (second) {
             if (threadIdx.x < kTileRows) s_bad[threadIdx.x] = 0;
             __syncthreads();
-            clear_bad_rows<T, kD>(s_k, s_bad);
+            clear_bad_rows<Rows, kD, kThreads>(s_k, s_bad);
             __syncthreads();
         }
         const int j0 = range.start(t);
@@ -232,8 +209,8 @@ void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
             f32x16 x = {}, y = {};
 #pragma unroll
             for (int n = 0; n < kD / 16; ++n) {
-                x = mma32(Op(Rows::along(s_k, 32 * b + c, 2 * n + half)), q[n], x);
-                y = mma32(Op(Rows::along(s_v, 32 * b + c, 2 * n + half)), g[n], y);
+                x = mma32(Rows::along(s_k, 32 * b + c, 2 * n + half), q[n], x);
+                y = mma32(Rows::along(s_v, 32 * b + c, 2 * n + half), g[n], y);
             }
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
@@ -257,17 +234,14 @@ void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
             for (int r = 0; r < 16; ++r) w[r >> 3][r & 7] = static_cast<T>(y[r]);
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const Op weights(w[s]);
+                const Operand<T> weights(w[s]);
 #pragma unroll
-                for (int n = 0; n < kD / 32; ++n) dq[n] = mma32(Op(Rows::across(s_k, n, 2 * b + s)), weights, dq[n]);
+                for (int n = 0; n < kD / 32; ++n) dq[n] = mma32(Rows::across(s_k, n, 2 * b + s), weights, dq[n]);
             }
         }
     };
     auto pass = [&](auto which) {
-        if (range.tiles > 0) {
-            load_k.load(s_mem, keys, range.start(0), nk);
-            load_v.load(s_mem + Rows::kBytes, values, range.start(0), nk);
-        }
+        if (range.tiles > 0) feed.start(keys, values, range.start(0), nk);
 #pragma unroll
         for (int n = 0; n < kD / 32; ++n) dq[n] = f32x16{};
         for (int t = 0; t < range.tiles; t += 2) {
@@ -309,7 +283,8 @@ template <typename T, int kD, bool kFar>
 __device__ inline void dkv_group(const AttentionArgs &a, const Work &work, float factor, int block, char *s_mem,
                                  float (&s_stats)[2][2][kTileRows], int *s_bad)
 {
-    typedef Tile<T, kD, kWaves> Rows;
+    typedef Feed<T, kD, kWaves> Queries;
+    typedef typename Queries::Rows Rows;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 31, half = lane >> 5;
     const int slot = block / a.kv_heads, kv = block % a.kv_heads, group = a.q_heads / a.kv_heads;
@@ -369,12 +344,10 @@ __device__ inline void dkv_group(const AttentionArgs &a, const Work &work, float
     const int64_t own = k0 + min(key, nk - 1);
     const T *own_k = static_cast<const T *>(a.k.data) + own * a.k.token + kv * a.k.head + 8 * half;
     const T *own_v = static_cast<const T *>(a.v.data) + own * a.v.token + kv * a.v.head + 8 * half;
-    const typename Rows::Loader load_q(a.q.token), load_g(a.dout.token);
-    auto load = [&](int buffer, int head, int i) {
-        char *s = s_mem + buffer * 2 * Rows::kBytes;
-        load_q.load(s, static_cast<const T *>(a.q.data) + static_cast<int64_t>(q0) * a.q.token + head * a.q.head, i, nq);
-        load_g.load(s + Rows::kBytes, static_cast<const T *>(a.dout.data) + static_cast<int64_t>(q0) * a.dout.token + head * a.dout.head,
-                    i, nq);
+    Queries feed(s_mem, a.q.token, a.dout.token);
+    const T *queries = static_cast<const T *>(a.q.data) + static_cast<int64_t>(q0) * a.q.token;
+    const T *slopes_of = static_cast<const T *>(a.dout.data) + static_cast<int64_t>(q0) * a.dout.token;
+    auto load_stats = [&](int buffer, int head, int i) {
         if (wave < 2)
             copy4((wave ? work.minus_delta : work.lse2) + head * a.q_tokens + q0 + i, 4 * min(lane, nq - 1 - i), s_stats[buffer][wave]);
     };
@@ -403,15 +376,14 @@ __device__ inline void dkv_group(const AttentionArgs &a, const Work &work, float
     // One tile of queries; buffer and pass are constants.
     auto tile = [&](int t, int i_tile, auto buffer, auto second) {
         typedef Operand<T> Op;
-        char *s_q = s_mem + buffer.value * 2 * Rows::kBytes, *s_g = s_q + Rows::kBytes;
-        wait_copies();
-        __syncthreads();     // tile t is there, tile t - 1 is no longer read
-        if (t + 1 < tiles) load(1 - buffer.value, head, i);
+        char *s_q = feed.tile_one(buffer), *s_g = feed.tile_two(buffer);
+        feed.turn(buffer, t + 1 < tiles, queries + head * a.q.head, slopes_of + head * a.dout.head, i, nq);
+        if (t + 1 < tiles) load_stats(1 - buffer.value, head, i);
         if (second.value) {
             if (threadIdx.x < kTileRows) s_bad[threadIdx.x] = 0;
             __syncthreads();
-            clear_bad_rows<T, kD>(s_q, s_bad);
-            clear_bad_rows<T, kD>(s_g, s_bad);
+            clear_bad_rows<Rows, kD, kThreads>(s_q, s_bad);
+            clear_bad_rows<Rows, kD, kThreads>(s_g, s_bad);
             __syncthreads();
         }
 #pragma unroll
@@ -454,9 +426,9 @@ __device__ inline void dkv_group(const AttentionArgs &a, const Work &work, float
             } else {
 #pragma unroll
                 for (int n = 0; n < kD / 16; ++n) {
-                    x = mma32(Op(Rows::along(s_q, 32 * b + c, 2 * n + half)), k[n], x);
-                    if constexpr (kKeep) y = mma32(Op(Rows::along(s_g, 32 * b + c, 2 * n + half)), v[n], y);
-                    else y = mma32(Op(Rows::along(s_g, 32 * b + c, 2 * n + half)), Op(load8(own_v + 16 * n)), y);
+                    x = mma32(Rows::along(s_q, 32 * b + c, 2 * n + half), k[n], x);
+                    if constexpr (kKeep) y = mma32(Rows::along(s_g, 32 * b + c, 2 * n + half), v[n], y);
+                    else y = mma32(Rows::along(s_g, 32 * b + c, 2 * n + half), Op(load8(own_v + 16 * n)), y);
                 }
             }
 #pragma unroll
@@ -490,8 +462,8 @@ __device__ inline void dkv_group(const AttentionArgs &a, const Work &work, float
                         dv[n] = mma32(tg[s][n], weights, dv[n]);
                         dk[n] = mma32(tq[s][n], slopes, dk[n]);
                     } else {
-                        dv[n] = mma32(Op(Rows::across(s_g, n, 2 * b + s)), weights, dv[n]);
-                        dk[n] = mma32(Op(Rows::across(s_q, n, 2 * b + s)), slopes, dk[n]);
+                        dv[n] = mma32(Rows::across(s_g, n, 2 * b + s), weights, dv[n]);
+                        dk[n] = mma32(Rows::across(s_q, n, 2 * b + s), slopes, dk[n]);
                     }
                 }
             }
@@ -500,7 +472,10 @@ __device__ inline void dkv_group(const AttentionArgs &a, const Work &work, float
     auto pass = [&](auto second) {
         head = kv * group;
         i = i_start;
-        if (tiles > 0) load(0, head, i);
+        if (tiles > 0) {
+            feed.start(queries + head * a.q.head, slopes_of + head * a.dout.head, i, nq);
+            load_stats(0, head, i);
+        }
 #pragma unroll
         for (int n = 0; n < kD / 32; ++n) dk[n] = dv[n] = f32x16{};
         auto step = [&](int t, auto buffer) {
@@ -562,7 +537,7 @@ template <typename T, int kD>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && kD == 64 ? 2 : 1)
 void dkv_tiles(AttentionArgs a, Work work, float factor, int near_groups)
 {
-    __shared__ __attribute__((aligned(16))) char s_mem[4 * Tile<T, kD, kWaves>::kBytes];
+    __shared__ __attribute__((aligned(16))) char s_mem[Feed<T, kD, kWaves>::kBytes];
     __shared__ __attribute__((aligned(16))) float s_stats[2][2][kTileRows];     // [buffer][lse2, -delta][query]
     __shared__ int s_bad[kTileRows];
     const int block = blockIdx.x;

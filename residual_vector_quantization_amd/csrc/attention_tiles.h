@@ -1,11 +1,13 @@
 // Tiles of head rows in the LDS, and the matrix operands read from them along
 // the rows or across them.
 //
-// A tile lies row after row, 16 bytes a piece; the pieces of a row are
-// exchanged (place) so that reads along the rows (16 neighbouring rows, the
-// same piece) and across them (4 neighbouring rows, 64 bytes each) spread over
-// all banks. Rows come straight from global memory into the LDS, each lane
-// picking the piece that belongs to its place.
+// A tile of 16-bit values lies row after row, 16 bytes a piece; the pieces of a
+// row are exchanged (place) so that reads along the rows (16 neighbouring rows,
+// the same piece) and across them (4 neighbouring rows, 64 bytes each) spread
+// over all banks. Rows come straight from global memory into the LDS, each lane
+// picking the piece that belongs to its place. A tile of float32 values is
+// three such tiles, of their bfloat16 parts: a workgroup splits each value
+// once, on the way from registers into the LDS.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -91,14 +93,14 @@ __device__ inline int below_window(int p, int window)
     return static_cast<int>(max(static_cast<int64_t>(p) - window, static_cast<int64_t>(-1)));
 }
 
+// 64 rows of 16-bit values.
 template <typename T, int kD, int kWaves>
 struct Tile {
-    static constexpr int kRowBytes = kD * static_cast<int>(sizeof(T));
+    static constexpr int kRowBytes = 2 * kD;
     static constexpr int kBytes = kTileRows * kRowBytes;
-    static constexpr int kPiece = 16 / static_cast<int>(sizeof(T));   // values in 16 bytes
     static constexpr int kRowPieces = kRowBytes / 16;
     static constexpr int kCopies = kTileRows * kRowPieces / (64 * kWaves);
-    static_assert(kCopies >= 1, "tile smaller than the workgroup");
+    static_assert(sizeof(T) == 2 && kCopies >= 1, "tile smaller than the workgroup");
 
     __device__ static int place(int row, int piece)
     {
@@ -111,7 +113,7 @@ struct Tile {
         uint32_t offset[kCopies];
         uint32_t step;      // bytes from row to row
 
-        __device__ Loader(int64_t stride)
+        __device__ explicit Loader(int64_t stride)
         {
             const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
             step = static_cast<uint32_t>(stride) * static_cast<uint32_t>(sizeof(T));
@@ -143,59 +145,186 @@ struct Tile {
     // Operand along the rows: values 8 k8 .. 8 k8 + 7 of a row.
     __device__ static vec8<T> along(const char *s, int row, int k8)
     {
-        const char *r = s + row * kRowBytes;
-        if constexpr (sizeof(T) == 2) {
-            return *reinterpret_cast<const vec8<T> *>(r + place(row, k8) * 16);
-        } else {
-            const f32x4 a = *reinterpret_cast<const f32x4 *>(r + place(row, 2 * k8) * 16);
-            const f32x4 b = *reinterpret_cast<const f32x4 *>(r + place(row, 2 * k8 + 1) * 16);
-            return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-        }
+        return *reinterpret_cast<const vec8<T> *>(s + row * kRowBytes + place(row, k8) * 16);
     }
 
     // Operand across the rows: lane l gets dim 32 n + l % 32 of rows 16 step + 4 half .. + 3 and 16 step + 8 + 4 half
-    // .. + 3 (half = l / 32), the order in which a 32-wide product leaves its results. 16-bit values are transposed by
+    // .. + 3 (half = l / 32), the order in which a 32-wide product leaves its results. The values are transposed by
     // the LDS read: of each 16 lanes, lanes 4 r .. 4 r + 3 point at 16 neighbouring values of row r, and lane i gets
     // the four rows' value i.
     __device__ static vec8<T> across(const char *s, int n, int step)
     {
+        typedef short s16x4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
         const int lane = threadIdx.x & 63, half = lane >> 5;
-        if constexpr (sizeof(T) == 2) {
-            typedef short s16x4 __attribute__((ext_vector_type(4)));
-            typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-            union { s16x4 part[2]; vec8<T> whole; } u;
-            const int i = lane & 15, group = (lane >> 4) & 1;
+        union { s16x4 part[2]; vec8<T> whole; } u;
+        const int i = lane & 15, group = (lane >> 4) & 1;
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int row = 16 * step + 8 * b + 4 * half + (i >> 2);
-                const int piece = 4 * n + 2 * group + ((i >> 1) & 1);
-                const char *at = s + row * kRowBytes + place(row, piece) * 16 + (i & 1) * 8;
-                u.part[b] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at);
-            }
-            return u.whole;
-        } else {
-            vec8<T> x;
-            const int dim = 32 * n + (lane & 31);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int row = 16 * step + 8 * (e >> 2) + 4 * half + (e & 3);
-                x[e] = *reinterpret_cast<const float *>(s + row * kRowBytes + place(row, dim >> 2) * 16 + (dim & 3) * 4);
-            }
-            return x;
+        for (int b = 0; b < 2; ++b) {
+            const int row = 16 * step + 8 * b + 4 * half + (i >> 2);
+            const int piece = 4 * n + 2 * group + ((i >> 1) & 1);
+            const char *at = s + row * kRowBytes + place(row, piece) * 16 + (i & 1) * 8;
+            u.part[b] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at);
         }
+        return u.whole;
     }
 
-    // Values of the tile that are not finite become 0; or, as markers, they become 1 and all others 0. Every thread
-    // of the workgroup takes part, barriers are the caller's.
-    __device__ static void only_finite(char *s, bool markers)
+    // Value i of the tile, in no order of interest, and its rewriting.
+    __device__ static bool fine(const char *s, int i)
     {
-        T *x = reinterpret_cast<T *>(s);
-        for (int i = threadIdx.x; i < kTileRows * kD; i += 64 * kWaves) {
-            const float y = to_float(x[i]);
-            const bool fine = y - y == 0.0f;
-            x[i] = static_cast<T>(markers ? (fine ? 0.0f : 1.0f) : (fine ? y : 0.0f));
-        }
+        const float x = to_float(reinterpret_cast<const T *>(s)[i]);
+        return x - x == 0.0f;
     }
+    __device__ static void set(char *s, int i, float x) { reinterpret_cast<T *>(s)[i] = static_cast<T>(x); }
+};
+
+// 64 rows of float32 values, in three parts.
+template <int kD, int kWaves>
+struct SplitTile {
+    typedef Tile<bf16_t, kD, kWaves> Part;
+    static constexpr int kBytes = 3 * Part::kBytes;
+    static constexpr int kUnits = kTileRows * kD / 8 / (64 * kWaves);      // 8 values each a thread
+
+    // Rows on their way: fetch sets out, store puts their parts into the tile.
+    struct Loader {
+        f32x8 x[kUnits];
+        int64_t stride;
+
+        __device__ explicit Loader(int64_t row_stride) : stride(row_stride) {}
+        __device__ void fetch(const float *rows, int first, int end)
+        {
+#pragma unroll
+            for (int n = 0; n < kUnits; ++n) {
+                const int at = n * 64 * kWaves + threadIdx.x, row = at / (kD / 8), piece = at % (kD / 8);
+                x[n] = load8(rows + min(first + row, end - 1) * stride + 8 * piece);
+            }
+        }
+        __device__ void store(char *s) const
+        {
+#pragma unroll
+            for (int n = 0; n < kUnits; ++n) {
+                const int at = n * 64 * kWaves + threadIdx.x, row = at / (kD / 8), piece = at % (kD / 8);
+                const Split8 y(x[n]);
+                char *to = s + row * Part::kRowBytes + Part::place(row, piece) * 16;
+                *reinterpret_cast<bf16x8 *>(to) = y.high;
+                *reinterpret_cast<bf16x8 *>(to + Part::kBytes) = y.middle;
+                *reinterpret_cast<bf16x8 *>(to + 2 * Part::kBytes) = y.low;
+            }
+        }
+    };
+
+    __device__ static Split8 along(const char *s, int row, int k8)
+    {
+        Split8 x;
+        x.high = Part::along(s, row, k8);
+        x.middle = Part::along(s + Part::kBytes, row, k8);
+        x.low = Part::along(s + 2 * Part::kBytes, row, k8);
+        return x;
+    }
+    __device__ static Split8 across(const char *s, int n, int step)
+    {
+        Split8 x;
+        x.high = Part::across(s, n, step);
+        x.middle = Part::across(s + Part::kBytes, n, step);
+        x.low = Part::across(s + 2 * Part::kBytes, n, step);
+        return x;
+    }
+    // The first part of a value that is not finite is not finite either.
+    __device__ static bool fine(const char *s, int i) { return Part::fine(s, i); }
+    __device__ static void set(char *s, int i, float x)     // 0 or 1
+    {
+        Part::set(s, i, x);
+        Part::set(s + Part::kBytes, i, 0.0f);
+        Part::set(s + 2 * Part::kBytes, i, 0.0f);
+    }
+};
+
+template <typename T, int kD, int kWaves> struct RowsOf { typedef Tile<T, kD, kWaves> type; };
+template <int kD, int kWaves> struct RowsOf<float, kD, kWaves> { typedef SplitTile<kD, kWaves> type; };
+
+// Values of a tile that are not finite become 0; or, as markers, they become 1 and all others 0. Every thread of the
+// workgroup takes part, barriers are the caller's.
+template <typename Rows, int kD, int kThreads>
+__device__ inline void only_finite(char *s, bool markers)
+{
+    for (int i = threadIdx.x; i < kTileRows * kD; i += kThreads) {
+        const bool fine = Rows::fine(s, i);
+        if (markers) Rows::set(s, i, fine ? 0.0f : 1.0f);
+        else if (!fine) Rows::set(s, i, 0.0f);
+    }
+}
+
+// Rows of a tile with a value that is not finite: their flag is set and they become zeros. Barriers are the caller's.
+template <typename Rows, int kD, int kThreads>
+__device__ inline void clear_bad_rows(char *s, int *flags)
+{
+    constexpr int kLanes = kThreads / kTileRows;
+    const int row = threadIdx.x / kLanes;
+    bool bad = false;
+    for (int i = threadIdx.x % kLanes; i < kD; i += kLanes) bad = bad || !Rows::fine(s, row * kD + i);
+#pragma unroll
+    for (int m = 1; m < kLanes; m <<= 1) bad = __shfl_xor(static_cast<int>(bad), m) || bad;
+    if (bad) {
+        flags[row] = 1;
+        for (int i = threadIdx.x % kLanes; i < kD; i += kLanes) Rows::set(s, row * kD + i, 0.0f);
+    }
+}
+
+// Two arrays of rows (keys and values, or queries and gradients) that go by tile after tile. 16-bit: two tiles of each
+// in the LDS, one worked on, one on its way. Float32: one tile of each in the LDS, the next in registers.
+template <typename T, int kD, int kWaves>
+struct Feed {
+    typedef Tile<T, kD, kWaves> Rows;
+    static constexpr int kBytes = 4 * Rows::kBytes;
+    typename Rows::Loader one, two;
+    char *s;
+
+    __device__ Feed(char *memory, int64_t stride_one, int64_t stride_two) : one(stride_one), two(stride_two), s(memory) {}
+    __device__ void start(const T *rows_one, const T *rows_two, int first, int end) { load(0, rows_one, rows_two, first, end); }
+    // Waits for the tile in `buffer`; then `go` sets out for the next one. Nothing of the tile before is read any more.
+    template <int kBuffer>
+    __device__ void turn(Constant<kBuffer>, bool go, const T *rows_one, const T *rows_two, int first, int end)
+    {
+        wait_copies();
+        __syncthreads();
+        if (go) load(1 - kBuffer, rows_one, rows_two, first, end);
+    }
+    template <int kBuffer> __device__ char *tile_one(Constant<kBuffer>) const { return s + kBuffer * 2 * Rows::kBytes; }
+    template <int kBuffer> __device__ char *tile_two(Constant<kBuffer>) const { return s + (kBuffer * 2 + 1) * Rows::kBytes; }
+
+private:
+    __device__ void load(int buffer, const T *rows_one, const T *rows_two, int first, int end)
+    {
+        one.load(s + buffer * 2 * Rows::kBytes, rows_one, first, end);
+        two.load(s + (buffer * 2 + 1) * Rows::kBytes, rows_two, first, end);
+    }
+};
+
+template <int kD, int kWaves>
+struct Feed<float, kD, kWaves> {
+    typedef SplitTile<kD, kWaves> Rows;
+    static constexpr int kBytes = 2 * Rows::kBytes;
+    typename Rows::Loader one, two;
+    char *s;
+
+    __device__ Feed(char *memory, int64_t stride_one, int64_t stride_two) : one(stride_one), two(stride_two), s(memory) {}
+    __device__ void start(const float *rows_one, const float *rows_two, int first, int end)
+    {
+        one.fetch(rows_one, first, end);
+        two.fetch(rows_two, first, end);
+    }
+    template <int kBuffer>
+    __device__ void turn(Constant<kBuffer>, bool go, const float *rows_one, const float *rows_two, int first, int end)
+    {
+        wait_copies();
+        __syncthreads();
+        one.store(s);
+        two.store(s + Rows::kBytes);
+        __syncthreads();
+        if (go) start(rows_one, rows_two, first, end);
+    }
+    template <int kBuffer> __device__ char *tile_one(Constant<kBuffer>) const { return s; }
+    template <int kBuffer> __device__ char *tile_two(Constant<kBuffer>) const { return s + Rows::kBytes; }
 };
 
 }  // namespace rvq
