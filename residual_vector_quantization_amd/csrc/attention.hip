@@ -5,6 +5,10 @@
 //
 // Bound by the matrix cores, the LDS reads that feed them and the exponentials,
 // all of about the same weight: 4 dim flops, 1 exponential a pair.
+// Measured: 16384 queries, window 4096, 4 sinks, 16 heads of 128 over 4, bfloat16:
+// 534 us, 980 TFLOP/s, where a large library product reaches 1250 (both at a
+// clock that the power limit brings to about 1.9 GHz); matrix cores busy in 49%
+// of the cycles, no LDS bank conflicts.
 // A workgroup takes 128 queries of one head and clip, 32 a wavefront, and goes
 // once over the keys they see: the sinks' tiles, then the window's, 64 keys a
 // tile. With transposed products a lane keeps to one query:
@@ -14,6 +18,10 @@
 // the scores that a lane holds are, in order, the P^T operand of the second
 // product: the keys of a V^T operand are numbered as the scores come out.
 // While one tile is worked on, the next is on its way from global memory.
+// Steps, on that case: one wavefront a row 95.5 ms; matrix products with V
+// transposed in registers 0.81; V read across its rows in the LDS, rows copied
+// there directly 0.68; copies from a scalar base address 0.60; a whole tile
+// between branches 0.55; the queries' loads waited for before the loop 0.53.
 #include <float.h>
 #include <limits.h>
 #include <stdint.h>

@@ -12,6 +12,11 @@
 // Bound by the matrix cores and the LDS reads that feed them, as in the
 // forward pass, with the same operand layouts: a lane keeps to one query (dq)
 // or one key (dk, dv), and what a product leaves in it is the next one's operand.
+// Measured: two clips of up to 8192 frames, window 750, 4 sinks, 16 heads of 128
+// over 4, bfloat16: dq 206 us (matrix cores busy 32% of the cycles), dk and dv
+// 286 us (28%; accumulators and operands take 400 registers, so 1 wavefront a
+// SIMD, and exponentials are not hidden behind another's products), sinks 6 us.
+// 8 clips of 2000 frames, all seen, 16 heads of 64 over 8, float16: 145 and 224 us.
 //
 // Weights and dx enter the products in the inputs' type. bfloat16 has float32's
 // range, but float16 has 5 bits of exponent, so there weights are taken times
