@@ -212,7 +212,8 @@ def random_tables(rng, clips, cols, pages, page):
 
 
 @pytest.mark.parametrize("clips,cols,pages,page", [(1, 1, 1, 1), (3, 4, 9, 16), (40, 7, 200, 8), (300, 9, 2100, 4),
-                                                   (700, 20, 9000, 3), (5, 3, 70000, 2)])
+                                                   (700, 20, 9000, 3), (5, 3, 70000, 2),
+                                                   (4500, 2, 7000, 2)])
 def test_reserve_free_fork_compact(clips, cols, pages, page):
     m = rvq()
     rng = random.Random(clips * 1000 + pages)
