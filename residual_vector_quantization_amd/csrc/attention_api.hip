@@ -142,8 +142,7 @@ RVQ_API int64_t rvq_window_attention_backward_bytes(const rvq_attention_shape *s
 {
     const rvq_status st = check_attention(shape);
     if (st != RVQ_OK) return st;
-    return rvq::window_attention_backward_bytes(shape->q_tokens, shape->k_tokens, shape->n_clips, shape->q_heads,
-                                                shape->kv_heads, shape->dim, shape->sinks);
+    return rvq::window_attention_backward_bytes(attention_args(shape));
 }
 
 RVQ_API rvq_status rvq_window_attention_backward(const rvq_attention_shape *shape, const rvq_heads *dout,

@@ -31,6 +31,10 @@
 // the keys' gradients as well. Small windows in float16, error of dq and dk over that of
 // a correct result rounded once: 1.52 without, 1.41 with (two roundings).
 //
+// Where keys and key heads make few workgroups, the query heads of a key head
+// are shared out among several (parts_of), and a third launch adds their float32
+// sums in order.
+//
 // The first sinks of a clip are seen by all of its later queries, hundreds of
 // tiles where other keys have a window's. When that matters (see split_sinks)
 // the queries beyond the window go in pieces of kFarRows to workgroups of their
@@ -65,6 +69,8 @@ struct Work {
     float *near;             // [n_clips][kv_heads]
     float *far;              // [far slots][kv_heads][2]
     bool split;
+    float *part;                   // [parts][k_tokens][kv_heads] where parts > 1, laid out as near
+    int parts;
 };
 
 int64_t rounded(int64_t floats) { return (floats + 3) / 4 * 4; }
@@ -78,13 +84,33 @@ bool split_sinks(int64_t q_tokens, int n_clips, int sinks)
     return sinks > 0 && sinks <= kMaxSplitSinks && q_tokens >= static_cast<int64_t>(n_clips) * kLongClip;
 }
 
+int64_t k_slots(int64_t k_tokens, int n_clips) { return k_tokens / kRows + n_clips + 1; }
+
+// Among how many workgroups the query heads of a key head are shared out: as many as fill the chip's 256 CUs twice, if
+// each has some 32 tiles of queries to go over (a float32 tile counts as 3); otherwise the additional launch (4 us, and
+// as much for the sums) is not made up for. Forward and gradient, us: 8 query heads over 1 of 64, 1500 frames, 295 ->
+// 99; 4 clips of up to 600, 8 heads over 1 of 128, 207 -> 85; 8 clips of up to 300, 8 over 4 of 64, 43 against 55 if
+// shared. Not where the sinks are split off.
+int parts_of(const AttentionArgs &a)
+{
+    if (split_sinks(a.q_tokens, a.n_clips, a.sinks) || a.n_clips == 0) return 1;
+    const int group = a.q_heads / a.kv_heads;
+    const int64_t length = a.k_tokens / a.n_clips, seen = static_cast<int64_t>(a.window) + kRows;
+    const int64_t tiles = ((length < seen ? length : seen) / kTileRows + 1) * group;
+    if (tiles * (a.dtype == RVQ_F32 ? 3 : 1) < 32) return 1;
+    const int64_t n = 512 / (k_slots(a.k_tokens, a.n_clips) * a.kv_heads);
+    return n < 2 ? 1 : n < group ? static_cast<int>(n) : group;
+}
+
 int64_t q_slots(int64_t q_tokens, int n_clips) { return q_tokens / kRows + n_clips + 1; }
 
-int64_t work_floats(int64_t q_tokens, int n_clips, int q_heads, int kv_heads, int dim, int sinks)
+int64_t work_floats(const AttentionArgs &a)
 {
-    int64_t n = 2 * rounded(q_tokens * q_heads) + rounded(q_slots(q_tokens, n_clips) * q_heads);
-    if (split_sinks(q_tokens, n_clips, sinks))
-        n += (n_clips + 2 * far_slots(q_tokens, n_clips)) * kv_heads * sinks * dim * 2;
+    int64_t n = 2 * rounded(a.q_tokens * a.q_heads) + rounded(q_slots(a.q_tokens, a.n_clips) * a.q_heads);
+    if (split_sinks(a.q_tokens, a.n_clips, a.sinks))
+        n += (a.n_clips + 2 * far_slots(a.q_tokens, a.n_clips)) * a.kv_heads * a.sinks * a.dim * 2;
+    const int parts = parts_of(a);
+    if (parts > 1) n += parts * a.k_tokens * a.kv_heads * a.dim * 2;
     return n;
 }
 
@@ -99,6 +125,8 @@ Work work_of(const AttentionArgs &a)
     w.near = w.largest + rounded(parts);
     w.far = w.near + static_cast<int64_t>(a.n_clips) * a.kv_heads * a.sinks * a.dim * 2;
     w.split = a.window != INT_MAX && split_sinks(a.q_tokens, a.n_clips, a.sinks);
+    w.part = w.near;               // never both
+    w.parts = parts_of(a);
     return w;
 }
 
@@ -292,7 +320,9 @@ __device__ inline void dkv_group(const AttentionArgs &a, const Work &work, float
     typedef typename Queries::Rows Rows;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 31, half = lane >> 5;
-    const int slot = block / a.kv_heads, kv = block % a.kv_heads, group = a.q_heads / a.kv_heads;
+    const int parts = kFar ? 1 : work.parts, part = block % parts;
+    const int slot = block / parts / a.kv_heads, kv = block / parts % a.kv_heads, group = a.q_heads / a.kv_heads;
+    const int first_head = kv * group + group * part / parts, heads = kv * group + group * (part + 1) / parts - first_head;
     const int32_t *cu = kFar ? a.cu_q : a.cu_k;
     constexpr int kPer = kFar ? kFarRows : kRows;
     const int clip = clip_of_slot(cu, a.n_clips, slot, kPer);
@@ -322,7 +352,7 @@ __device__ inline void dkv_group(const AttentionArgs &a, const Work &work, float
     }
     const int i_start = i_first / kTileRows * kTileRows;
     const int per_head = i_end > i_first ? (i_end - i_start + kTileRows - 1) / kTileRows : 0;
-    const int tiles = per_head * group;
+    const int tiles = per_head * heads;
     const int key_first = __builtin_amdgcn_readfirstlane(key - c), key_last = key_first + 31;
     // below this position all of the wavefront's keys are seen, from the other on none
     int hi_all = hi, hi_any = hi;
@@ -475,7 +505,7 @@ __device__ inline void dkv_group(const AttentionArgs &a, const Work &work, float
         }
     };
     auto pass = [&](auto second) {
-        head = kv * group;
+        head = first_head;
         i = i_start;
         if (tiles > 0) {
             feed.start(queries + head * a.q.head, slopes_of + head * a.dout.head, i, nq);
@@ -505,11 +535,12 @@ __device__ inline void dkv_group(const AttentionArgs &a, const Work &work, float
         for (int r = 0; r < 16; ++r) odd = odd || not_finite(dk[n][r]) || not_finite(dv[n][r]);
     if (__syncthreads_or(odd)) pass(Constant<1>{});
     if (key >= nk) return;
-    if (kFar || (work.split && key < a.sinks)) {
-        if (key >= a.sinks) return;
+    if (kFar || parts > 1 || (work.split && key < a.sinks)) {
+        if (kFar && key >= a.sinks) return;
         const int64_t which = kFar ? (static_cast<int64_t>(slot) * a.kv_heads + kv) * 2 + (wave & 1)
                                    : static_cast<int64_t>(clip) * a.kv_heads + kv;
-        float *to = (kFar ? work.far : work.near) + (which * a.sinks + key) * 2 * kD;
+        float *to = parts > 1 ? work.part + ((part * a.k_tokens + k0 + key) * a.kv_heads + kv) * 2 * kD
+                              : (kFar ? work.far : work.near) + (which * a.sinks + key) * 2 * kD;
 #pragma unroll
         for (int n = 0; n < kD / 32; ++n)
 #pragma unroll
@@ -550,6 +581,36 @@ void dkv_tiles(AttentionArgs a, Work work, float factor, int near_groups)
     else dkv_group<T, kD, true>(a, work, factor, block - near_groups, s_mem, s_stats, s_bad);
 }
 
+// The parts' sums: a workgroup takes kJoinRows of the 128 keys that those of dkv_group took, a thread 4 values at a time.
+constexpr int kJoinRows = 16;
+
+template <typename T, int kD>
+__global__ __launch_bounds__(kThreads)
+void join_parts(AttentionArgs a, Work work)
+{
+    const int slot = blockIdx.x / a.kv_heads, kv = blockIdx.x % a.kv_heads;
+    const int clip = clip_of_slot(a.cu_k, a.n_clips, slot, kRows);
+    int k0, nk;
+    clip_range(a.cu_k, clip, a.k_tokens, k0, nk);
+    const int tile = (slot - (a.cu_k[clip] / kRows + clip)) * kRows, first = tile + blockIdx.y * kJoinRows;
+    if (tile < 0 || first >= nk) return;
+    constexpr int kFours = 2 * kD / 4;
+    for (int at = threadIdx.x; at < min(kJoinRows, nk - first) * kFours; at += kThreads) {
+        const int64_t row = k0 + first + at / kFours;
+        const int d = at % kFours * 4;      // below kD: dk, others dv
+        f32x4 sum = {};
+#pragma unroll 4
+        for (int part = 0; part < work.parts; ++part)
+            sum += *reinterpret_cast<const f32x4 *>(work.part + ((part * a.k_tokens + row) * a.kv_heads + kv) * 2 * kD + d);
+        if (d < kD) sum *= a.scale;
+        T y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = static_cast<T>(sum[i]);
+        if (d < kD) store4(static_cast<T *>(a.dk.data) + row * a.dk.token + kv * a.dk.head + d, y);
+        else store4(static_cast<T *>(a.dv.data) + row * a.dv.token + kv * a.dv.head + d - kD, y);
+    }
+}
+
 // The sinks' gradients: the part within the first keys' window, then the pieces beyond it in order.
 template <typename T, int kD>
 __global__ __launch_bounds__(2 * kD)
@@ -583,7 +644,7 @@ hipError_t backward(const AttentionArgs &a, hipStream_t stream)
     const float factor = fmaxf(a.scale * kLog2e, FLT_MIN);     // as in the forward pass
     const int64_t q_groups = q_slots(a.q_tokens, a.n_clips) * a.q_heads;
     const int64_t far_groups = work.split ? far_slots(a.q_tokens, a.n_clips) * a.kv_heads : 0;
-    const int64_t near_groups = (a.k_tokens / kRows + a.n_clips + 1) * a.kv_heads;
+    const int64_t key_groups = k_slots(a.k_tokens, a.n_clips) * a.kv_heads, near_groups = key_groups * work.parts;
     if (q_groups > INT_MAX || near_groups + far_groups > INT_MAX) return hipErrorInvalidConfiguration;
     if (a.q_tokens > 0)
         dq_tiles<T, kD><<<static_cast<unsigned>(q_groups), kThreads, 0, stream>>>(
@@ -591,6 +652,7 @@ hipError_t backward(const AttentionArgs &a, hipStream_t stream)
     if (a.k_tokens > 0) {
         dkv_tiles<T, kD><<<static_cast<unsigned>(near_groups + far_groups), kThreads, 0, stream>>>(
             a, work, factor, static_cast<int>(near_groups));
+        if (work.parts > 1) join_parts<T, kD><<<dim3(static_cast<unsigned>(key_groups), kRows / kJoinRows), kThreads, 0, stream>>>(a, work);
         if (work.split)
             join_sinks<T, kD><<<dim3(a.sinks, a.kv_heads, a.n_clips < 1024 ? a.n_clips : 1024), 2 * kD, 0, stream>>>(a, work);
     }
@@ -599,11 +661,7 @@ hipError_t backward(const AttentionArgs &a, hipStream_t stream)
 
 }  // namespace
 
-int64_t window_attention_backward_bytes(int64_t q_tokens, int64_t k_tokens, int n_clips, int q_heads, int kv_heads,
-                                        int dim, int sinks)
-{
-    return work_floats(q_tokens, n_clips, q_heads, kv_heads, dim, sinks) * 4;
-}
+int64_t window_attention_backward_bytes(const AttentionArgs &a) { return work_floats(a) * 4; }
 
 hipError_t launch_window_attention_backward(const AttentionArgs &a, hipStream_t stream)
 {

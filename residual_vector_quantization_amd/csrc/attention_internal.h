@@ -40,8 +40,7 @@ struct CacheAttentionArgs {
 };
 
 hipError_t launch_window_attention(const AttentionArgs &a, hipStream_t stream);
-int64_t window_attention_backward_bytes(int64_t q_tokens, int64_t k_tokens, int n_clips, int q_heads, int kv_heads,
-                                        int dim, int sinks);
+int64_t window_attention_backward_bytes(const AttentionArgs &a);     // of the shape alone
 hipError_t launch_window_attention_backward(const AttentionArgs &a, hipStream_t stream);
 
 int64_t cache_attention_bytes(int n_clips, int q_heads, int kv_heads, int dim, int64_t capacity);

@@ -118,6 +118,14 @@ def test_sinks_of_long_clips(typ, dim, q_lens, k_lens, window, sinks):
     check(typ, dim, 2, 1, q_lens, k_lens, window=window, sinks=sinks)
 
 
+@pytest.mark.parametrize("typ,dim,hq,hk,q_lens,k_lens,window", [
+    ("bf16", 64, 8, 1, [700], None, None), ("fp16", 128, 7, 1, [500, 0, 333], None, None), ("fp32", 64, 5, 1, [300], [380], 90),
+    ("bf16", 128, 12, 2, [450, 130], None, 300)])
+def test_query_heads_shared_out(typ, dim, hq, hk, q_lens, k_lens, window):
+    """Few key heads and clips: several workgroups share the query heads of a key head."""
+    check(typ, dim, hq, hk, q_lens, k_lens, window=window, sinks=2)
+
+
 def test_large_scores_and_other_scales():
     check("bf16", 64, 2, 1, [140], scale=3.0, train=False)
     check("fp32", 64, 2, 1, [140], scale=0.0)
