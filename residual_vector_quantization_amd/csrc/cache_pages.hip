@@ -622,8 +622,9 @@ hipError_t launch_cache_free(const int32_t *table, const int32_t *lens, const in
         return hipGetLastError();
     }
     if (n_pages > 0) copy_ints<<<ceil_div(n_pages, kThreads), kThreads, 0, stream>>>(refs, refs_out, n_pages);
-    free_entries<<<ceil_div(items, kThreads), kThreads, 0, stream>>>(table, n_clips, table_ld, n_pages, leaves, table_out,
-                                                                     lens_out, refs_out);
+    if (items > 0)
+        free_entries<<<ceil_div(items, kThreads), kThreads, 0, stream>>>(table, n_clips, table_ld, n_pages, leaves,
+                                                                         table_out, lens_out, refs_out);
     return hipGetLastError();
 }
 
