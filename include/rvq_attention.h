@@ -185,10 +185,13 @@ RVQ_API rvq_status rvq_cache_attention(const rvq_cache_shape *shape, int32_t q_h
  * or another output. workspace: at least rvq_cache_scratch_bytes(n_clips,
  * n_pages) bytes, 16-byte aligned.
  *
- * rvq_cache_reserve gives every clip the pages for positions lens[b] ..
- * new_lens[b] - 1, in order of clips and positions. missing [1] int32
- * counts the pages that were wanted and not there (none free, or a position
- * beyond the table); their entries stay -1.
+ * rvq_cache_reserve gives every clip pages for positions lens[b] ..
+ * new_lens[b] - 1, in order of clips and positions, in the columns behind
+ * that of position lens[b] - 1. Columns that name a page keep it, so pages
+ * may be reserved ahead, and a call that found too few may be made again with
+ * its results. missing [1] int32 counts the pages that were wanted and not
+ * there (none free, or a position beyond the table); their entries stay as
+ * they were.
  *
  * rvq_cache_fork lets clip children[c] go on from clip parents[c], for all c
  * at once (the step of a beam search when children are all clips). The child

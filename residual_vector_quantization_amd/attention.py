@@ -344,10 +344,11 @@ def _scratch(table: torch.Tensor, refs: torch.Tensor) -> torch.Tensor:
 
 def rvq_cache_reserve(table: torch.Tensor, lens: torch.Tensor, new_lens: torch.Tensor, refs: torch.Tensor,
                       page_size: int):
-    """Gives every clip the pages for positions ``lens[b]`` .. ``new_lens[b] - 1``, lowest free pages first.
+    """Gives every clip pages for positions ``lens[b]`` .. ``new_lens[b] - 1``, lowest free pages first; pages that it
+    was given for them before (reserved ahead) stay.
 
     ``table`` [clips, E], ``lens``, ``new_lens`` [clips], ``refs`` [pages], all int32. Returns ``(table, refs,
-    missing [1])``; ``missing`` counts the pages that were not there (their entries stay -1).
+    missing [1])``; ``missing`` counts the pages that were not there (their entries stay as they were).
     """
     _require_table(table, lens, table.device, refs)
     _require(new_lens, "new_lens", torch.int32, 1, table.device)

@@ -145,18 +145,26 @@ __device__ inline int used_before(const int32_t *refs, int n_pages, const int32_
 
 // What a fork or a reserve wants of the free pages.
 struct Wanted {
-    const int32_t *lens, *new_lens;             // reserve
+    const int32_t *table, *lens, *new_lens;     // reserve (table and lens: fork too)
     const int32_t *parents, *children;          // fork (new_lens null)
     int n, n_clips, table_ld, page_size;        // n: clips (reserve) or children (fork)
+    int n_pages;
 
-    // pages that item i wants; past: those that would lie beyond the table
-    __device__ int of(int i, int &past) const
+    __device__ bool is_page(int page) const { return static_cast<unsigned>(page) < static_cast<unsigned>(n_pages); }
+
+    // reserve: the columns first .. first + count - 1 of clip i hold the positions asked for, `past` more lie beyond the
+    // table. Those of them that name a page already want none.
+    __device__ int columns(int i, int &first, int &past) const
     {
-        if (new_lens) {
-            const int had = pages_for(lens[i], page_size), want = pages_for(new_lens[i], page_size);
-            past += max(0, want - max(had, table_ld));
-            return max(0, min(want, table_ld) - had);
-        }
+        const int want = pages_for(new_lens[i], page_size);
+        first = pages_for(lens[i], page_size);
+        past = max(0, want - max(first, table_ld));
+        return max(0, min(want, table_ld) - first);
+    }
+
+    // fork: pages that item i wants
+    __device__ int of(int i) const
+    {
         const int parent = parents[i], child = children[i];
         if (static_cast<unsigned>(parent) >= static_cast<unsigned>(n_clips) ||
             static_cast<unsigned>(child) >= static_cast<unsigned>(n_clips))
@@ -166,30 +174,49 @@ struct Wanted {
     }
 };
 
-// All that is wanted, by the whole workgroup.
-__device__ inline int total_wanted(const Wanted &w, int *s_wave)
-{
-    int sum = 0, past = 0, total;
-    for (int i = threadIdx.x; i < w.n; i += kThreads) sum += w.of(i, past);
-    block_exclusive(sum, total, s_wave);
-    return total;
-}
-
 // Scratch totals: pages wanted in the table, wanted beyond it, free; compact: pages in use, moves.
 enum Total { kInTable = 0, kBeyond = 1, kFree = 2, kLive = 0, kMoves = 1 };
 
-// base[i] = pages wanted before item i, and the totals; one workgroup.
+// base[i] = pages wanted before item i, i <= w.n, and the totals; one workgroup. A reserve's threads share out the
+// columns asked for, of kThreads clips at a time: one clip may ask for one column or thousands.
 __device__ inline void rank_wanted(const Wanted &w, int32_t *base, int32_t *totals, int *s_wave)
 {
+    __shared__ int s_before[kThreads], s_column[kThreads], s_there[kThreads];
     int before = 0, past = 0, total;
     for (int i0 = 0; i0 < w.n; i0 += kThreads) {
         const int i = i0 + threadIdx.x;
-        const int rank = block_exclusive(i < w.n ? w.of(i, past) : 0, total, s_wave);
+        int wants = 0;
+        if (w.new_lens) {
+            int first = 0, beyond = 0, all;
+            if (i < w.n) wants = w.columns(i, first, beyond);
+            past += beyond;
+            s_before[threadIdx.x] = block_exclusive(wants, all, s_wave);
+            s_column[threadIdx.x] = first;
+            s_there[threadIdx.x] = 0;
+            __syncthreads();
+#pragma unroll 4
+            for (int at = threadIdx.x; at < all; at += kThreads) {
+                int lo = 0, hi = min(kThreads, w.n - i0);      // the last clip with s_before <= at
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (s_before[mid] <= at) lo = mid;
+                    else hi = mid;
+                }
+                if (w.is_page(w.table[static_cast<int64_t>(i0 + lo) * w.table_ld + s_column[lo] + at - s_before[lo]]))
+                    atomicAdd(&s_there[lo], 1);
+            }
+            __syncthreads();
+            wants -= s_there[threadIdx.x];
+        } else if (i < w.n) {
+            wants = w.of(i);
+        }
+        const int rank = block_exclusive(wants, total, s_wave);
         if (i < w.n) base[i] = before + rank;
         before += total;
     }
     block_exclusive(past, total, s_wave);
     if (threadIdx.x == 0) {
+        base[w.n] = before;
         totals[kInTable] = before;
         totals[kBeyond] = total;
     }
@@ -202,9 +229,9 @@ void rank_wanted_alone(Wanted w, int32_t *__restrict__ base, int32_t *__restrict
     rank_wanted(w, base, totals, s_wave);
 }
 
-// First launch of reserve and fork. Workgroups 0 .. n_chunks - 1: free pages in order -> list (as many as are
-// wanted), and refs_out with those taken. The next one ranks what is wanted, unless that has been done (counted).
-// Those that are left copy the n_copies pairs of arrays for fork.
+// First launch of reserve and fork. Workgroups 0 .. n_chunks - 1: free pages in order -> list, and refs_out = refs (the
+// second launch enters the pages that it takes). The next one ranks what is wanted, unless that has been done (counted).
+// Those that are left copy the pairs of arrays for fork.
 struct IntCopy {
     const int32_t *from;
     int32_t *to;
@@ -226,11 +253,9 @@ void take_free(const int32_t *__restrict__ refs, int n_pages, int n_chunks, cons
     }
     if (chunk == n_chunks) {
         if (!counts) rank_wanted(w, base, totals, s_wave);
-        const int used = used_below(refs, counts, n_pages, s_wave);
-        if (threadIdx.x == 0) totals[kFree] = n_pages - used;
+        if (n_chunks == 0 && threadIdx.x == 0) totals[kFree] = 0;
         return;
     }
-    const int take = counts ? totals[kInTable] : total_wanted(w, s_wave);
     const int64_t first = static_cast<int64_t>(chunk) * kChunk + threadIdx.x * kPerThread;
     int ref[kPerThread];
     int used = used_before(refs, n_pages, counts, chunk, first, ref, s_wave);
@@ -238,12 +263,11 @@ void take_free(const int32_t *__restrict__ refs, int n_pages, int n_chunks, cons
     for (int i = 0; i < kPerThread; ++i) {
         const int64_t p = first + i;
         if (p >= n_pages) break;
-        const int64_t rank = p - used;
-        const bool mine = ref[i] <= 0 && rank < take;
-        if (mine) list[rank] = static_cast<int32_t>(p);
-        refs_out[p] = mine ? 1 : ref[i];
+        if (ref[i] <= 0) list[p - used] = static_cast<int32_t>(p);
+        refs_out[p] = ref[i];
         used += ref[i] > 0;
     }
+    if (chunk == n_chunks - 1 && threadIdx.x == kThreads - 1) totals[kFree] = n_pages - used;
 }
 
 __device__ inline void write_missing(const int32_t *totals, int32_t *missing)
@@ -251,23 +275,27 @@ __device__ inline void write_missing(const int32_t *totals, int32_t *missing)
     *missing = max(0, totals[kInTable] - totals[kFree]) + totals[kBeyond];
 }
 
-// reserve, second launch: table_out = table with the wanted entries filled from the list of free pages; one thread an
-// entry.
+// reserve, second launch: table_out = table with the wanted entries filled from the list of free pages as far as it goes;
+// one thread an entry.
 __global__ __launch_bounds__(kThreads)
-void fill_table(const int32_t *__restrict__ table, const int32_t *__restrict__ lens,
-                const int32_t *__restrict__ new_lens, int n_clips, int table_ld, int page_size,
-                const int32_t *__restrict__ totals, const int32_t *__restrict__ base,
-                const int32_t *__restrict__ list, int32_t *__restrict__ table_out, int32_t *__restrict__ missing)
+void fill_table(Wanted w, const int32_t *__restrict__ totals, const int32_t *__restrict__ base,
+                const int32_t *__restrict__ list, int32_t *__restrict__ table_out, int32_t *__restrict__ refs_out,
+                int32_t *__restrict__ missing)
 {
     const int64_t at = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
     if (at == 0) write_missing(totals, missing);
-    if (at >= static_cast<int64_t>(n_clips) * table_ld) return;
-    const int b = static_cast<int>(at / table_ld), e = static_cast<int>(at - static_cast<int64_t>(b) * table_ld);
-    const int had = pages_for(lens[b], page_size), want = pages_for(new_lens[b], page_size);
-    int page = table[at];
-    if (e >= had && e < want) {
-        const int rank = base[b] + e - had;
-        if (rank < totals[kFree]) page = list[rank];
+    if (at >= static_cast<int64_t>(w.n) * w.table_ld) return;
+    const int b = static_cast<int>(at / w.table_ld), e = static_cast<int>(at - static_cast<int64_t>(b) * w.table_ld);
+    int first, past, page = w.table[at];
+    const int count = w.columns(b, first, past);
+    if (e >= first && e < first + count && !w.is_page(page)) {
+        int rank = base[b] + e - first;
+        if (base[b + 1] - base[b] < count)      // less those before it that are there
+            for (int64_t i = at - (e - first); i < at; ++i) rank -= w.is_page(w.table[i]);
+        if (rank < totals[kFree]) {
+            page = list[rank];
+            refs_out[page] = 1;
+        }
     }
     table_out[at] = page;
 }
@@ -307,8 +335,7 @@ void fork_rows(Wanted w, const int32_t *__restrict__ table, const int32_t *__res
     const int n_free = totals[kFree];
     // the child's page for the parent's partial one: its column, and the page
     auto part_of = [&](int c, int &column) {
-        int past = 0;
-        const bool part = w.of(c, past) != 0;
+        const bool part = w.of(c) != 0;
         column = part ? w.lens[w.parents[c]] / w.page_size : -1;
         return part && base[c] < n_free ? list[base[c]] : -1;
     };
@@ -337,8 +364,10 @@ void fork_rows(Wanted w, const int32_t *__restrict__ table, const int32_t *__res
         const int left = was[e];
         int page = from[e];
         if (static_cast<unsigned>(left) < static_cast<unsigned>(pools.n_pages)) atomicSub(&refs_out[left], 1);
-        if (e == own) page = fresh;
-        else if (static_cast<unsigned>(page) < static_cast<unsigned>(pools.n_pages)) atomicAdd(&refs_out[page], 1);
+        if (e == own) {
+            page = fresh;
+            if (fresh >= 0) refs_out[fresh] = 1;
+        } else if (static_cast<unsigned>(page) < static_cast<unsigned>(pools.n_pages)) atomicAdd(&refs_out[page], 1);
         to[e] = page;
     }
     if (threadIdx.x == 0) lens_out[child] = w.lens[parent];
@@ -574,11 +603,11 @@ hipError_t launch_cache_reserve(const int32_t *table, const int32_t *lens, const
                                 hipStream_t stream)
 {
     const Scratch s = scratch(workspace, n_clips, n_pages);
-    const Wanted w = {lens, new_lens, nullptr, nullptr, n_clips, n_clips, table_ld, page_size};
+    const Wanted w = {table, lens, new_lens, nullptr, nullptr, n_clips, n_clips, table_ld, page_size, n_pages};
     launch_take_free(refs, n_pages, w, s, s.sources, refs_out, IntCopy{}, IntCopy{}, stream);
     const int64_t entries = static_cast<int64_t>(n_clips) * table_ld;
-    fill_table<<<entries ? ceil_div(entries, kThreads) : 1, kThreads, 0, stream>>>(
-        table, lens, new_lens, n_clips, table_ld, page_size, s.totals, s.base, s.sources, table_out, missing);
+    fill_table<<<entries ? ceil_div(entries, kThreads) : 1, kThreads, 0, stream>>>(w, s.totals, s.base, s.sources,
+                                                                                   table_out, refs_out, missing);
     return hipGetLastError();
 }
 
@@ -590,14 +619,13 @@ hipError_t launch_cache_fork(const int32_t *table, const int32_t *lens, const in
 {
     const Scratch s = scratch(workspace, n_clips, n_pages);
     // new_lens null makes it a fork; a fork of no children still copies the arrays and reports nothing missing
-    const Wanted w = {lens, nullptr, parents, children, n_children, n_clips, table_ld, page_size};
+    const Wanted w = {table, lens, nullptr, parents, children, n_children, n_clips, table_ld, page_size, n_pages};
     const Pools pools = {static_cast<char *>(k_pool), static_cast<char *>(v_pool), n_pages, n_layers, page_bytes};
     launch_take_free(refs, n_pages, w, s, s.sources, refs_out,
                      IntCopy{table, table_out, static_cast<int64_t>(n_clips) * table_ld}, IntCopy{lens, lens_out, n_clips},
                      stream);
     if (n_children == 0) {
-        fill_table<<<1, kThreads, 0, stream>>>(nullptr, nullptr, nullptr, 0, 0, 1, s.totals, s.base, s.sources, nullptr,
-                                               missing);
+        fill_table<<<1, kThreads, 0, stream>>>(w, s.totals, s.base, s.sources, table_out, refs_out, missing);
         return hipGetLastError();
     }
     const int64_t jobs = static_cast<int64_t>(n_children) * n_layers * 2;

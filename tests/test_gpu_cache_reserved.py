@@ -30,3 +30,78 @@ def test_free_without_clips(pages):
     refs = (torch.arange(pages, device=DEV) % 3).int()
     got = m.rvq_cache_free(table, none, refs, 16)
     assert got[0].shape == (0, 4) and got[1].shape == (0,) and torch.equal(got[2], refs)
+
+
+# ---------------------------------------------------------------- reserve
+
+def reserved(table, lens, new_lens, refs, page):
+    """The account of a reserve: in the columns of positions lens .. new_lens - 1, entries that name no page get one."""
+    table, refs = [list(r) for r in table], list(refs)
+    pages = len(refs)
+    free, missing = [p for p, n in enumerate(refs) if n <= 0], 0
+    for row, had, want in zip(table, lens, new_lens):
+        for e in range(-(-max(had, 0) // page), -(-max(want, 0) // page)):
+            if e < len(row) and 0 <= row[e] < pages:
+                continue
+            if e >= len(row) or not free:
+                missing += 1
+                continue
+            row[e] = free.pop(0)
+            refs[row[e]] = 1
+    return table, refs, missing
+
+
+def test_pages_reserved_ahead_stay():
+    m = rvq()
+    table, lens = [[0, -1, -1, -1], [-1, -1, -1, -1], [1, 2, -1, -1]], ints([3, 0, 8])
+    refs = ints(counted(table, 12))
+    held = [[0, 3, 4, -1], [5, 6, -1, -1], [1, 2, -1, -1]]
+    table, refs, missing = m.rvq_cache_reserve(ints(table), lens, ints([9, 5, 8]), refs, 4)
+    assert table.tolist() == held and refs.tolist() == counted(held, 12) and missing.item() == 0
+    # the same again, before any frame has been written
+    table, refs, missing = m.rvq_cache_reserve(table, lens, ints([9, 5, 8]), refs, 4)
+    assert table.tolist() == held and refs.tolist() == counted(held, 12) and missing.item() == 0
+    # and further ahead
+    held = [[0, 3, 4, 7], [5, 6, -1, -1], [1, 2, 8, 9]]
+    table, refs, missing = m.rvq_cache_reserve(table, lens, ints([13, 5, 16]), refs, 4)
+    assert table.tolist() == held and refs.tolist() == counted(held, 12) and missing.item() == 0
+
+
+def test_a_reserve_that_found_too_few_pages_is_taken_up_again():
+    m = rvq()
+    table, lens, new = [[-1, -1, -1], [-1, -1, -1], [1, 4, -1]], ints([0, 0, 8]), ints([12, 8, 8])
+    refs = ints(counted(table, 6))
+    table, refs, missing = m.rvq_cache_reserve(ints(table), lens, new, refs, 4)
+    assert table.tolist() == [[0, 2, 3], [5, -1, -1], [1, 4, -1]] and missing.item() == 1
+    table, lens, refs = m.rvq_cache_free(table, lens, refs, 4, drop=ints([0, 0, 1]))
+    held = [[0, 2, 3], [5, 1, -1], [-1, -1, -1]]
+    table, refs, missing = m.rvq_cache_reserve(table, lens, ints([12, 8, 0]), refs, 4)
+    assert table.tolist() == held and refs.tolist() == counted(held, 6) and missing.item() == 0
+
+
+@pytest.mark.parametrize("clips,cols,pages,page", [(1, 1, 1, 1), (1, 700, 900, 3), (7, 5, 40, 16), (300, 9, 2100, 4),
+                                                   (20, 130, 70000, 2), (4500, 4, 9000, 2)])
+def test_reserve_among_pages_that_are_there(clips, cols, pages, page):
+    """Some columns beyond the count already name a page, some name none or something that is no page."""
+    m = rvq()
+    g = torch.Generator().manual_seed(clips + pages)
+    for turn in range(3):
+        announce("reserve", clips=clips, cols=cols, pages=pages, page=page, turn=turn)
+        lens = torch.randint(0, cols * page + 1, (clips,), generator=g)
+        new = lens + torch.randint(0, 2 * page * min(cols, 8), (clips,), generator=g) * torch.randint(0, 2, (clips,), generator=g)
+        order = torch.randperm(pages, generator=g).tolist()
+        table, there = [], torch.rand(clips, cols, generator=g).tolist()
+        for b in range(clips):
+            row = []
+            for e in range(cols):
+                inside = e * page < lens[b]
+                if (inside or there[b][e] < 0.3) and order:
+                    row.append(order.pop())
+                else:
+                    row.append(-1 if there[b][e] < 0.8 else (pages, -5, 2 ** 31 - 1)[e % 3])
+            table.append(row)
+        refs = counted(table, pages)
+        want = reserved(table, lens.tolist(), new.tolist(), refs, page)
+        got = m.rvq_cache_reserve(ints(table), lens.int().to(DEV), new.int().to(DEV), ints(refs), page)
+        assert got[0].tolist() == want[0] and got[1].tolist() == want[1] and got[2].item() == want[2]
+        assert want[1] == counted(want[0], pages)
