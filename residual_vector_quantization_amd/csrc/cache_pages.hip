@@ -162,15 +162,20 @@ struct Wanted {
         return max(0, min(want, table_ld) - first);
     }
 
-    // fork: pages that item i wants
-    __device__ int of(int i) const
+    // fork: the partial page of item i's parent, to be copied, or -1 for none (full pages only, or none where it should
+    // be), and the column that it is in (-1: full pages only)
+    __device__ int partial(int i, int &column) const
     {
         const int parent = parents[i], child = children[i];
+        column = -1;
         if (static_cast<unsigned>(parent) >= static_cast<unsigned>(n_clips) ||
             static_cast<unsigned>(child) >= static_cast<unsigned>(n_clips))
-            return 0;
+            return -1;
         const int len = max(lens[parent], 0);
-        return len % page_size != 0 && len / page_size < table_ld;     // a partial page, to be copied
+        if (len % page_size == 0 || len / page_size >= table_ld) return -1;
+        column = len / page_size;
+        const int page = table[static_cast<int64_t>(parent) * table_ld + column];
+        return is_page(page) ? page : -1;
     }
 };
 
@@ -208,7 +213,8 @@ __device__ inline void rank_wanted(const Wanted &w, int32_t *base, int32_t *tota
             __syncthreads();
             wants -= s_there[threadIdx.x];
         } else if (i < w.n) {
-            wants = w.of(i);
+            int column;
+            wants = w.partial(i, column) >= 0;
         }
         const int rank = block_exclusive(wants, total, s_wave);
         if (i < w.n) base[i] = before + rank;
@@ -333,20 +339,15 @@ void fork_rows(Wanted w, const int32_t *__restrict__ table, const int32_t *__res
                int32_t *__restrict__ lens_out, int32_t *__restrict__ refs_out, int32_t *__restrict__ missing, Pools pools)
 {
     const int n_free = totals[kFree];
-    // the child's page for the parent's partial one: its column, and the page
-    auto part_of = [&](int c, int &column) {
-        const bool part = w.of(c) != 0;
-        column = part ? w.lens[w.parents[c]] / w.page_size : -1;
-        return part && base[c] < n_free ? list[base[c]] : -1;
-    };
+    // the child's page for the parent's partial one, -1 for none
+    auto copy_of = [&](int c, int source) { return source >= 0 && base[c] < n_free ? list[base[c]] : -1; };
     if (blockIdx.x >= static_cast<unsigned>(w.n)) {
         const int64_t jobs = static_cast<int64_t>(w.n) * pools.n_layers * 2, step = gridDim.x - w.n;
         for (int64_t job = blockIdx.x - w.n; job < jobs; job += step) {
             const int64_t pair = job / (2 * pools.n_layers);
             int column;
-            const int target = part_of(static_cast<int>(pair), column);
-            if (target >= 0)
-                pools.copy(job, pair, table[static_cast<int64_t>(w.parents[pair]) * w.table_ld + column], target);
+            const int source = w.partial(static_cast<int>(pair), column), target = copy_of(static_cast<int>(pair), source);
+            if (target >= 0) pools.copy(job, pair, source, target);
         }
         return;
     }
@@ -356,7 +357,7 @@ void fork_rows(Wanted w, const int32_t *__restrict__ table, const int32_t *__res
         static_cast<unsigned>(child) >= static_cast<unsigned>(w.n_clips))
         return;
     int own;
-    const int fresh = part_of(c, own);
+    const int fresh = copy_of(c, w.partial(c, own));
     const int32_t *from = table + static_cast<int64_t>(parent) * w.table_ld;
     const int32_t *was = table + static_cast<int64_t>(child) * w.table_ld;
     int32_t *to = table_out + static_cast<int64_t>(child) * w.table_ld;

@@ -105,3 +105,23 @@ def test_reserve_among_pages_that_are_there(clips, cols, pages, page):
         got = m.rvq_cache_reserve(ints(table), lens.int().to(DEV), new.int().to(DEV), ints(refs), page)
         assert got[0].tolist() == want[0] and got[1].tolist() == want[1] and got[2].item() == want[2]
         assert want[1] == counted(want[0], pages)
+
+
+# ---------------------------------------------------------------- fork
+
+@pytest.mark.parametrize("gone", [-1, 7, 2 ** 31 - 1, -2 ** 31])
+def test_a_fork_of_a_clip_whose_partial_page_is_not_there(gone):
+    """The child has no page there either: it does not get one with another clip's old frames."""
+    m = rvq()
+    page, pages = 4, 7
+    table, lens = [[1, gone, -1], [2, -1, -1], [-1, -1, -1], [-1, -1, -1]], [6, 3, 0, 0]
+    refs = counted(table, pages)
+    g = torch.Generator().manual_seed(1)
+    pools = [torch.randn(pages, 1, page, 64, generator=g).to(DEV) for _ in range(2)]
+    table, lens, refs, missing = m.rvq_cache_fork(ints(table), ints(lens), ints(refs), ints([0, 1]), ints([2, 3]), *pools)
+    held = [[1, gone, -1], [2, -1, -1], [1, -1, -1], [0, -1, -1]]
+    assert table.tolist() == held and refs.tolist() == counted(held, pages)
+    assert lens.tolist() == [6, 3, 6, 3] and missing.item() == 0
+    out = m.rvq_cache_attention(torch.ones(4, 1, 64, device=DEV), *pools, table, lens)
+    assert torch.isnan(out[0]).all() and torch.isnan(out[2]).all()
+    assert torch.isfinite(out[1]).all() and torch.equal(out[1], out[3])
