@@ -201,7 +201,8 @@ RVQ_API rvq_status rvq_cache_attention(const rvq_cache_shape *shape, int32_t q_h
  * children must be distinct. A pair with a clip outside [0, n_clips) is
  * skipped. missing [1] counts the children whose partial page found no room
  * (entry -1). Where the parent itself has no partial page the child has none
- * either (entry -1, not counted).
+ * either (entry -1, not counted). Pages that the parent has reserved ahead
+ * stay its own: the child's columns behind its frames are -1.
  *
  * rvq_cache_free lets go of all pages of the clips with drop[b] != 0 (NULL:
  * none), whose count becomes 0, and, with window >= 0, of the pages that no

@@ -163,17 +163,17 @@ struct Wanted {
     }
 
     // fork: the partial page of item i's parent, to be copied, or -1 for none (full pages only, or none where it should
-    // be), and the column that it is in (-1: full pages only)
-    __device__ int partial(int i, int &column) const
+    // be); full: the number of columns with full pages
+    __device__ int partial(int i, int &full) const
     {
         const int parent = parents[i], child = children[i];
-        column = -1;
+        full = 0;
         if (static_cast<unsigned>(parent) >= static_cast<unsigned>(n_clips) ||
             static_cast<unsigned>(child) >= static_cast<unsigned>(n_clips))
             return -1;
-        const int len = max(lens[parent], 0);
-        if (len % page_size == 0 || len / page_size >= table_ld) return -1;
-        column = len / page_size;
+        const int len = max(lens[parent], 0), column = len / page_size;
+        full = min(column, table_ld);
+        if (len % page_size == 0 || column >= table_ld) return -1;
         const int page = table[static_cast<int64_t>(parent) * table_ld + column];
         return is_page(page) ? page : -1;
     }
@@ -213,8 +213,8 @@ __device__ inline void rank_wanted(const Wanted &w, int32_t *base, int32_t *tota
             __syncthreads();
             wants -= s_there[threadIdx.x];
         } else if (i < w.n) {
-            int column;
-            wants = w.partial(i, column) >= 0;
+            int full;
+            wants = w.partial(i, full) >= 0;
         }
         const int rank = block_exclusive(wants, total, s_wave);
         if (i < w.n) base[i] = before + rank;
@@ -345,8 +345,8 @@ void fork_rows(Wanted w, const int32_t *__restrict__ table, const int32_t *__res
         const int64_t jobs = static_cast<int64_t>(w.n) * pools.n_layers * 2, step = gridDim.x - w.n;
         for (int64_t job = blockIdx.x - w.n; job < jobs; job += step) {
             const int64_t pair = job / (2 * pools.n_layers);
-            int column;
-            const int source = w.partial(static_cast<int>(pair), column), target = copy_of(static_cast<int>(pair), source);
+            int full;
+            const int source = w.partial(static_cast<int>(pair), full), target = copy_of(static_cast<int>(pair), source);
             if (target >= 0) pools.copy(job, pair, source, target);
         }
         return;
@@ -356,8 +356,8 @@ void fork_rows(Wanted w, const int32_t *__restrict__ table, const int32_t *__res
     if (static_cast<unsigned>(parent) >= static_cast<unsigned>(w.n_clips) ||
         static_cast<unsigned>(child) >= static_cast<unsigned>(w.n_clips))
         return;
-    int own;
-    const int fresh = copy_of(c, w.partial(c, own));
+    int full;
+    const int fresh = copy_of(c, w.partial(c, full));
     const int32_t *from = table + static_cast<int64_t>(parent) * w.table_ld;
     const int32_t *was = table + static_cast<int64_t>(child) * w.table_ld;
     int32_t *to = table_out + static_cast<int64_t>(child) * w.table_ld;
@@ -365,10 +365,12 @@ void fork_rows(Wanted w, const int32_t *__restrict__ table, const int32_t *__res
         const int left = was[e];
         int page = from[e];
         if (static_cast<unsigned>(left) < static_cast<unsigned>(pools.n_pages)) atomicSub(&refs_out[left], 1);
-        if (e == own) {
-            page = fresh;
-            if (fresh >= 0) refs_out[fresh] = 1;
-        } else if (static_cast<unsigned>(page) < static_cast<unsigned>(pools.n_pages)) atomicAdd(&refs_out[page], 1);
+        if (e >= full) {       // behind the full pages: the copy, and nothing that the parent has reserved ahead
+            page = e == full ? fresh : -1;
+            if (page >= 0) refs_out[page] = 1;
+        } else if (static_cast<unsigned>(page) < static_cast<unsigned>(pools.n_pages)) {
+            atomicAdd(&refs_out[page], 1);
+        }
         to[e] = page;
     }
     if (threadIdx.x == 0) lens_out[child] = w.lens[parent];

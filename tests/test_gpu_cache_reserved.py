@@ -2,6 +2,8 @@
 there, no clips at all. Accounts are written out by hand; after every operation a page's count is the number of
 table entries that name it."""
 
+import math
+
 import pytest
 import torch
 
@@ -125,3 +127,66 @@ def test_a_fork_of_a_clip_whose_partial_page_is_not_there(gone):
     out = m.rvq_cache_attention(torch.ones(4, 1, 64, device=DEV), *pools, table, lens)
     assert torch.isnan(out[0]).all() and torch.isnan(out[2]).all()
     assert torch.isfinite(out[1]).all() and torch.equal(out[1], out[3])
+
+
+def test_a_fork_does_not_share_pages_that_were_reserved_ahead():
+    m = rvq()
+    page, pages = 4, 9
+    table, lens = [[0, 1, 2], [3, 4, -1], [5, -1, -1], [-1, -1, -1]], [6, 4, 0, 0]
+    refs = counted(table, pages)
+    pools = [torch.full((pages, 1, page, 64), math.nan, device=DEV) for _ in range(2)]
+    for b, n in enumerate(lens):                    # frame j of clip b holds 100 b + j
+        for j in range(n):
+            for pool in pools:
+                pool[table[b][j // page], :, j % page] = 100 * b + j
+    table, lens, refs, missing = m.rvq_cache_fork(ints(table), ints(lens), ints(refs), ints([0, 1, 0]), ints([2, 3, 1]), *pools)
+    held = [[0, 1, 2], [0, 7, -1], [0, 6, -1], [3, -1, -1]]
+    assert table.tolist() == held and refs.tolist() == counted(held, pages)
+    assert lens.tolist() == [6, 6, 6, 4] and missing.item() == 0
+    # every clip goes on by four frames of its own
+    table, refs, missing = m.rvq_cache_reserve(table, lens, lens + 4, refs, page)
+    assert missing.item() == 0 and refs.tolist() == counted(table.tolist(), pages)
+    new = (1000 + torch.arange(16.0, device=DEV)).view(16, 1, 1).expand(16, 1, 64).contiguous()
+    m.rvq_cache_append(new, new, *pools, table, lens, ints([0, 4, 8, 12, 16]))
+    was = [[0, 1, 2, 3, 4, 5], [0, 1, 2, 3, 4, 5], [0, 1, 2, 3, 4, 5], [100, 101, 102, 103]]
+    rows = table.tolist()
+    for pool in pools:
+        for b, before in enumerate(was):
+            want = before + [1000 + 4 * b + i for i in range(4)]
+            assert [pool[rows[b][j // page], 0, j % page, 0].item() for j in range(len(want))] == want, b
+
+
+@pytest.mark.parametrize("clips,cols,pages,page", [(2, 3, 9, 1), (30, 9, 400, 4), (300, 5, 70000, 3), (4500, 3, 20000, 2)])
+def test_forks_of_tables_with_pages_ahead_and_pages_gone(clips, cols, pages, page):
+    m = rvq()
+    g = torch.Generator().manual_seed(clips)
+    for turn in range(2):
+        announce("fork", clips=clips, cols=cols, pages=pages, page=page, turn=turn)
+        lens = torch.randint(0, cols * page + 1, (clips,), generator=g).tolist()
+        order, luck = torch.randperm(pages, generator=g).tolist(), torch.rand(clips, cols, generator=g).tolist()
+        table = [[order.pop() if luck[b][e] < (0.8 if e * page < lens[b] else 0.4) else (-1, pages, -9)[e % 3]
+                  for e in range(cols)] for b in range(clips)]
+        refs = counted(table, pages)
+        parents = torch.randint(0, clips, (clips,), generator=g).tolist()
+        children = torch.randperm(clips, generator=g).tolist()
+        pools = [torch.arange(float(pages), device=DEV).view(pages, 1, 1, 1).expand(pages, 1, page, 64).contiguous() + x
+                 for x in (0, 0.25)]
+        before = [p.clone() for p in pools]
+        got = m.rvq_cache_fork(ints(table), ints(lens), ints(refs), ints(parents), ints(children), *pools)
+        free, want, copies, missing = [p for p, n in enumerate(refs) if n <= 0], [list(r) for r in table], [], 0
+        for p, c in zip(parents, children):
+            full, part = divmod(lens[p], page)
+            row = table[p][:full] + [-1] * (cols - full)
+            if part and 0 <= table[p][full] < pages:
+                if free:
+                    row[full] = free.pop(0)
+                    copies.append((table[p][full], row[full]))
+                else:
+                    missing += 1
+            want[c] = row
+        assert got[0].tolist() == want and got[1].tolist() == [lens[parents[children.index(c)]] for c in range(clips)]
+        assert got[2].tolist() == counted(want, pages) and got[3].item() == missing
+        for pool, old in zip(pools, before):
+            for s, t in copies:
+                old[t] = old[s]
+            assert torch.equal(pool, old)
