@@ -21,8 +21,9 @@
 // Weights and dx enter the products in the inputs' type. bfloat16 has float32's
 // range, but float16 has 5 bits of exponent, so there weights are taken times
 // 2^4 and dx is brought near 1 by powers of two: dq by its own row's largest
-// |dout|, dk by the whole call's (a sum over rows needs one factor); both leave
-// again in float32 at the end. Powers of two change no rounding.
+// |dout|, dk by that of the rows that its workgroup goes over (a sum over rows
+// needs one factor); both leave again in float32 at the end. Powers of two
+// change no rounding.
 //
 // delta comes from the rounded out. Its error enters dx as (1 / number of keys
 // that matter) of the size of dx's own rounding squared, so it shows only where
@@ -64,8 +65,8 @@ constexpr int kMaxSplitSinks = 64;
 // are 0) and -delta a query and head, then the float32 parts of the sinks' gradients, { dk, dv } [sinks][dim] each.
 struct Work {
     float *lse2, *minus_delta;     // [q_heads][q_tokens]
-    float *largest;          // [largest_parts] largest finite |dout| of each workgroup of dq_tiles (float16 only)
-    int largest_parts;
+    float *largest;          // [q_heads][q_slots] largest finite |dout| of each workgroup of dq_tiles (float16 only)
+    int q_slots;
     float *near;             // [n_clips][kv_heads]
     float *far;              // [far slots][kv_heads][2]
     bool split;
@@ -120,9 +121,8 @@ Work work_of(const AttentionArgs &a)
     w.lse2 = static_cast<float *>(a.workspace);
     w.minus_delta = w.lse2 + rounded(a.q_tokens * a.q_heads);
     w.largest = w.minus_delta + rounded(a.q_tokens * a.q_heads);
-    const int64_t parts = q_slots(a.q_tokens, a.n_clips) * a.q_heads;
-    w.largest_parts = a.q_tokens > 0 ? static_cast<int>(parts) : 0;
-    w.near = w.largest + rounded(parts);
+    w.q_slots = static_cast<int>(q_slots(a.q_tokens, a.n_clips));
+    w.near = w.largest + rounded(static_cast<int64_t>(w.q_slots) * a.q_heads);
     w.far = w.near + static_cast<int64_t>(a.n_clips) * a.kv_heads * a.sinks * a.dim * 2;
     w.split = a.window != INT_MAX && split_sinks(a.q_tokens, a.n_clips, a.sinks);
     w.part = w.near;               // never both
@@ -144,7 +144,7 @@ __device__ inline int exponent_of(float x) { return x == 0.0f || not_finite(x) ?
 // them as NaN, so that only those get it.
 template <typename T, int kD>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? (kD == 64 ? 3 : 2) : 1)
-void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
+void dq_tiles(AttentionArgs a, Work work, float factor)
 {
     typedef Feed<T, kD, kWaves> Keys;
     typedef typename Keys::Rows Rows;
@@ -152,17 +152,14 @@ void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
     __shared__ int s_bad[kTileRows];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 31, half = lane >> 5;
-    const int slot = slots - 1 - static_cast<int>(blockIdx.x / a.q_heads), head = blockIdx.x % a.q_heads;
+    const int slot = work.q_slots - 1 - static_cast<int>(blockIdx.x / a.q_heads), head = blockIdx.x % a.q_heads;
     const int kv = head / (a.q_heads / a.kv_heads);
     const int clip = clip_of_slot(a.cu_q, a.n_clips, slot, kRows);
     int q0, nq, k0, nk;
     clip_range(a.cu_q, clip, a.q_tokens, q0, nq);
     clip_range(a.cu_k, clip, a.k_tokens, k0, nk);
     const int i0 = (slot - (a.cu_q[clip] / kRows + clip)) * kRows;
-    if (i0 < 0 || i0 >= nq) {
-        if (kNarrow<T> && threadIdx.x == 0) work.largest[blockIdx.x] = 0.0f;
-        return;
-    }
+    if (i0 < 0 || i0 >= nq) return;
 
     const int back = nk - nq;
     const int row = i0 + 32 * wave + c;
@@ -214,7 +211,8 @@ void dq_tiles(AttentionArgs a, Work work, float factor, int slots)
         for (int m = 32; m > 0; m >>= 1) finite = fmaxf(finite, __shfl_xor(finite, m));
         s_top[wave] = finite;
         __syncthreads();
-        if (threadIdx.x == 0) work.largest[blockIdx.x] = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
+        if (threadIdx.x == 0)
+            work.largest[static_cast<int64_t>(head) * work.q_slots + slot] = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
     }
     Keys feed(s_mem, a.k.token, a.v.token);
     const T *keys = static_cast<const T *>(a.k.data) + static_cast<int64_t>(k0) * a.k.token + kv * a.k.head;
@@ -367,8 +365,14 @@ __device__ inline void dkv_group(const AttentionArgs &a, const Work &work, float
     // float16: dw - delta times `small`, weights times 2^kWeightShift
     float small = 1.0f, unit_k = 1.0f, unit_v = 1.0f;
     if constexpr (kNarrow<T>) {
+        // the rows gone over, in the slots that dq_tiles took them by
+        const int slot0 = q0 / kRows + clip + i_first / kRows, slots = per_head > 0 ? (i_end - 1) / kRows - i_first / kRows + 1 : 0;
         float top = 0.0f;
-        for (int n = lane; n < work.largest_parts; n += 64) top = fmaxf(top, work.largest[n]);
+#pragma unroll 4
+        for (int n = lane; n < slots * heads; n += 64) {
+            const int h = n / slots;
+            top = fmaxf(top, work.largest[static_cast<int64_t>(first_head + h) * work.q_slots + slot0 + n - h * slots]);
+        }
 #pragma unroll
         for (int m = 32; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
         const int e = exponent_of(top);
@@ -647,8 +651,7 @@ hipError_t backward(const AttentionArgs &a, hipStream_t stream)
     const int64_t key_groups = k_slots(a.k_tokens, a.n_clips) * a.kv_heads, near_groups = key_groups * work.parts;
     if (q_groups > INT_MAX || near_groups + far_groups > INT_MAX) return hipErrorInvalidConfiguration;
     if (a.q_tokens > 0)
-        dq_tiles<T, kD><<<static_cast<unsigned>(q_groups), kThreads, 0, stream>>>(
-            a, work, factor, static_cast<int>(q_slots(a.q_tokens, a.n_clips)));
+        dq_tiles<T, kD><<<static_cast<unsigned>(q_groups), kThreads, 0, stream>>>(a, work, factor);
     if (a.k_tokens > 0) {
         dkv_tiles<T, kD><<<static_cast<unsigned>(near_groups + far_groups), kThreads, 0, stream>>>(
             a, work, factor, static_cast<int>(near_groups));
