@@ -60,9 +60,8 @@ typedef struct rvq_heads {
  * cu_k[b+1]-1 (device int32 [n_clips + 1], non-decreasing, within
  * 0..q_tokens / 0..k_tokens). Its queries are the last ones of its keys'
  * positions: query i of n_q is at position i + n_k - n_q. Rows outside every
- * clip have no influence (in float16 gradients: but for the choice of a power
- * of two) and are not written. Offsets that break these rules give
- * unspecified results, but no access outside the arrays.
+ * clip have no influence and are not written. Offsets that break these rules
+ * give unspecified results, but no access outside the arrays.
  *
  * dim must be 64 or 128, q_heads a multiple of kv_heads (query head h reads
  * key head h / (q_heads / kv_heads)); scale >= 0 and finite.

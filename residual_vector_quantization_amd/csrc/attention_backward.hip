@@ -20,10 +20,14 @@
 //
 // Weights and dx enter the products in the inputs' type. bfloat16 has float32's
 // range, but float16 has 5 bits of exponent, so there weights are taken times
-// 2^4 and dx is brought near 1 by powers of two: dq by its own row's largest
-// |dout|, dk by that of the rows that its workgroup goes over (a sum over rows
-// needs one factor); both leave again in float32 at the end. Powers of two
-// change no rounding.
+// 2^14 and dx times 2^14 over a power of two that bounds |dw - delta|: no value
+// can overflow, and those down to 2^-28 of the bound keep all their bits.
+//   dq: |dw_ij - delta_i| <= 2 |dout_i| |v|, the largest |v| of the keys gone over
+//     (a launch before the two finds it for every 128 keys, 16 MB of values in 5 us);
+//   dk: |dw_ij - delta_i| <= |dout| |v_j| + |delta|, the largest |dout| and |delta| of
+//     the rows gone over (from dq_tiles). A lane keeps to one key, so it may have
+//     its own factor.
+// The factors leave again in float32 at the end; powers of two change no rounding.
 //
 // delta comes from the rounded out. Its error enters dx as (1 / number of keys
 // that matter) of the size of dx's own rounding squared, so it shows only where
@@ -65,8 +69,9 @@ constexpr int kMaxSplitSinks = 64;
 // are 0) and -delta a query and head, then the float32 parts of the sinks' gradients, { dk, dv } [sinks][dim] each.
 struct Work {
     float *lse2, *minus_delta;     // [q_heads][q_tokens]
-    float *largest;          // [q_heads][q_slots] largest finite |dout| of each workgroup of dq_tiles (float16 only)
-    int q_slots;
+    float *largest;          // float16: [q_heads][q_slots] the largest |dout| and |delta| of the rows of dq_tiles' workgroups
+    float *values;           // float16: [kv_heads][k_slots] the largest |v| of 128 keys
+    int q_slots, k_slots;
     float *near;             // [n_clips][kv_heads]
     float *far;              // [far slots][kv_heads][2]
     bool split;
@@ -107,7 +112,9 @@ int64_t q_slots(int64_t q_tokens, int n_clips) { return q_tokens / kRows + n_cli
 
 int64_t work_floats(const AttentionArgs &a)
 {
-    int64_t n = 2 * rounded(a.q_tokens * a.q_heads) + rounded(q_slots(a.q_tokens, a.n_clips) * a.q_heads);
+    int64_t n = 2 * rounded(a.q_tokens * a.q_heads);
+    if (a.dtype == RVQ_F16)
+        n += rounded(2 * q_slots(a.q_tokens, a.n_clips) * a.q_heads) + rounded(k_slots(a.k_tokens, a.n_clips) * a.kv_heads);
     if (split_sinks(a.q_tokens, a.n_clips, a.sinks))
         n += (a.n_clips + 2 * far_slots(a.q_tokens, a.n_clips)) * a.kv_heads * a.sinks * a.dim * 2;
     const int parts = parts_of(a);
@@ -122,7 +129,10 @@ Work work_of(const AttentionArgs &a)
     w.minus_delta = w.lse2 + rounded(a.q_tokens * a.q_heads);
     w.largest = w.minus_delta + rounded(a.q_tokens * a.q_heads);
     w.q_slots = static_cast<int>(q_slots(a.q_tokens, a.n_clips));
-    w.near = w.largest + rounded(static_cast<int64_t>(w.q_slots) * a.q_heads);
+    w.k_slots = static_cast<int>(k_slots(a.k_tokens, a.n_clips));
+    const bool narrow = a.dtype == RVQ_F16;
+    w.values = w.largest + (narrow ? rounded(static_cast<int64_t>(2) * w.q_slots * a.q_heads) : 0);
+    w.near = w.values + (narrow ? rounded(static_cast<int64_t>(w.k_slots) * a.kv_heads) : 0);
     w.far = w.near + static_cast<int64_t>(a.n_clips) * a.kv_heads * a.sinks * a.dim * 2;
     w.split = a.window != INT_MAX && split_sinks(a.q_tokens, a.n_clips, a.sinks);
     w.part = w.near;               // never both
@@ -132,12 +142,61 @@ Work work_of(const AttentionArgs &a)
 
 template <typename T> constexpr bool kNarrow = false;      // few exponent bits
 template <> constexpr bool kNarrow<f16_t> = true;
-constexpr float kWeightShift = 4.0f;                       // float16 weights are taken times 2^this
+constexpr float kWeightShift = 14.0f;                      // float16 weights are taken times 2^this
 
 __device__ inline bool not_finite(float x) { return !(fabsf(x) <= FLT_MAX); }
 
 // e with 2^(e - 1) <= x < 2^e, 0 for x = 0 and values that are not finite.
 __device__ inline int exponent_of(float x) { return x == 0.0f || not_finite(x) ? 0 : __builtin_amdgcn_frexp_expf(x); }
+
+__device__ inline float finite_or_0(float x) { return not_finite(x) ? 0.0f : x; }
+
+__device__ inline float wave_max(float x)
+{
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1) x = fmaxf(x, __shfl_xor(x, m));
+    return x;
+}
+
+template <typename V>
+__device__ inline float square_sum(V x)
+{
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += to_float(x[i]) * to_float(x[i]);
+    return sum;
+}
+
+// float16: the largest finite |v| (as a vector's length) of every 128 keys of a clip and key head.
+template <typename T, int kD>
+__global__ __launch_bounds__(kThreads)
+void value_sizes(AttentionArgs a, Work work)
+{
+    constexpr int kLanes = kD / 8, kStep = kThreads / kLanes;      // lanes a row, rows at a time
+    __shared__ float s_top[kWaves];
+    const int slot = blockIdx.x / a.kv_heads, kv = blockIdx.x % a.kv_heads;
+    const int clip = clip_of_slot(a.cu_k, a.n_clips, slot, kRows);
+    int k0, nk;
+    clip_range(a.cu_k, clip, a.k_tokens, k0, nk);
+    const int first = (slot - (a.cu_k[clip] / kRows + clip)) * kRows;
+    if (first < 0 || first >= nk) return;
+    const T *rows = static_cast<const T *>(a.v.data) + static_cast<int64_t>(k0 + first) * a.v.token + kv * a.v.head;
+    const int at = threadIdx.x / kLanes, end = min(kRows, nk - first);
+    float top = 0.0f;
+#pragma unroll
+    for (int n = 0; n < kRows / kStep; ++n) {
+        const int row = n * kStep + at;
+        float sum = square_sum(load8(rows + min(row, end - 1) * a.v.token + threadIdx.x % kLanes * 8));
+#pragma unroll
+        for (int m = 1; m < kLanes; m <<= 1) sum += __shfl_xor(sum, m);
+        top = fmaxf(top, finite_or_0(sum));
+    }
+    top = wave_max(top);
+    if ((threadIdx.x & 63) == 0) s_top[threadIdx.x >> 6] = top;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        work.values[static_cast<int64_t>(kv) * work.k_slots + slot] = sqrtf(fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3])));
+}
 
 // dq, and lse2 and delta of the rows. As in the forward pass a workgroup takes 128 queries and goes over the tiles of keys they see. If a result is
 // not finite, a second pass takes rows of K that are not finite as zeros and the weights of the queries that do see
@@ -176,7 +235,7 @@ void dq_tiles(AttentionArgs a, Work work, float factor)
     Operand<T> q[kD / 16], g[kD / 16];
     float lse2 = a.lse[head * a.q_tokens + at], minus_delta = 0.0f, unshift = 1.0f;
     lse2 = lse2 == -INFINITY ? INFINITY : lse2 * kLog2e - (kNarrow<T> ? kWeightShift : 0.0f);
-    float top = 0.0f, finite = 0.0f;      // largest |dout| of the row, and of its finite values
+    float size = 0.0f;      // |dout| of the row, squared at first
     vec8<T> rows[3][kD / 16];
 #pragma unroll
     for (int t = 0; t < kD / 16; ++t) {
@@ -191,28 +250,29 @@ void dq_tiles(AttentionArgs a, Work work, float factor)
         arrive(q[t]);
         arrive(g[t]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            minus_delta -= to_float(rows[1][t][i]) * to_float(rows[2][t][i]);
-            if constexpr (kNarrow<T>) {
-                const float x = fabsf(to_float(rows[1][t][i]));
-                top = fmaxf(top, x);
-                finite = fmaxf(finite, not_finite(x) ? 0.0f : x);
-            }
-        }
+        for (int i = 0; i < 8; ++i) minus_delta -= to_float(rows[1][t][i]) * to_float(rows[2][t][i]);
+        if constexpr (kNarrow<T>) size += square_sum(rows[1][t]);
     }
     minus_delta += __shfl_xor(minus_delta, 32);
     if (half == 0 && row < nq) work.lse2[head * a.q_tokens + at] = lse2;
     if constexpr (kNarrow<T>) {
-        __shared__ float s_top[kWaves];
-        const float e = static_cast<float>(exponent_of(fmaxf(top, __shfl_xor(top, 32))));
+        __shared__ float s_top[2][kWaves];
+        float value = 0.0f;
+        const float *values = work.values + static_cast<int64_t>(kv) * work.k_slots + k0 / kRows + clip;
+#pragma unroll 4
+        for (int t = lane; t < range.tiles; t += 64) value = fmaxf(value, values[range.start(t) / kRows]);
+        value = wave_max(value);
+        size = sqrtf(size + __shfl_xor(size, 32));
+        const float e = static_cast<float>(exponent_of(2.0f * size * value));
         lse2 += e;
         unshift = fast_exp2(e - kWeightShift);
-#pragma unroll
-        for (int m = 32; m > 0; m >>= 1) finite = fmaxf(finite, __shfl_xor(finite, m));
-        s_top[wave] = finite;
+        s_top[0][wave] = wave_max(finite_or_0(size));
+        s_top[1][wave] = wave_max(finite_or_0(fabsf(minus_delta)));
         __syncthreads();
-        if (threadIdx.x == 0)
-            work.largest[static_cast<int64_t>(head) * work.q_slots + slot] = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
+        if (threadIdx.x < 2) {
+            const float *top = s_top[threadIdx.x];
+            work.largest[2 * (static_cast<int64_t>(head) * work.q_slots + slot) + threadIdx.x] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        }
     }
     Keys feed(s_mem, a.k.token, a.v.token);
     const T *keys = static_cast<const T *>(a.k.data) + static_cast<int64_t>(k0) * a.k.token + kv * a.k.head;
@@ -362,24 +422,6 @@ __device__ inline void dkv_group(const AttentionArgs &a, const Work &work, float
     hi_all = __builtin_amdgcn_readfirstlane(hi_all);     // the same in both halves of the wavefront
     hi_any = __builtin_amdgcn_readfirstlane(hi_any);
 
-    // float16: dw - delta times `small`, weights times 2^kWeightShift
-    float small = 1.0f, unit_k = 1.0f, unit_v = 1.0f;
-    if constexpr (kNarrow<T>) {
-        // the rows gone over, in the slots that dq_tiles took them by
-        const int slot0 = q0 / kRows + clip + i_first / kRows, slots = per_head > 0 ? (i_end - 1) / kRows - i_first / kRows + 1 : 0;
-        float top = 0.0f;
-#pragma unroll 4
-        for (int n = lane; n < slots * heads; n += 64) {
-            const int h = n / slots;
-            top = fmaxf(top, work.largest[static_cast<int64_t>(first_head + h) * work.q_slots + slot0 + n - h * slots]);
-        }
-#pragma unroll
-        for (int m = 32; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
-        const int e = exponent_of(top);
-        small = fast_exp2(static_cast<float>(-e));
-        unit_v = fast_exp2(-kWeightShift);
-        unit_k = fast_exp2(static_cast<float>(e) - kWeightShift);
-    }
     const int64_t own = k0 + min(key, nk - 1);
     const T *own_k = static_cast<const T *>(a.k.data) + own * a.k.token + kv * a.k.head + 8 * half;
     const T *own_v = static_cast<const T *>(a.v.data) + own * a.v.token + kv * a.v.head + 8 * half;
@@ -409,6 +451,25 @@ __device__ inline void dkv_group(const AttentionArgs &a, const Work &work, float
     for (int t = 0; t < kD / 16; ++t) {
         arrive(k[t]);
         if constexpr (kKeep) arrive(v[t]);
+    }
+    // float16: dw - delta times `small`, weights times 2^kWeightShift
+    float small = 1.0f, unit_v = 1.0f;
+    if constexpr (kNarrow<T>) {
+        // the rows gone over, in the slots that dq_tiles took them by
+        const int slot0 = q0 / kRows + clip + i_first / kRows, slots = per_head > 0 ? (i_end - 1) / kRows - i_first / kRows + 1 : 0;
+        float size = 0.0f, delta = 0.0f, value = 0.0f;
+#pragma unroll 4
+        for (int n = lane; n < slots * heads; n += 64) {
+            const int h = n / slots;
+            const float *top = work.largest + 2 * (static_cast<int64_t>(first_head + h) * work.q_slots + slot0 + n - h * slots);
+            size = fmaxf(size, top[0]);
+            delta = fmaxf(delta, top[1]);
+        }
+#pragma unroll
+        for (int t = 0; t < kD / 16; ++t) value += square_sum(v[t]);
+        value = finite_or_0(sqrtf(value + __shfl_xor(value, 32)));
+        small = fast_exp2(static_cast<float>(-exponent_of(wave_max(size) * value + wave_max(delta))));
+        unit_v = fast_exp2(-kWeightShift);
     }
     f32x16 dk[kD / 32], dv[kD / 32];
     int head, i;     // of the next tile to load
@@ -539,6 +600,7 @@ __device__ inline void dkv_group(const AttentionArgs &a, const Work &work, float
         for (int r = 0; r < 16; ++r) odd = odd || not_finite(dk[n][r]) || not_finite(dv[n][r]);
     if (__syncthreads_or(odd)) pass(Constant<1>{});
     if (key >= nk) return;
+    const float unit_k = unit_v / small;
     if (kFar || parts > 1 || (work.split && key < a.sinks)) {
         if (kFar && key >= a.sinks) return;
         const int64_t which = kFar ? (static_cast<int64_t>(slot) * a.kv_heads + kv) * 2 + (wave & 1)
@@ -650,6 +712,9 @@ hipError_t backward(const AttentionArgs &a, hipStream_t stream)
     const int64_t far_groups = work.split ? far_slots(a.q_tokens, a.n_clips) * a.kv_heads : 0;
     const int64_t key_groups = k_slots(a.k_tokens, a.n_clips) * a.kv_heads, near_groups = key_groups * work.parts;
     if (q_groups > INT_MAX || near_groups + far_groups > INT_MAX) return hipErrorInvalidConfiguration;
+    if constexpr (kNarrow<T>)
+        if (a.q_tokens > 0 && a.k_tokens > 0)
+            value_sizes<T, kD><<<static_cast<unsigned>(key_groups), kThreads, 0, stream>>>(a, work);
     if (a.q_tokens > 0)
         dq_tiles<T, kD><<<static_cast<unsigned>(q_groups), kThreads, 0, stream>>>(a, work, factor);
     if (a.k_tokens > 0) {

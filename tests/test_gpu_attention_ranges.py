@@ -80,3 +80,54 @@ def test_float16_gradients_where_loud_frames_are_far():
     for name, x in zip(("dq", "dk", "dv"), got):
         close(name, x, want[name])
         rms_close(name, x[s], want[name][0][s], 2.0 ** -11)
+
+
+# ---------------------------------------------------------------- gradients: values of other sizes
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("size", [200.0, 3000.0])
+def test_float16_gradients_between_opposite_values(dim, size):
+    """Two keys with equal scores and values of opposite sign: dx = dim size / 2, within float16, and larger than its
+    range for a few powers of two more."""
+    m = rvq()
+    n = 2
+    g = torch.Generator().manual_seed(5)
+    q = torch.randn(n, 1, dim, generator=g).half().to(DEV)
+    k = (torch.randn(1, 1, dim, generator=g) / dim).half().to(DEV).expand(n, 1, dim).contiguous()
+    v = torch.tensor([size, -size], device=DEV).half().view(n, 1, 1).expand(n, 1, dim).contiguous()
+    dout = torch.ones(n, 1, dim, dtype=torch.float16, device=DEV)
+    announce("opposite values", dim=dim, size=size)
+    got = gradients(m, q, k, v, dout, ints([0, n]))
+    want = oracle.attention(q, k, v, [0, n], [0, n], None, 0, 1 / math.sqrt(dim), dout)
+    for name, x in zip(("dq", "dk", "dv"), got):
+        close(name, x, want[name])
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(None, 0), (300, 4)])
+@pytest.mark.parametrize("v_power,dout_power", [(12, -10), (15, -12), (-12, 6), (-8, 0), (0, 0)])
+def test_float16_gradients_of_large_and_small_values(dim, window, sinks, v_power, dout_power):
+    m = rvq()
+    n = 1100
+    announce("sizes of values", dim=dim, window=window, v=v_power, dout=dout_power)
+    q, k, v, dout = draw("fp16", [n], 2, 1, dim, seed=6)
+    v, dout = (v.clamp(-1.9, 1.9) * 2.0 ** v_power).half(), (dout * 2.0 ** dout_power).half()
+    got = gradients(m, q, k, v, dout, ints([0, n]), window=window, sinks=sinks)
+    want = oracle.attention(q, k, v, [0, n], [0, n], window, sinks, 1 / math.sqrt(dim), dout)
+    for name, x in zip(("dq", "dk", "dv"), got):
+        close(name, x, want[name])
+        if want[name][0].square().mean().sqrt() > 2.0 ** -10:      # the results themselves are normal numbers
+            rms_close(name, x, want[name][0], 2.0 ** -11)
+
+
+def test_float16_gradients_of_sinks_and_long_clips_with_large_values():
+    """Sums that are added up from pieces (queries beyond the window of the sinks, shared query heads)."""
+    m = rvq()
+    for lens, hq, hk, window, sinks in (([4300], 2, 1, 100, 4), ([700], 8, 1, None, 0)):
+        announce("pieces", lens=lens, window=window, sinks=sinks)
+        q, k, v, dout = draw("fp16", lens, hq, hk, 64, seed=7)
+        v, dout = (v.clamp(-1.9, 1.9) * 2.0 ** 14).half(), (dout * 2.0 ** -12).half()
+        got = gradients(m, q, k, v, dout, ints(offsets(lens)), window=window, sinks=sinks)
+        want = oracle.attention(q, k, v, offsets(lens), offsets(lens), window, sinks, 1 / 8, dout)
+        for name, x in zip(("dq", "dk", "dv"), got):
+            close(name, x, want[name])
