@@ -140,8 +140,6 @@ Work work_of(const AttentionArgs &a)
     return w;
 }
 
-template <typename T> constexpr bool kNarrow = false;      // few exponent bits
-template <> constexpr bool kNarrow<f16_t> = true;
 constexpr float kWeightShift = 14.0f;                      // float16 weights are taken times 2^this
 
 __device__ inline bool not_finite(float x) { return !(fabsf(x) <= FLT_MAX); }

@@ -17,6 +17,9 @@ typedef _Float16 f16_t;
 template <typename T>
 __device__ inline float to_float(T x) { return static_cast<float>(x); }
 
+template <typename T> inline constexpr bool kNarrow = false;      // few exponent bits
+template <> inline constexpr bool kNarrow<f16_t> = true;
+
 // A number known to the compiler, as an argument.
 template <int kN> struct Constant { static constexpr int value = kN; };
 

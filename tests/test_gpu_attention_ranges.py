@@ -131,3 +131,36 @@ def test_float16_gradients_of_sinks_and_long_clips_with_large_values():
         want = oracle.attention(q, k, v, offsets(lens), offsets(lens), window, sinks, 1 / 8, dout)
         for name, x in zip(("dq", "dk", "dv"), got):
             close(name, x, want[name])
+
+
+# ---------------------------------------------------------------- many small weights beside a large one
+
+def sink_and_crowd(n, dim, bits):
+    """One query, one key with a score `bits` powers of two above all others', whose values are 1 where its own is 0."""
+    q, k, v = torch.zeros(1, 1, dim), torch.zeros(n, 1, dim), torch.ones(n, 1, dim)
+    q[0, 0, 0], k[0, 0, 0] = 1.0, bits * math.log(2)
+    v[0] = 0
+    return q, k, v
+
+
+def crowd_bound(bound, n):
+    """Weights are rounded to float16 relative to their size, and below its normal numbers by half its smallest step,
+    2^-25, where the largest weight stands at 2^7 or more: n of them by 2^-32 n of the largest value, here 1."""
+    return bound + n * 2.0 ** -32
+
+
+@pytest.mark.parametrize("typ", list(TYPES))
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("bits", [14, 20, 26])
+def test_small_weights_beside_a_large_one(typ, dim, bits):
+    m = rvq()
+    n = 40000
+    announce("a sink and a crowd", typ=typ, dim=dim, bits=bits)
+    q, k, v = (x.to(TYPES[typ]).to(DEV) for x in sink_and_crowd(n, dim, bits))
+    for last in (False, True):                     # the large one comes first, or last
+        if last:
+            k, v = k.flip(0).contiguous(), v.flip(0).contiguous()
+        out, lse = m.rvq_window_attention(q, k, v, ints([0, 1]), ints([0, n]), scale=1.0)
+        want = oracle.attention(q, k, v, [0, 1], [0, n], None, 0, 1.0)
+        close("out", out, (want["out"][0], crowd_bound(want["out"][1], n)))
+        close("lse", lse, want["lse"])
