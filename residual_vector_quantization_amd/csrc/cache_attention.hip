@@ -17,6 +17,11 @@
 // The frames of S^T's rows are numbered so that the scores a lane holds belong
 // to the 8 frames of its V^T operand: weights go from one product into the
 // next without leaving the lane, and keys and values never enter the LDS.
+// Weights enter the second product in the cache's type, rounded once (half a step
+// of theirs beside the result's own, as in the windowed attention); their sum is
+// of the unrounded ones. float16 weights are taken times 2^kShift: half a step is
+// then 2^-32 of the largest, so that a long cache's many small ones are not lost
+// beside a large one.
 //
 // A wavefront takes tiles of 32 seen frames; its running maximum moves only
 // when a score exceeds it by more than 2^8, so most tiles need neither an
@@ -107,6 +112,7 @@ void newest_frame(Params p, Partials part)
 {
     constexpr int kSteps = kD / 32;      // products along the head dim
     constexpr int kN = kD / 16;          // dims a lane holds of a value row
+    constexpr float kShift = kNarrow<T> ? 15.0f - kSlack : 0.0f;      // weights are below 2^(kSlack + kShift)
     __shared__ float s_out[kWaves][kQueries][kD + 4];
     __shared__ float s_max[kWaves][kQueries], s_sum[kWaves][kQueries];
     const CacheAttentionArgs &a = p.a;
@@ -204,7 +210,7 @@ void newest_frame(Params p, Partials part)
                 for (int n = 0; n < kN; ++n) o[n] *= keep;
             }
         }
-        const float safe = m == -INFINITY ? 0.0f : m;
+        const float safe = m == -INFINITY ? 0.0f : m - kShift;
         vec8<T> w;
 #pragma unroll
         for (int b = 0; b < 2; ++b)

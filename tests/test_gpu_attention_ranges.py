@@ -164,3 +164,18 @@ def test_small_weights_beside_a_large_one(typ, dim, bits):
         want = oracle.attention(q, k, v, [0, 1], [0, n], None, 0, 1.0)
         close("out", out, (want["out"][0], crowd_bound(want["out"][1], n)))
         close("lse", lse, want["lse"])
+
+
+@pytest.mark.parametrize("typ", list(TYPES))
+@pytest.mark.parametrize("dim,n", [(64, 40000), (128, 500)])
+@pytest.mark.parametrize("bits", [14, 20, 26])
+def test_small_weights_beside_a_large_one_in_a_cache(typ, dim, n, bits):
+    m = rvq()
+    page = 50
+    announce("a sink and a crowd in a cache", typ=typ, dim=dim, n=n, bits=bits)
+    q, k, v = (x.to(TYPES[typ]).to(DEV) for x in sink_and_crowd(n, dim, bits))
+    pools = [x.view(n // page, page, 1, dim).transpose(1, 2).contiguous() for x in (k, v)]
+    table = torch.arange(n // page, dtype=torch.int32, device=DEV)[None]
+    out = m.rvq_cache_attention(q, *pools, table, ints([n]), scale=1.0)
+    want = oracle.attention(q, k, v, [0, 1], [0, n], None, 0, 1.0)["out"]
+    close("out", out, (want[0], crowd_bound(want[1], n)))
