@@ -90,7 +90,8 @@ typedef struct rvq_attention_shape {
  *           exponentials (natural log); NULL to skip it
  *
  * A value that a frame does not see has no influence on its output, not even
- * where it is infinite or NaN.
+ * where it is infinite or NaN. A seen one that is infinite makes the output
+ * infinite there, with its sign; NaN or infinities of both signs make it NaN.
  */
 RVQ_API rvq_status rvq_window_attention(const rvq_attention_shape *shape, const rvq_heads *q, const rvq_heads *k,
                                         const rvq_heads *v, const rvq_heads *out, float *lse, void *stream);

@@ -169,6 +169,13 @@ void forward_tiles(AttentionArgs a, float factor, int slots)
             }
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        if (markers.value) {
+            // counts of a tile and the one before stay below 1 / kMinus: whole and broken part apart
+#pragma unroll
+            for (int n = 0; n < kD / 32; ++n)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[n][r] = (o[n][r] >= 1.0f ? 1.0f : 0.0f) + (o[n][r] > floorf(o[n][r]) ? kMinus : 0.0f);
+        }
     };
     auto pass = [&](auto markers, auto clean) {
         if (range.tiles > 0) feed.start(keys, values, range.start(0), nk);
@@ -189,23 +196,28 @@ void forward_tiles(AttentionArgs a, float factor, int slots)
 #pragma unroll
         for (int r = 0; r < 16; ++r) odd = odd || !(fabsf(o[n][r]) <= FLT_MAX);
     // Weights of unseen keys are 0, but 0 times a value that is not finite is not 0. So when a result is not finite, a
-    // second pass counts, for every result, the keys seen that have such a value there, and a third computes the
-    // results with these values taken as 0: results with a count are NaN, the others are what they would be without
-    // the values that are not seen.
+    // second pass finds, for every result, whether keys that are seen have an infinity of either sign there (a NaN is
+    // both), and a third computes the results with these values taken as 0: results with one sign are that infinity,
+    // with both NaN, the others are what they would be without the values that are not seen.
     if (__syncthreads_or(odd)) {
         pass(Constant<1>{}, Constant<1>{});
-        uint32_t marked[kD / 64] = {};
+        uint32_t up[kD / 64] = {}, down[kD / 64] = {};
 #pragma unroll
         for (int n = 0; n < kD / 32; ++n)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) marked[n >> 1] |= static_cast<uint32_t>(o[n][r] > 0.0f) << (16 * (n & 1) + r);
+            for (int r = 0; r < 16; ++r) {
+                up[n >> 1] |= static_cast<uint32_t>(o[n][r] >= 1.0f) << (16 * (n & 1) + r);
+                down[n >> 1] |= static_cast<uint32_t>(o[n][r] > floorf(o[n][r])) << (16 * (n & 1) + r);
+            }
         __syncthreads();     // the tiles are no longer read
         pass(Constant<0>{}, Constant<1>{});
 #pragma unroll
         for (int n = 0; n < kD / 32; ++n)
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-                if (marked[n >> 1] >> (16 * (n & 1) + r) & 1) o[n][r] = __builtin_nanf("");
+            for (int r = 0; r < 16; ++r) {
+                const bool plus = up[n >> 1] >> (16 * (n & 1) + r) & 1, minus = down[n >> 1] >> (16 * (n & 1) + r) & 1;
+                if (plus || minus) o[n][r] = plus && minus ? __builtin_nanf("") : plus ? INFINITY : -INFINITY;
+            }
     }
     if (!real) return;
     l += __shfl_xor(l, 32);

@@ -170,11 +170,7 @@ struct Tile {
     }
 
     // Value i of the tile, in no order of interest, and its rewriting.
-    __device__ static bool fine(const char *s, int i)
-    {
-        const float x = to_float(reinterpret_cast<const T *>(s)[i]);
-        return x - x == 0.0f;
-    }
+    __device__ static float value(const char *s, int i) { return to_float(reinterpret_cast<const T *>(s)[i]); }
     __device__ static void set(char *s, int i, float x) { reinterpret_cast<T *>(s)[i] = static_cast<T>(x); }
 };
 
@@ -229,9 +225,9 @@ struct SplitTile {
         x.low = Part::across(s + 2 * Part::kBytes, n, step);
         return x;
     }
-    // The first part of a value that is not finite is not finite either.
-    __device__ static bool fine(const char *s, int i) { return Part::fine(s, i); }
-    __device__ static void set(char *s, int i, float x)     // 0 or 1
+    // The first part: of a value that is not finite, that value.
+    __device__ static float value(const char *s, int i) { return Part::value(s, i); }
+    __device__ static void set(char *s, int i, float x)     // a value of 8 bits
     {
         Part::set(s, i, x);
         Part::set(s + Part::kBytes, i, 0.0f);
@@ -242,15 +238,19 @@ struct SplitTile {
 template <typename T, int kD, int kWaves> struct RowsOf { typedef Tile<T, kD, kWaves> type; };
 template <int kD, int kWaves> struct RowsOf<float, kD, kWaves> { typedef SplitTile<kD, kWaves> type; };
 
-// Values of a tile that are not finite become 0; or, as markers, they become 1 and all others 0. Every thread of the
-// workgroup takes part, barriers are the caller's.
+__device__ inline bool fine(float x) { return x - x == 0.0f; }
+
+// Values of a tile that are not finite become 0; or, as markers, +inf becomes 1, -inf kMinus, NaN their sum and all others
+// 0. Every thread of the workgroup takes part, barriers are the caller's.
+constexpr float kMinus = 0.0078125f;
+
 template <typename Rows, int kD, int kThreads>
 __device__ inline void only_finite(char *s, bool markers)
 {
     for (int i = threadIdx.x; i < kTileRows * kD; i += kThreads) {
-        const bool fine = Rows::fine(s, i);
-        if (markers) Rows::set(s, i, fine ? 0.0f : 1.0f);
-        else if (!fine) Rows::set(s, i, 0.0f);
+        const float x = Rows::value(s, i);
+        if (markers) Rows::set(s, i, fine(x) ? 0.0f : x > 0.0f ? 1.0f : x < 0.0f ? kMinus : 1.0f + kMinus);
+        else if (!fine(x)) Rows::set(s, i, 0.0f);
     }
 }
 
@@ -261,7 +261,7 @@ __device__ inline void clear_bad_rows(char *s, int *flags)
     constexpr int kLanes = kThreads / kTileRows;
     const int row = threadIdx.x / kLanes;
     bool bad = false;
-    for (int i = threadIdx.x % kLanes; i < kD; i += kLanes) bad = bad || !Rows::fine(s, row * kD + i);
+    for (int i = threadIdx.x % kLanes; i < kD; i += kLanes) bad = bad || !fine(Rows::value(s, row * kD + i));
 #pragma unroll
     for (int m = 1; m < kLanes; m <<= 1) bad = __shfl_xor(static_cast<int>(bad), m) || bad;
     if (bad) {

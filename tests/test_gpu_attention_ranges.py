@@ -179,3 +179,33 @@ def test_small_weights_beside_a_large_one_in_a_cache(typ, dim, n, bits):
     out = m.rvq_cache_attention(q, *pools, table, ints([n]), scale=1.0)
     want = oracle.attention(q, k, v, [0, 1], [0, n], None, 0, 1.0)["out"]
     close("out", out, (want[0], crowd_bound(want[1], n)))
+
+
+# ---------------------------------------------------------------- infinite values
+
+@pytest.mark.parametrize("typ", list(TYPES))
+@pytest.mark.parametrize("dim", [64, 128])
+def test_seen_infinities_keep_their_sign(typ, dim):
+    """A value that is seen is infinite: so is the result, with its sign; NaN for infinities of both signs or a NaN;
+    all other results as with a 0 in its place."""
+    m = rvq()
+    n, window, sinks = 260, 50, 2
+    announce("infinite values", typ=typ, dim=dim)
+    q, k, v, _ = draw(typ, [n], 2, 1, dim, seed=8)
+    marks = {(0, 3): math.inf, (37, 5): math.inf, (40, 5): -math.inf, (100, 6): math.nan, (150, dim - 1): -math.inf,
+             (151, 33): math.inf, (259, 0): -math.inf, (200, 8): math.inf, (202, 8): math.inf}
+    bad = v.clone()
+    for (j, d), x in marks.items():
+        v[j, 0, d], bad[j, 0, d] = 0, x
+    cu = ints([0, n])
+    clean, lse = m.rvq_window_attention(q, k, v, cu, window=window, sinks=sinks)
+    got, got_lse = m.rvq_window_attention(q, k, bad, cu, window=window, sinks=sinks)
+    sees, want = oracle.sees(n, n, window, sinks).to(DEV), clean.clone()
+    for d in {d for _, d in marks}:
+        for p in range(n):
+            seen = [x for (j, e), x in marks.items() if e == d and sees[p, j]]
+            if seen:
+                want[p, :, d] = sum(seen)
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(got.nan_to_num(nan=5.0, posinf=math.inf, neginf=-math.inf), want.nan_to_num(nan=5.0, posinf=math.inf, neginf=-math.inf))
+    assert torch.equal(lse, got_lse)
