@@ -10,7 +10,10 @@
  * Conventions are those of rvq.h: plain C99, caller-owned DEVICE memory, no
  * allocation and no state between calls, work enqueued on `stream` (a
  * hipStream_t cast to void*), argument errors reported synchronously before
- * anything is enqueued, status codes of rvq_status.
+ * anything is enqueued, status codes of rvq_status. Shapes that take 2^24
+ * workgroups or more are refused (RVQ_ERR_UNSUPPORTED). A workgroup is a head
+ * of 128 frames or of a clip's rest in the windowed attention, 16 query heads
+ * of a key head and clip in the cache attention, 8 new frames in an append.
  *
  * Which frames a frame sees. A frame at position p of its clip sees the
  * frames j <= p with p - j < window, and of those further back the first

@@ -240,7 +240,7 @@ template <typename T, int kD>
 hipError_t forward(const AttentionArgs &a, hipStream_t stream)
 {
     const int64_t slots = a.q_tokens / kRows + a.n_clips + 1;
-    if (slots * a.q_heads > INT_MAX) return hipErrorInvalidConfiguration;
+    if (!fits(slots * a.q_heads, kThreads)) return hipErrorNotSupported;
     // scale 0 (equal weights) becomes the smallest factor: 0 times the -inf of an unseen key does not arise
     const float factor = fmaxf(a.scale * kLog2e, FLT_MIN);
     forward_tiles<T, kD><<<static_cast<unsigned>(slots * a.q_heads), kThreads, 0, stream>>>(a, factor, static_cast<int>(slots));

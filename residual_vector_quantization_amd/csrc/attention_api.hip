@@ -15,7 +15,10 @@ namespace {
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-rvq_status from_hip(hipError_t e) { return e == hipSuccess ? RVQ_OK : RVQ_ERR_DEVICE; }
+rvq_status from_hip(hipError_t e)
+{
+    return e == hipSuccess ? RVQ_OK : e == hipErrorNotSupported ? RVQ_ERR_UNSUPPORTED : RVQ_ERR_DEVICE;
+}
 
 int element_bytes(int32_t dtype) { return dtype == RVQ_F32 ? 4 : 2; }
 

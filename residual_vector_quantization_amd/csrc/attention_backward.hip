@@ -709,7 +709,7 @@ hipError_t backward(const AttentionArgs &a, hipStream_t stream)
     const int64_t q_groups = q_slots(a.q_tokens, a.n_clips) * a.q_heads;
     const int64_t far_groups = work.split ? far_slots(a.q_tokens, a.n_clips) * a.kv_heads : 0;
     const int64_t key_groups = k_slots(a.k_tokens, a.n_clips) * a.kv_heads, near_groups = key_groups * work.parts;
-    if (q_groups > INT_MAX || near_groups + far_groups > INT_MAX) return hipErrorInvalidConfiguration;
+    if (!fits(q_groups, kThreads) || !fits(near_groups + far_groups, kThreads)) return hipErrorNotSupported;
     if constexpr (kNarrow<T>)
         if (a.q_tokens > 0 && a.k_tokens > 0)
             value_sizes<T, kD><<<static_cast<unsigned>(key_groups), kThreads, 0, stream>>>(a, work);

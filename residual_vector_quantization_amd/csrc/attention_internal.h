@@ -39,6 +39,9 @@ struct CacheAttentionArgs {
     void *workspace;
 };
 
+// A launch holds fewer than 2^32 threads. Launches that need more are refused with hipErrorNotSupported before any other.
+inline bool fits(int64_t groups, int threads) { return groups <= 0xffffffffll / threads; }
+
 hipError_t launch_window_attention(const AttentionArgs &a, hipStream_t stream);
 int64_t window_attention_backward_bytes(const AttentionArgs &a);     // of the shape alone
 hipError_t launch_window_attention_backward(const AttentionArgs &a, hipStream_t stream);

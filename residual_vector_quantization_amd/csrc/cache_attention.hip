@@ -322,7 +322,7 @@ hipError_t run(const Params &p, hipStream_t stream)
         part.out = part.stats + stats_floats(static_cast<int64_t>(a.n_clips) * a.q_heads * p.splits);
     }
     const int64_t groups = static_cast<int64_t>(a.n_clips) * p.splits * a.kv_heads * p.chunks;
-    if (groups > INT_MAX) return hipErrorInvalidConfiguration;
+    if (!fits(groups, 64 * (p.wide ? kWideWaves : kWaves))) return hipErrorNotSupported;
     if (p.wide) newest_frame<T, kD, kWideWaves><<<static_cast<unsigned>(groups), 64 * kWideWaves, 0, stream>>>(p, part);
     else newest_frame<T, kD, kWaves><<<static_cast<unsigned>(groups), 64 * kWaves, 0, stream>>>(p, part);
     if (p.splits > 1) join_splits<T, kD><<<dim3(a.n_clips, a.q_heads), 64, 0, stream>>>(p, part);

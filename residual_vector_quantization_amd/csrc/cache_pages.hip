@@ -594,6 +594,7 @@ hipError_t launch_cache_append(const Heads &k, const Heads &v, int64_t n_tokens,
                                hipStream_t stream)
 {
     const int pieces = dim * element_bytes / 16;
+    if (!fits(ceil_div(n_tokens, kAppendTokens), kThreads)) return hipErrorNotSupported;
     append_rows<<<ceil_div(n_tokens, kAppendTokens), kThreads, 0, stream>>>(
         k, v, n_tokens, cu, n_clips, kv_heads, pieces, element_bytes, page_size, n_pages, table_ld, table, lens,
         static_cast<char *>(k_pool), static_cast<char *>(v_pool));
