@@ -199,14 +199,18 @@ __device__ inline void rank_wanted(const Wanted &w, int32_t *base, int32_t *tota
             s_column[threadIdx.x] = first;
             s_there[threadIdx.x] = 0;
             __syncthreads();
+            // a thread takes neighbouring columns, starting in the last clip with s_before <= at
+            const int clips = min(kThreads, w.n - i0), each = (all + kThreads - 1) / kThreads;
+            int at = min(static_cast<int>(threadIdx.x) * each, all), lo = 0, hi = clips;
+            const int end = min(at + each, all);
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (s_before[mid] <= at) lo = mid;
+                else hi = mid;
+            }
 #pragma unroll 4
-            for (int at = threadIdx.x; at < all; at += kThreads) {
-                int lo = 0, hi = min(kThreads, w.n - i0);      // the last clip with s_before <= at
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (s_before[mid] <= at) lo = mid;
-                    else hi = mid;
-                }
+            for (; at < end; ++at) {
+                while (lo + 1 < clips && s_before[lo + 1] <= at) ++lo;
                 if (w.is_page(w.table[static_cast<int64_t>(i0 + lo) * w.table_ld + s_column[lo] + at - s_before[lo]]))
                     atomicAdd(&s_there[lo], 1);
             }
