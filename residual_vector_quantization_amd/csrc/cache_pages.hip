@@ -202,7 +202,7 @@ __device__ inline void rank_wanted(const Wanted &w, int32_t *base, int32_t *tota
             // a thread takes neighbouring columns, starting in the last clip with s_before <= at
             const int clips = min(kThreads, w.n - i0), each = (all + kThreads - 1) / kThreads;
             int at = min(static_cast<int>(threadIdx.x) * each, all), lo = 0, hi = clips;
-            const int end = min(at + each, all);
+            const int end = at + min(each, all - at);
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
                 if (s_before[mid] <= at) lo = mid;
