@@ -23,11 +23,12 @@
  *
  * Arithmetic. Products run on the matrix cores in the inputs' type with
  * float32 accumulation (float32 inputs: as three bfloat16 parts a value, six
- * products, or as float32, either way as exact as float32); scores, softmax
- * statistics and accumulators are float32. Attention weights and score
- * gradients are rounded once to the inputs' type where they enter a matrix
- * product of it, outputs once at the end. No sum's order depends on timing:
- * the same call gives the same bits.
+ * products, off by 2^-22 of a product of two values at most and 2^-25 in the
+ * mean square, or as float32); scores, softmax statistics and accumulators
+ * are float32. Attention weights and score gradients are rounded once to the
+ * inputs' type where they enter a matrix product of it (in float16 times a
+ * power of two that keeps them within its range), outputs once at the end. No
+ * sum's order depends on timing: the same call gives the same bits.
  */
 #ifndef RVQ_ATTENTION_H
 #define RVQ_ATTENTION_H

@@ -6,8 +6,8 @@
 // Bound by the matrix cores, the LDS reads that feed them and the exponentials,
 // all of about the same weight: 4 dim flops, 1 exponential a pair.
 // Measured: 16384 queries, window 4096, 4 sinks, 16 heads of 128 over 4, bfloat16:
-// 534 us, 980 TFLOP/s, where a large library product reaches 1250 (both at a
-// clock that the power limit brings to about 1.9 GHz); matrix cores busy in 49%
+// 524 us, 997 TFLOP/s, where a large library product reaches 1250 (both at a
+// clock that the power limit brings to about 1.9 GHz); matrix cores busy in 50%
 // of the cycles, no LDS bank conflicts.
 // A workgroup takes 128 queries of one head and clip, 32 a wavefront, and goes
 // once over the keys they see: the sinks' tiles, then the window's, 64 keys a

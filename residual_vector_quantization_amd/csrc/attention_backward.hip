@@ -4,26 +4,28 @@
 //   dw_ij = dout_i . v_j,  dx_ij = w_ij (dw_ij - delta_i)
 //   dq_i = scale sum_j dx_ij k_j,  dk_j = scale sum_i dx_ij q_i,  dv_j = sum_i w_ij dout_i
 //
-// Two launches and no atomics, so the sums' order is fixed: dq and the rows'
+// Two main launches and no atomics, so the sums' order is fixed: dq and the rows'
 // delta (queries in registers, keys go by), dk and dv (keys in registers, queries
-// go by, all query heads of a key head one after another). Scores and dw are
-// made twice, 14 dim flops a pair with the forward pass' 4 make 18 where 14
-// would do; in exchange no partial dq goes through memory.
+// go by, all query heads of a key head one after another); a small one before them
+// in float16, and one behind them where dk and dv come in parts (both below). Scores
+// and dw are made twice, 14 dim flops a pair with the forward pass' 4 make 18 where
+// 14 would do; in exchange no partial dq goes through memory.
 // Bound by the matrix cores and the LDS reads that feed them, as in the
 // forward pass, with the same operand layouts: a lane keeps to one query (dq)
 // or one key (dk, dv), and what a product leaves in it is the next one's operand.
 // Measured: two clips of up to 8192 frames, window 750, 4 sinks, 16 heads of 128
-// over 4, bfloat16: dq 206 us (matrix cores busy 32% of the cycles), dk and dv
-// 286 us (28%; accumulators and operands take 400 registers, so 1 wavefront a
+// over 4, bfloat16: dq 204 us (matrix cores busy 32% of the cycles), dk and dv
+// 286 us (27%; accumulators and operands take 400 registers, so 1 wavefront a
 // SIMD, and exponentials are not hidden behind another's products), sinks 6 us.
-// 8 clips of 2000 frames, all seen, 16 heads of 64 over 8, float16: 145 and 224 us.
+// 8 clips of 2000 frames, all seen, 16 heads of 64 over 8, float16: 145 and 211 us.
 //
 // Weights and dx enter the products in the inputs' type. bfloat16 has float32's
 // range, but float16 has 5 bits of exponent, so there weights are taken times
 // 2^14 and dx times 2^14 over a power of two that bounds |dw - delta|: no value
 // can overflow, and those down to 2^-28 of the bound keep all their bits.
 //   dq: |dw_ij - delta_i| <= 2 |dout_i| |v|, the largest |v| of the keys gone over
-//     (a launch before the two finds it for every 128 keys, 16 MB of values in 5 us);
+//     (a launch before the two finds it for every 128 keys, 16 MB of values in 5 us;
+//     a small call of 36 us takes 3 us longer by it);
 //   dk: |dw_ij - delta_i| <= |dout| |v_j| + |delta|, the largest |dout| and |delta| of
 //     the rows gone over (from dq_tiles). A lane keeps to one key, so it may have
 //     its own factor.
@@ -33,8 +35,9 @@
 // that matter) of the size of dx's own rounding squared, so it shows only where
 // queries see few keys: there (kFewKeys) dq_tiles first goes over the keys for
 // sum_j w_ij (dw_ij - delta_i), which is what delta lacks, and corrects it, for
-// the keys' gradients as well. Small windows in float16, error of dq and dk over that of
-// a correct result rounded once: 1.52 without, 1.41 with (two roundings).
+// the keys' gradients as well. Small windows in float16, error of dq and dk over
+// that of a correct result rounded once: 1.52 without, 1.41 with (two roundings);
+// over windows of 2 to 600 frames 1.39 to 1.47.
 //
 // Where keys and key heads make few workgroups, the query heads of a key head
 // are shared out among several (parts_of), and a third launch adds their float32
@@ -196,9 +199,9 @@ void value_sizes(AttentionArgs a, Work work)
         work.values[static_cast<int64_t>(kv) * work.k_slots + slot] = sqrtf(fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3])));
 }
 
-// dq, and lse2 and delta of the rows. As in the forward pass a workgroup takes 128 queries and goes over the tiles of keys they see. If a result is
-// not finite, a second pass takes rows of K that are not finite as zeros and the weights of the queries that do see
-// them as NaN, so that only those get it.
+// dq, and lse2 and delta of the rows. As in the forward pass a workgroup takes 128 queries and goes over the tiles of
+// keys they see. If a result is not finite, a second pass takes rows of K that are not finite as zeros and the weights of
+// the queries that do see them as NaN, so that only those get it.
 template <typename T, int kD>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? (kD == 64 ? 3 : 2) : 1)
 void dq_tiles(AttentionArgs a, Work work, float factor)

@@ -121,7 +121,10 @@ struct Split8 {
 };
 
 // What a 32-wide product takes for 8 values of type T. Float32 values are split: six bfloat16 products of 32 cycles
-// give what eight float32 products of 64 do, to the 2^-26 of the parts' products left out. Infinities split into NaN.
+// give what eight float32 products of 64 do, but for the parts' products left out. A middle part is up to 2^-7 of its
+// value (high is cut off, not rounded: rounded up it would leave float32's range), a low one up to 2^-16, so middle times
+// low, twice, is up to 2^-22 of the product of two values; in the mean square of normal ones 2^-25.4, where a float32
+// rounding is 2^-24 at most. Infinities split into NaN.
 template <typename T> struct OperandOf { typedef vec8<T> type; };
 template <> struct OperandOf<float> { typedef Split8 type; };
 template <typename T> using Operand = typename OperandOf<T>::type;

@@ -4,13 +4,15 @@
 // prefix count over refs. A workgroup ranks the kChunk pages of its chunk; what
 // precedes them it counts itself in pools of up to kSelfCounted pages (reading
 // them again from the L2 costs less than the launch that would count them), or
-// finds as counts of the chunks in larger ones. Table entries, pages and
-// reference counts are then written by a second launch. Only integer atomics
+// finds as counts of the chunks in larger ones. One workgroup ranks what is
+// wanted: the columns asked for that name no page yet, or the partial pages of a
+// fork's parents. Table entries, pages and the counts of those taken are then
+// written by a second launch. Only integer atomics
 // (reference counts) are used, whose order changes nothing. Page contents move
 // in 16-byte pieces, one read and one write of every byte: bound by HBM.
-// Measured: 0.91 GB moved by a compaction in 182 us (5.0 TB/s), 0.54 GB copied by
-// a fork of 256 clips in 98 us (5.5 TB/s), 0.22 GB appended in 47 us (4.8 TB/s);
-// the ranking launches take 4 to 9 us, a call from Python 10 us at least.
+// Measured: 0.91 GB moved by a compaction in 183 us (5.0 TB/s), 0.54 GB copied by
+// a fork of 256 clips in 98 us (5.5 TB/s), 0.22 GB appended in 46 us (4.8 TB/s);
+// the ranking launches take 3 to 9 us, a call from Python 10 us at least.
 #include <limits.h>
 #include <stdint.h>
 
