@@ -50,7 +50,8 @@ typedef enum rvq_dtype {
  * data[t * token_stride + h * head_stride + d], strides in elements. data and
  * both strides must be multiples of 16 bytes, token_stride below 2^23 - 16
  * elements; rows may be slices of a wider
- * array (a fused projection's output). Output rows must not overlap.
+ * array (a fused projection's output). Output rows must not overlap each
+ * other or an input.
  */
 typedef struct rvq_heads {
     void *data;
