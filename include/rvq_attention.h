@@ -1,7 +1,8 @@
 /*
  * rvq_attention.h -- C ABI of the streaming-attention operators of librvq:
  * windowed attention with its gradient, attention of one new frame over a
- * paged key-value cache, and the upkeep of the cache's pages.
+ * paged key-value cache, rotary positions, and the upkeep of the cache's
+ * pages.
  *
  * These are the operators of the transformers that stand around a residual
  * quantizer and of the models that generate its codes: both run over frames
@@ -183,6 +184,78 @@ RVQ_API rvq_status rvq_cache_attention(const rvq_cache_shape *shape, int32_t q_h
                                        const void *k_pool, const void *v_pool, const int32_t *table,
                                        const int32_t *lens, int64_t window, int32_t sinks, float scale,
                                        const rvq_heads *out, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Rotary positions. Of every head's first rot_dim values (even, 2..dim) pair
+ * i turns by the angle position * frequencies[i]: (a, b) becomes amplitude *
+ * (a cos - b sin, b cos + a sin). The pairs are the values i and rot_dim / 2
+ * + i, or 2 i and 2 i + 1 where interleaved != 0; the values behind rot_dim
+ * stay as they are. With inverse != 0 the angles are negative: the gradient of
+ * the same call without it. frequencies [rot_dim / 2] are radians a position,
+ * device float64; angles are taken in float64, so far positions lose nothing.
+ */
+typedef struct rvq_rotation {
+    const double *frequencies;
+    int32_t rot_dim;
+    int32_t interleaved;
+    int32_t inverse;
+    float amplitude;    /* finite */
+} rvq_rotation;
+
+/*
+ * rvq_rotary_frequencies -- base^(-2 i / rot_dim) for i < rot_dim / 2, scaled
+ * for clips longer than a model was trained on. HOST memory, no GPU involved.
+ *
+ *   RVQ_ROTARY_PLAIN   as they are
+ *   RVQ_ROTARY_LINEAR  all divided by factor (positions are)
+ *   RVQ_ROTARY_BASE    base times factor^(rot_dim / (rot_dim - 2)): the last
+ *                      pair's frequency is divided by factor, the first stays
+ *   RVQ_ROTARY_RAMP    pairs that turn at least `fast` times within `context`
+ *                      positions stay, those that turn at most `slow` times
+ *                      are divided by factor, between them in proportion to
+ *                      the turns
+ *
+ * base and factor must be positive; slow < fast and context > 0 (RAMP only,
+ * else not read).
+ */
+typedef enum rvq_rotary_scaling {
+    RVQ_ROTARY_PLAIN = 0,
+    RVQ_ROTARY_LINEAR = 1,
+    RVQ_ROTARY_BASE = 2,
+    RVQ_ROTARY_RAMP = 3
+} rvq_rotary_scaling;
+
+RVQ_API rvq_status rvq_rotary_frequencies(int32_t rot_dim, double base, int32_t scaling, double factor,
+                                          double context, double slow, double fast, double *frequencies);
+
+/*
+ * rvq_rotary -- turns packed queries and keys, in one launch.
+ *
+ *   q, q_out   [n_tokens, q_heads, dim]; q_heads 0: none (NULL)
+ *   k, k_out   [n_tokens, kv_heads, dim]; kv_heads 0: none (NULL)
+ *   positions  [n_tokens] int32, or NULL: frame i of clip b (rows cu[b] ..
+ *              cu[b+1]-1) is at position first[b] + i (first [n_clips] int32,
+ *              NULL: 0). Rows outside every clip are not written.
+ *
+ * dim must be 64 or 128. An output may be its input (the same data and
+ * strides); otherwise outputs must not overlap inputs.
+ */
+RVQ_API rvq_status rvq_rotary(const rvq_rotation *rotation, int32_t dtype, int64_t n_tokens, int32_t q_heads,
+                              int32_t kv_heads, int32_t dim, int32_t n_clips, const int32_t *cu, const int32_t *first,
+                              const int32_t *positions, const rvq_heads *q, const rvq_heads *k,
+                              const rvq_heads *q_out, const rvq_heads *k_out, void *stream);
+
+/*
+ * rvq_rotary_append -- rvq_cache_append with rotary positions: new frame i of
+ * clip b is at position lens[b] + i. Its queries are turned into q_out (which
+ * may be q), its keys on their way into the pages; values go there as they
+ * are. q_heads 0: keys and values alone. Frames whose position has no page
+ * are dropped, but their queries are turned. rotation->inverse must be 0.
+ */
+RVQ_API rvq_status rvq_rotary_append(const rvq_cache_shape *shape, const rvq_rotation *rotation, int32_t q_heads,
+                                     const rvq_heads *q, const rvq_heads *k, const rvq_heads *v, int64_t n_tokens,
+                                     const int32_t *cu, const int32_t *table, const int32_t *lens,
+                                     const rvq_heads *q_out, void *k_pool, void *v_pool, void *stream);
 
 /*
  * Upkeep of the pages. Each operation reads its inputs and writes new table,

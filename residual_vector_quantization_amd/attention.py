@@ -8,6 +8,12 @@ workspaces come from ``torch.empty``, raw pointers and the current HIP stream go
   -> ``(dq, dk, dv)``
 * ``rvq_cache_append(k, v, k_pool, v_pool, table, lens, cu=None)``
 * ``rvq_cache_attention(q, k_pool, v_pool, table, lens, window=None, sinks=0, scale=None)`` -> ``out``
+* ``rvq_rotary_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, context=0, slow=1.0, fast=32.0)``
+  -> float64 CPU tensor
+* ``rvq_rotary(q, k, frequencies, cu=None, first=None, positions=None, interleaved=False, amplitude=1.0,
+  inverse=False)`` -> ``(q, k)``
+* ``rvq_rotary_append(q, k, v, frequencies, k_pool, v_pool, table, lens, cu=None, interleaved=False, amplitude=1.0)``
+  -> ``q``
 * ``rvq_cache_reserve(table, lens, new_lens, refs, page_size)`` -> ``(table, refs, missing)``
 * ``rvq_cache_fork(table, lens, refs, parents, children, k_pool, v_pool)`` -> ``(table, lens, refs, missing)``
 * ``rvq_cache_free(table, lens, refs, page_size, drop=None, window=None, sinks=0)`` -> ``(table, lens, refs)``
@@ -35,9 +41,11 @@ from . import RVQError, _check, _ptr, _require, load, rvq_status_string
 EXPORTED_ATTENTION = ("rvq_window_attention", "rvq_window_attention_backward", "rvq_window_attention_backward_bytes",
                       "rvq_cache_append", "rvq_cache_attention", "rvq_cache_attention_bytes",
                       "rvq_cache_scratch_bytes", "rvq_cache_reserve", "rvq_cache_fork", "rvq_cache_free",
-                      "rvq_cache_compact", "rvq_cache_copy")
+                      "rvq_cache_compact", "rvq_cache_copy", "rvq_rotary_frequencies", "rvq_rotary",
+                      "rvq_rotary_append")
 
 DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+SCALINGS = {None: 0, "linear": 1, "base": 2, "ramp": 3}
 
 
 class _Heads(ctypes.Structure):
@@ -57,10 +65,16 @@ class _CacheShape(ctypes.Structure):
                 ("table_ld", ctypes.c_int32)]
 
 
+class _Rotation(ctypes.Structure):
+    _fields_ = [("frequencies", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("inverse", ctypes.c_int32), ("amplitude", ctypes.c_float)]
+
+
 # The same structures packed by hand: a tenth of the time of a ctypes.Structure, which counts where a call takes 10 us.
 _pack_heads = struct.Struct("=Qqq").pack
 _pack_attention = struct.Struct("=6i3qQQf4x").pack
 _pack_cache = struct.Struct("=7i").pack
+_pack_rotation = struct.Struct("=Q3if").pack
 
 _ready = None
 
@@ -70,7 +84,7 @@ def _lib() -> ctypes.CDLL:
     if _ready is not None:
         return _ready
     lib = load()
-    vp, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+    vp, i32, i64, f32, f64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_double
     heads = shape = cache = vp      # packed bytes or a pointer to the structure
     for name, restype, argtypes in (
             ("rvq_window_attention", ctypes.c_int, [shape, heads, heads, heads, heads, vp, vp]),
@@ -81,6 +95,11 @@ def _lib() -> ctypes.CDLL:
             ("rvq_cache_attention_bytes", i64, [cache, i32]),
             ("rvq_cache_attention", ctypes.c_int,
              [cache, i32, heads, vp, vp, vp, vp, i64, i32, f32, heads, vp, i64, vp]),
+            ("rvq_rotary_frequencies", ctypes.c_int, [i32, f64, i32, f64, f64, f64, f64, vp]),
+            ("rvq_rotary", ctypes.c_int,
+             [vp, i32, i64, i32, i32, i32, i32, vp, vp, vp, heads, heads, heads, heads, vp]),
+            ("rvq_rotary_append", ctypes.c_int,
+             [cache, vp, i32, heads, heads, heads, i64, vp, vp, vp, heads, vp, vp, vp]),
             ("rvq_cache_scratch_bytes", i64, [i32, i32]),
             ("rvq_cache_reserve", ctypes.c_int, [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, i64, vp]),
             ("rvq_cache_fork", ctypes.c_int,
@@ -327,6 +346,123 @@ def rvq_cache_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Ten
                                     1.0 / math.sqrt(dim) if scale is None else scale, out_heads, workspace.data_ptr(),
                                     workspace.numel(), _stream(k_pool))
     _check("rvq_cache_attention", st)
+    return out
+
+
+def rvq_rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
+                           context: float = 0.0, slow: float = 1.0, fast: float = 32.0) -> torch.Tensor:
+    """Radians a position of the ``rot_dim / 2`` pairs, float64 on the CPU: ``base^(-2 i / rot_dim)``.
+
+    ``scaling`` stretches them for clips ``factor`` times longer: "linear" divides all by ``factor``; "base" raises
+    the base so that the slowest one is divided by it; "ramp" keeps those that turn ``fast`` times or more within
+    ``context`` positions and divides those that turn ``slow`` times or less.
+    """
+    if scaling not in SCALINGS:
+        raise ValueError(f"scaling must be one of {', '.join(map(repr, SCALINGS))}, got {scaling!r}")
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError(f"rot_dim={rot_dim} must be even and at least 2")
+    out = torch.empty(rot_dim // 2, dtype=torch.float64)
+    st = _lib().rvq_rotary_frequencies(rot_dim, base, SCALINGS[scaling], factor, context, slow, fast, out.data_ptr())
+    _check("rvq_rotary_frequencies", st)
+    return out
+
+
+def _rotation(frequencies: torch.Tensor, interleaved: bool, inverse: bool, amplitude: float, device, dim: int) -> bytes:
+    _require(frequencies, "frequencies", torch.float64, 1, device)
+    n = frequencies.shape[0]
+    if not 0 < 2 * n <= dim:
+        raise ValueError(f"frequencies must have 1 to {dim // 2} entries, got {n}")
+    return _pack_rotation(frequencies.data_ptr(), 2 * n, interleaved, inverse, amplitude)
+
+
+def rvq_rotary(q: Optional[torch.Tensor], k: Optional[torch.Tensor], frequencies: torch.Tensor,
+               cu: Optional[torch.Tensor] = None, first: Optional[torch.Tensor] = None,
+               positions: Optional[torch.Tensor] = None, interleaved: bool = False, amplitude: float = 1.0,
+               inverse: bool = False, out=None):
+    """Rotary positions of packed queries ``q`` [T, Hq, D] and keys ``k`` [T, Hk, D] (either may be None).
+
+    ``frequencies`` float64 [n]: the first 2 n values of every head turn, in pairs of (i, n + i), or of neighbours
+    where ``interleaved``; turned values are scaled by ``amplitude``. Positions are ``positions`` int32 [T], or
+    ``first[b] + i`` for frame i of clip b (``cu`` int32 [clips + 1]; ``first`` int32 [clips], None: 0); rows outside
+    every clip are not written. ``inverse`` turns backwards: gradients of the results give those of ``q`` and ``k``.
+    ``out`` may pass the two outputs preallocated; they may be ``q`` and ``k`` themselves. Returns ``(q_out, k_out)``.
+    """
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q or k must be given")
+    dtype, dev = _float_type(x, "q" if q is not None else "k"), x.device
+    x_heads = _require_heads(x, "q" if q is not None else "k", dtype, dev)
+    tokens, _, dim = x.shape
+    if q is not None and k is not None:
+        k_heads = _require_heads(k, "k", dtype, dev, dim=dim, tokens=tokens)
+    else:
+        k_heads = x_heads
+    rotation = _rotation(frequencies, interleaved, inverse, amplitude, dev, dim)
+    clips = 0
+    if positions is not None:
+        if cu is not None or first is not None:
+            raise ValueError("positions, or cu and first")
+        _require(positions, "positions", torch.int32, 1, dev)
+        if positions.shape[0] != tokens:
+            raise ValueError(f"positions must have one entry per row ({tokens}), got {positions.shape[0]}")
+    else:
+        if cu is None:
+            raise ValueError("positions or cu must be given")
+        clips = _offsets(cu, "cu", dev)
+        if first is not None:
+            _require(first, "first", torch.int32, 1, dev)
+            if first.shape[0] != clips:
+                raise ValueError(f"first must have one entry per clip ({clips}), got {first.shape[0]}")
+    q_out, k_out = (None, None) if out is None else out
+    hq, hk = 0 if q is None else q.shape[1], 0 if k is None else k.shape[1]
+    q_to = k_to = None
+    if q is not None:
+        if q_out is None:
+            q_out = q.new_empty(q.shape)
+        q_to = x_heads if q_out is q else _require_heads(q_out, "q_out", dtype, dev, hq, dim, tokens)
+    if k is not None:
+        if k_out is None:
+            k_out = k.new_empty(k.shape)
+        k_to = k_heads if k_out is k else _require_heads(k_out, "k_out", dtype, dev, hk, dim, tokens)
+    st = _lib().rvq_rotary(rotation, DTYPES[dtype], tokens, hq, hk, dim, clips, _ptr(cu), _ptr(first),
+                           _ptr(positions), x_heads if hq else None, k_heads if hk else None, q_to, k_to, _stream(x))
+    _check("rvq_rotary", st)
+    return (None if q is None else q_out), (None if k is None else k_out)
+
+
+def rvq_rotary_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, frequencies: torch.Tensor,
+                      k_pool: torch.Tensor, v_pool: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                      cu: Optional[torch.Tensor] = None, interleaved: bool = False, amplitude: float = 1.0,
+                      out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """``rvq_cache_append`` with rotary positions: new frame i of clip b is at position ``lens[b] + i``. Keys turn on
+    their way into the pages, values go there as they are, and the queries ``q`` [T, Hq, D] (None: there are none) are
+    returned turned, in ``out`` where given (which may be ``q``)."""
+    _require_pools(k_pool, v_pool, (4,))
+    dtype, dev = k_pool.dtype, k_pool.device
+    _, heads, _, dim = k_pool.shape
+    k_heads = _require_heads(k, "k", dtype, dev, heads, dim)
+    n = k.shape[0]
+    v_heads = _require_heads(v, "v", dtype, dev, heads, dim, n)
+    _require_table(table, lens, dev)
+    clips, cols = table.shape
+    if cu is not None:
+        _offsets(cu, "cu", dev, clips)
+    elif n != clips:
+        raise ValueError("without cu, k must have one frame per clip")
+    rotation = _rotation(frequencies, interleaved, False, amplitude, dev, dim)
+    hq, q_heads, to = 0, None, None
+    if q is not None:
+        q_heads = _require_heads(q, "q", dtype, dev, dim=dim, tokens=n)
+        hq = q.shape[1]
+        if out is None:
+            out = q.new_empty(q.shape)
+        to = q_heads if out is q else _require_heads(out, "out", dtype, dev, hq, dim, n)
+    elif out is not None:
+        raise ValueError("out needs q")
+    st = _lib().rvq_rotary_append(_cache_shape(k_pool, clips, cols), rotation, hq, q_heads, k_heads, v_heads, n,
+                                  _ptr(cu), table.data_ptr(), lens.data_ptr(), to, k_pool.data_ptr(),
+                                  v_pool.data_ptr(), _stream(k_pool))
+    _check("rvq_rotary_append", st)
     return out
 
 

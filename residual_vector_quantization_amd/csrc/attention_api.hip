@@ -109,6 +109,26 @@ int64_t page_bytes(const rvq_cache_shape *s)
     return static_cast<int64_t>(s->kv_heads) * s->page_size * s->dim * element_bytes(s->dtype);
 }
 
+bool good_rotation(const rvq_rotation *r)
+{
+    return r && r->frequencies && aligned(r->frequencies, 8) && r->rot_dim >= 2 && r->rot_dim % 2 == 0 && isfinite(r->amplitude);
+}
+
+rvq::RotaryArgs rotary_args(const rvq_rotation *r, int32_t dtype, int32_t dim, int64_t n_tokens, int32_t n_clips)
+{
+    rvq::RotaryArgs a = {};
+    a.dtype = dtype;
+    a.dim = dim;
+    a.rot_dim = r->rot_dim;
+    a.interleaved = r->interleaved != 0;
+    a.inverse = r->inverse != 0;
+    a.amplitude = r->amplitude;
+    a.frequencies = r->frequencies;
+    a.n_tokens = n_tokens;
+    a.n_clips = n_clips;
+    return a;
+}
+
 bool ints(const void *p) { return p && aligned(p, 4); }
 
 bool scratch(const void *p, int64_t given, int64_t wanted)
@@ -247,6 +267,100 @@ RVQ_API rvq_status rvq_cache_append(const rvq_cache_shape *shape, const rvq_head
                                              shape->dim, element_bytes(shape->dtype), shape->page_size,
                                              shape->n_pages, shape->table_ld, table, lens, k_pool, v_pool,
                                              static_cast<hipStream_t>(stream)));
+}
+
+RVQ_API rvq_status rvq_rotary_frequencies(int32_t rot_dim, double base, int32_t scaling, double factor,
+                                          double context, double slow, double fast, double *frequencies)
+{
+    if (rot_dim < 2 || rot_dim % 2 != 0 || !frequencies || !isfinite(base) || base <= 0.0) return RVQ_ERR_INVALID_ARG;
+    if (scaling < RVQ_ROTARY_PLAIN || scaling > RVQ_ROTARY_RAMP) return RVQ_ERR_INVALID_ARG;
+    if (scaling != RVQ_ROTARY_PLAIN && (!isfinite(factor) || factor <= 0.0)) return RVQ_ERR_INVALID_ARG;
+    if (scaling == RVQ_ROTARY_RAMP &&
+        (!isfinite(context) || context <= 0.0 || !isfinite(slow) || !isfinite(fast) || slow >= fast))
+        return RVQ_ERR_INVALID_ARG;
+    if (scaling == RVQ_ROTARY_BASE && rot_dim > 2) base *= pow(factor, rot_dim / (rot_dim - 2.0));
+    for (int32_t i = 0; i < rot_dim / 2; ++i) {
+        double f = pow(base, -2.0 * i / rot_dim);
+        if (scaling == RVQ_ROTARY_LINEAR) f /= factor;
+        if (scaling == RVQ_ROTARY_RAMP) {
+            const double turns = context * f / 6.283185307179586476925;
+            const double keep = fmin(fmax((turns - slow) / (fast - slow), 0.0), 1.0);
+            f *= keep + (1.0 - keep) / factor;
+        }
+        frequencies[i] = f;
+    }
+    return RVQ_OK;
+}
+
+RVQ_API rvq_status rvq_rotary(const rvq_rotation *rotation, int32_t dtype, int64_t n_tokens, int32_t q_heads,
+                              int32_t kv_heads, int32_t dim, int32_t n_clips, const int32_t *cu, const int32_t *first,
+                              const int32_t *positions, const rvq_heads *q, const rvq_heads *k,
+                              const rvq_heads *q_out, const rvq_heads *k_out, void *stream)
+{
+    if (!good_rotation(rotation) || !known_dtype(dtype) || n_tokens < 0 || q_heads < 0 || kv_heads < 0 || dim <= 0 ||
+        n_clips < 0)
+        return RVQ_ERR_INVALID_ARG;
+    if ((dim != 64 && dim != 128) || n_tokens > INT_MAX - 1024 || q_heads > 65535 || kv_heads > 65535 ||
+        n_clips > (1 << 20))
+        return RVQ_ERR_UNSUPPORTED;
+    if (rotation->rot_dim > dim) return RVQ_ERR_INVALID_ARG;
+    if (n_tokens == 0 || q_heads + kv_heads == 0 || (!positions && n_clips == 0)) return RVQ_OK;
+    if (positions ? !aligned(positions, 4) : !ints(cu) || (first && !aligned(first, 4))) return RVQ_ERR_INVALID_ARG;
+    rvq::RotaryArgs a = rotary_args(rotation, dtype, dim, n_tokens, n_clips);
+    if (q_heads > 0) {
+        if (!good_heads(q, dtype) || !good_output(q_out, dtype, q_heads, dim, n_tokens)) return RVQ_ERR_INVALID_ARG;
+        a.q = heads(q);
+        a.q_out = heads(q_out);
+    }
+    if (kv_heads > 0) {
+        if (!good_heads(k, dtype) || !good_output(k_out, dtype, kv_heads, dim, n_tokens)) return RVQ_ERR_INVALID_ARG;
+        a.k = heads(k);
+        a.k_out = heads(k_out);
+    }
+    a.q_heads = q_heads;
+    a.kv_heads = kv_heads;
+    a.positions = positions;
+    a.cu = positions ? nullptr : cu;
+    a.first = positions ? nullptr : first;
+    return from_hip(rvq::launch_rotary(a, static_cast<hipStream_t>(stream)));
+}
+
+RVQ_API rvq_status rvq_rotary_append(const rvq_cache_shape *shape, const rvq_rotation *rotation, int32_t q_heads,
+                                     const rvq_heads *q, const rvq_heads *k, const rvq_heads *v, int64_t n_tokens,
+                                     const int32_t *cu, const int32_t *table, const int32_t *lens,
+                                     const rvq_heads *q_out, void *k_pool, void *v_pool, void *stream)
+{
+    const rvq_status st = check_cache(shape);
+    if (st != RVQ_OK) return st;
+    if (!good_rotation(rotation) || rotation->rot_dim > shape->dim || rotation->inverse != 0 || q_heads < 0 ||
+        n_tokens < 0 || (!cu && n_tokens != shape->n_clips))
+        return RVQ_ERR_INVALID_ARG;
+    if (n_tokens > INT_MAX - 1024 || q_heads > 65535 || shape->n_clips > (1 << 20)) return RVQ_ERR_UNSUPPORTED;
+    if (n_tokens == 0 || shape->n_clips == 0) return RVQ_OK;
+    const bool pages = shape->n_pages > 0 && shape->table_ld > 0;
+    if (!good_heads(k, shape->dtype) || !good_heads(v, shape->dtype) || !ints(lens) || (cu && !aligned(cu, 4)) ||
+        (pages && (!ints(table) || !k_pool || !v_pool || !aligned(k_pool, 16) || !aligned(v_pool, 16))))
+        return RVQ_ERR_INVALID_ARG;
+    rvq::RotaryArgs a = rotary_args(rotation, shape->dtype, shape->dim, n_tokens, shape->n_clips);
+    if (q_heads > 0) {
+        if (!good_heads(q, shape->dtype) || !good_output(q_out, shape->dtype, q_heads, shape->dim, n_tokens))
+            return RVQ_ERR_INVALID_ARG;
+        a.q = heads(q);
+        a.q_out = heads(q_out);
+    }
+    a.q_heads = q_heads;
+    a.kv_heads = shape->kv_heads;
+    a.k = heads(k);
+    a.v = heads(v);
+    a.cu = cu;
+    a.first = lens;
+    a.page_size = shape->page_size;
+    a.n_pages = shape->n_pages;
+    a.table_ld = pages ? shape->table_ld : 0;
+    a.table = table;
+    a.k_pool = k_pool;
+    a.v_pool = v_pool;
+    return from_hip(rvq::launch_rotary_append(a, static_cast<hipStream_t>(stream)));
 }
 
 RVQ_API int64_t rvq_cache_scratch_bytes(int32_t n_clips, int32_t n_pages)

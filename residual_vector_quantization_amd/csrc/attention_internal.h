@@ -39,12 +39,29 @@ struct CacheAttentionArgs {
     void *workspace;
 };
 
+// Rotary positions: of q and k into q_out and k_out, or (append) of q into q_out and of k, with v, into the pools.
+struct RotaryArgs {
+    int dtype, dim, rot_dim, n_clips, q_heads, kv_heads;
+    bool interleaved, inverse;
+    float amplitude;
+    int64_t n_tokens;             // below 2^31
+    const int32_t *cu, *first, *positions;   // positions, or cu (null in an append: token = clip) and first (null: 0)
+    const double *frequencies;    // [rot_dim / 2]
+    Heads q, k, q_out, k_out, v;
+    int page_size, n_pages, table_ld;
+    const int32_t *table;
+    void *k_pool, *v_pool;
+};
+
 // A launch holds fewer than 2^32 threads. Launches that need more are refused with hipErrorNotSupported before any other.
 inline bool fits(int64_t groups, int threads) { return groups <= 0xffffffffll / threads; }
 
 hipError_t launch_window_attention(const AttentionArgs &a, hipStream_t stream);
 int64_t window_attention_backward_bytes(const AttentionArgs &a);     // of the shape alone
 hipError_t launch_window_attention_backward(const AttentionArgs &a, hipStream_t stream);
+
+hipError_t launch_rotary(const RotaryArgs &a, hipStream_t stream);
+hipError_t launch_rotary_append(const RotaryArgs &a, hipStream_t stream);
 
 int64_t cache_attention_bytes(int n_clips, int q_heads, int kv_heads, int dim, int64_t capacity);
 hipError_t launch_cache_attention(const CacheAttentionArgs &a, hipStream_t stream);
