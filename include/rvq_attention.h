@@ -1,8 +1,8 @@
 /*
  * rvq_attention.h -- C ABI of the streaming-attention operators of librvq:
  * windowed attention with its gradient, attention of one new frame over a
- * paged key-value cache, rotary positions, and the upkeep of the cache's
- * pages.
+ * paged key-value cache and of a chunk of new frames over it, rotary positions,
+ * and the upkeep of the cache's pages.
  *
  * These are the operators of the transformers that stand around a residual
  * quantizer and of the models that generate its codes: both run over frames
@@ -184,6 +184,37 @@ RVQ_API rvq_status rvq_cache_attention(const rvq_cache_shape *shape, int32_t q_h
                                        const void *k_pool, const void *v_pool, const int32_t *table,
                                        const int32_t *lens, int64_t window, int32_t sinks, float scale,
                                        const rvq_heads *out, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * rvq_cache_chunk_attention -- attention of every clip's newest frames, as
+ * many as each has: drafted frames that are looked at together, the next
+ * piece of a long recording, single frames of some clips beside whole chunks of
+ * others.
+ *
+ *   q, out     [n_tokens, q_heads, dim], packed by clip
+ *   cu         [n_clips + 1] int32: clip b's queries are cu[b] .. cu[b+1]-1
+ *              (non-decreasing, within 0..n_tokens; rows outside every clip
+ *              are not written); NULL: one query each, n_tokens == n_clips
+ *   lens       counts with the new frames, whose keys and values are in the
+ *              cache: query i of n is at position lens[b] - n + i. Queries at
+ *              negative positions see nothing
+ *   lse        [q_heads, n_tokens] float32 as in rvq_window_attention, or NULL
+ *   window, sinks, scale   as in rvq_window_attention
+ *   workspace  device memory of at least rvq_cache_chunk_attention_bytes(shape,
+ *              q_heads, n_tokens) bytes, 16-byte aligned (NULL where that is 0)
+ *
+ * Only pages with frames that are seen need to be there. A query that sees a
+ * frame without a valid page gets quiet NaN, and so do all queries of a clip
+ * whose count is beyond the table. A value that a query does not see has no
+ * influence on its output, not even where it is infinite or NaN; a seen one
+ * that is not finite makes the output not finite there.
+ */
+RVQ_API int64_t rvq_cache_chunk_attention_bytes(const rvq_cache_shape *shape, int32_t q_heads, int64_t n_tokens);
+RVQ_API rvq_status rvq_cache_chunk_attention(const rvq_cache_shape *shape, int32_t q_heads, int64_t n_tokens,
+                                             const int32_t *cu, const rvq_heads *q, const void *k_pool,
+                                             const void *v_pool, const int32_t *table, const int32_t *lens,
+                                             int64_t window, int32_t sinks, float scale, const rvq_heads *out,
+                                             float *lse, void *workspace, int64_t workspace_bytes, void *stream);
 
 /*
  * Rotary positions. Of every head's first rot_dim values (even, 2..dim) pair

@@ -574,7 +574,8 @@ def rvq_cosine_encode(h: torch.Tensor, w_in: torch.Tensor, b_in: Optional[torch.
 
 
 from .attention import (EXPORTED_ATTENTION, rvq_cache_append, rvq_cache_attention,  # noqa: E402,F401
-                        rvq_cache_attention_bytes, rvq_cache_compact, rvq_cache_copy, rvq_cache_fork,
+                        rvq_cache_attention_bytes, rvq_cache_chunk_attention, rvq_cache_chunk_attention_bytes,
+                        rvq_cache_compact, rvq_cache_copy, rvq_cache_fork,
                         rvq_cache_free, rvq_cache_reserve, rvq_cache_scratch_bytes, rvq_rotary, rvq_rotary_append,
                         rvq_rotary_frequencies, rvq_window_attention,
                         rvq_window_attention_backward, rvq_window_attention_backward_bytes)

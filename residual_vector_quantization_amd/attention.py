@@ -8,6 +8,8 @@ workspaces come from ``torch.empty``, raw pointers and the current HIP stream go
   -> ``(dq, dk, dv)``
 * ``rvq_cache_append(k, v, k_pool, v_pool, table, lens, cu=None)``
 * ``rvq_cache_attention(q, k_pool, v_pool, table, lens, window=None, sinks=0, scale=None)`` -> ``out``
+* ``rvq_cache_chunk_attention(q, k_pool, v_pool, table, lens, cu=None, window=None, sinks=0, scale=None)``
+  -> ``(out, lse)``
 * ``rvq_rotary_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, context=0, slow=1.0, fast=32.0)``
   -> float64 CPU tensor
 * ``rvq_rotary(q, k, frequencies, cu=None, first=None, positions=None, interleaved=False, amplitude=1.0,
@@ -42,7 +44,7 @@ EXPORTED_ATTENTION = ("rvq_window_attention", "rvq_window_attention_backward", "
                       "rvq_cache_append", "rvq_cache_attention", "rvq_cache_attention_bytes",
                       "rvq_cache_scratch_bytes", "rvq_cache_reserve", "rvq_cache_fork", "rvq_cache_free",
                       "rvq_cache_compact", "rvq_cache_copy", "rvq_rotary_frequencies", "rvq_rotary",
-                      "rvq_rotary_append")
+                      "rvq_rotary_append", "rvq_cache_chunk_attention", "rvq_cache_chunk_attention_bytes")
 
 DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 SCALINGS = {None: 0, "linear": 1, "base": 2, "ramp": 3}
@@ -95,6 +97,9 @@ def _lib() -> ctypes.CDLL:
             ("rvq_cache_attention_bytes", i64, [cache, i32]),
             ("rvq_cache_attention", ctypes.c_int,
              [cache, i32, heads, vp, vp, vp, vp, i64, i32, f32, heads, vp, i64, vp]),
+            ("rvq_cache_chunk_attention_bytes", i64, [cache, i32, i64]),
+            ("rvq_cache_chunk_attention", ctypes.c_int,
+             [cache, i32, i64, vp, heads, vp, vp, vp, vp, i64, i32, f32, heads, vp, vp, i64, vp]),
             ("rvq_rotary_frequencies", ctypes.c_int, [i32, f64, i32, f64, f64, f64, f64, vp]),
             ("rvq_rotary", ctypes.c_int,
              [vp, i32, i64, i32, i32, i32, i32, vp, vp, vp, heads, heads, heads, heads, vp]),
@@ -347,6 +352,62 @@ def rvq_cache_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Ten
                                     workspace.numel(), _stream(k_pool))
     _check("rvq_cache_attention", st)
     return out
+
+
+def _chunk_bytes(shape: bytes, q_heads: int, tokens: int) -> int:
+    size = _lib().rvq_cache_chunk_attention_bytes(shape, q_heads, tokens)
+    if size < 0:
+        raise RVQError("rvq_cache_chunk_attention_bytes", size, rvq_status_string(size))
+    return size
+
+
+def rvq_cache_chunk_attention_bytes(k_pool: torch.Tensor, table: torch.Tensor, q_heads: int, tokens: int) -> int:
+    """Workspace of ``rvq_cache_chunk_attention`` for these pools, this table and ``tokens`` rows of ``q_heads`` heads."""
+    _require_pools(k_pool, k_pool, (4,))
+    _require(table, "table", torch.int32, 2, k_pool.device)
+    return _chunk_bytes(_cache_shape(k_pool, *table.shape), q_heads, tokens)
+
+
+def rvq_cache_chunk_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, table: torch.Tensor,
+                              lens: torch.Tensor, cu: Optional[torch.Tensor] = None, window: Optional[int] = None,
+                              sinks: int = 0, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                              workspace: Optional[torch.Tensor] = None):
+    """Attention of every clip's newest frames ``q`` [T, Hq, D] over its cache.
+
+    Clip b's queries are rows ``cu[b]`` and on (int32 [clips + 1]; None: one a clip), the last ones of the ``lens[b]``
+    frames that its cache holds; their keys and values have been appended. Returns ``(out [T, Hq, D],
+    lse [Hq, T] float32)``. ``out`` and ``workspace`` (uint8, ``rvq_cache_chunk_attention_bytes``) may be preallocated.
+    Rows outside every clip are not written.
+    """
+    _require_pools(k_pool, v_pool, (4,))
+    dev = k_pool.device
+    _require_table(table, lens, dev)
+    clips, cols = table.shape
+    _, heads, _, dim = k_pool.shape
+    q_heads = _require_heads(q, "q", k_pool.dtype, dev, dim=dim)
+    n, hq, _ = q.shape
+    if cu is not None:
+        _offsets(cu, "cu", dev, clips)
+    elif n != clips:
+        raise ValueError("without cu, q must have one frame per clip")
+    if heads == 0 or hq % heads != 0:
+        raise ValueError(f"q's heads ({hq}) must be a multiple of the pools' ({heads})")
+    if sinks < 0:
+        raise ValueError(f"sinks={sinks} must not be negative")
+    if out is None:
+        out = q.new_empty((n, hq, dim))
+    out_heads = _require_heads(out, "out", q.dtype, dev, hq, dim, n)
+    lse = q.new_empty((hq, n), dtype=torch.float32)
+    shape = _cache_shape(k_pool, clips, cols)
+    if workspace is None:
+        workspace = q.new_empty(_chunk_bytes(shape, hq, n), dtype=torch.uint8)
+    _require(workspace, "workspace", torch.uint8, 1, dev)
+    st = _lib().rvq_cache_chunk_attention(shape, hq, n, _ptr(cu), q_heads, k_pool.data_ptr(), v_pool.data_ptr(),
+                                          table.data_ptr(), lens.data_ptr(), _window(window), sinks,
+                                          1.0 / math.sqrt(dim) if scale is None else scale, out_heads, lse.data_ptr(),
+                                          workspace.data_ptr(), workspace.numel(), _stream(k_pool))
+    _check("rvq_cache_chunk_attention", st)
+    return out, lse
 
 
 def rvq_rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,

@@ -21,7 +21,8 @@ PROBE_LIBRARY = os.path.join(PKG, "librvq_probe.so")
 PROBE_SOURCES = ["probes.hip"]
 SOURCES = ["rvq_api.hip", "encode.hip", "encode_bf16.hip", "encode_f16.hip", "decode.hip", "linear.hip", "projected.hip",
            "cosine.hip", "noalloc.hip", "attention_api.hip", "attention.hip",
-           "attention_backward.hip", "cache_attention.hip", "cache_pages.hip", "rotary.hip"]
+           "attention_backward.hip", "cache_attention.hip", "cache_pages.hip", "rotary.hip",
+           "chunk_attention.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

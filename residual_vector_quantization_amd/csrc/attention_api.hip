@@ -109,6 +109,25 @@ int64_t page_bytes(const rvq_cache_shape *s)
     return static_cast<int64_t>(s->kv_heads) * s->page_size * s->dim * element_bytes(s->dtype);
 }
 
+// The shape, with every frame seen and more than one query a clip.
+rvq::RowsArgs chunk_args(const rvq_cache_shape *s, int32_t q_heads, int64_t n_tokens)
+{
+    static const int32_t any[1] = {0};
+    rvq::RowsArgs a = {};
+    a.dtype = s->dtype;
+    a.dim = s->dim;
+    a.n_clips = s->n_clips;
+    a.q_heads = q_heads;
+    a.kv_heads = s->kv_heads;
+    a.window = INT_MAX;
+    a.q_tokens = n_tokens;
+    a.cu_q = any;      // read by nobody: the workspace is sized for offsets
+    a.page_size = s->page_size;
+    a.n_pages = s->n_pages;
+    a.table_ld = s->table_ld;
+    return a;
+}
+
 bool good_rotation(const rvq_rotation *r)
 {
     return r && r->frequencies && aligned(r->frequencies, 8) && r->rot_dim >= 2 && r->rot_dim % 2 == 0 && isfinite(r->amplitude);
@@ -267,6 +286,48 @@ RVQ_API rvq_status rvq_cache_append(const rvq_cache_shape *shape, const rvq_head
                                              shape->dim, element_bytes(shape->dtype), shape->page_size,
                                              shape->n_pages, shape->table_ld, table, lens, k_pool, v_pool,
                                              static_cast<hipStream_t>(stream)));
+}
+
+RVQ_API int64_t rvq_cache_chunk_attention_bytes(const rvq_cache_shape *shape, int32_t q_heads, int64_t n_tokens)
+{
+    const rvq_status st = check_cache(shape);
+    if (st != RVQ_OK) return st;
+    if (q_heads <= 0 || q_heads % shape->kv_heads != 0 || n_tokens < 0) return RVQ_ERR_INVALID_ARG;
+    if (q_heads > 65535 || shape->n_clips > (1 << 20) || n_tokens > INT_MAX - 1024) return RVQ_ERR_UNSUPPORTED;
+    rvq::RowsArgs a = chunk_args(shape, q_heads, n_tokens);
+    return rvq::chunk_attention_bytes(a);
+}
+
+RVQ_API rvq_status rvq_cache_chunk_attention(const rvq_cache_shape *shape, int32_t q_heads, int64_t n_tokens,
+                                             const int32_t *cu, const rvq_heads *q, const void *k_pool,
+                                             const void *v_pool, const int32_t *table, const int32_t *lens,
+                                             int64_t window, int32_t sinks, float scale, const rvq_heads *out,
+                                             float *lse, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    const int64_t wanted = rvq_cache_chunk_attention_bytes(shape, q_heads, n_tokens);
+    if (wanted < 0) return static_cast<rvq_status>(wanted);
+    if (sinks < 0 || !good_scale(scale) || (!cu && n_tokens != shape->n_clips)) return RVQ_ERR_INVALID_ARG;
+    if (n_tokens == 0 || shape->n_clips == 0) return RVQ_OK;
+    if (!good_heads(q, shape->dtype) || !good_output(out, shape->dtype, q_heads, shape->dim, n_tokens) ||
+        (cu && !aligned(cu, 4)) || !ints(lens) || (lse && !aligned(lse, 4)) || !scratch(workspace, workspace_bytes, wanted))
+        return RVQ_ERR_INVALID_ARG;
+    if (shape->table_ld > 0 && !ints(table)) return RVQ_ERR_INVALID_ARG;
+    if (shape->n_pages > 0 && (!k_pool || !v_pool || !aligned(k_pool, 16) || !aligned(v_pool, 16)))
+        return RVQ_ERR_INVALID_ARG;
+    rvq::RowsArgs a = chunk_args(shape, q_heads, n_tokens);
+    a.window = clamp_window(window);
+    a.sinks = sinks;
+    a.scale = scale;
+    a.cu_q = cu;
+    a.q = heads(q);
+    a.out = heads(out);
+    a.lse = lse;
+    a.k_pool = shape->n_pages > 0 ? k_pool : q->data;
+    a.v_pool = shape->n_pages > 0 ? v_pool : q->data;
+    a.table = table;
+    a.lens = lens;
+    a.workspace = workspace;
+    return from_hip(rvq::launch_chunk_attention(a, static_cast<hipStream_t>(stream)));
 }
 
 RVQ_API rvq_status rvq_rotary_frequencies(int32_t rot_dim, double base, int32_t scaling, double factor,

@@ -39,6 +39,24 @@ struct CacheAttentionArgs {
     void *workspace;
 };
 
+// Packed queries over the pages of a cache, or over packed keys.
+struct RowsArgs {
+    int dtype, dim, n_clips, q_heads, kv_heads;
+    int window, sinks;            // window INT32_MAX: unbounded
+    float scale;
+    int64_t q_tokens;             // below 2^31
+    const int32_t *cu_q;          // null: one query a clip
+    Heads q, out;
+    float *lse;                   // nullable
+    Heads k, v;                   // packed keys and values
+    const int32_t *cu_k;
+    int64_t k_tokens;
+    const void *k_pool, *v_pool;  // pages; readable rows even where there are none
+    const int32_t *table, *lens;
+    int page_size, n_pages, table_ld;
+    void *workspace;
+};
+
 // Rotary positions: of q and k into q_out and k_out, or (append) of q into q_out and of k, with v, into the pools.
 struct RotaryArgs {
     int dtype, dim, rot_dim, n_clips, q_heads, kv_heads;
@@ -59,6 +77,9 @@ inline bool fits(int64_t groups, int threads) { return groups <= 0xffffffffll / 
 hipError_t launch_window_attention(const AttentionArgs &a, hipStream_t stream);
 int64_t window_attention_backward_bytes(const AttentionArgs &a);     // of the shape alone
 hipError_t launch_window_attention_backward(const AttentionArgs &a, hipStream_t stream);
+
+int64_t chunk_attention_bytes(const RowsArgs &a);                    // of the shape alone; more with cu_q than without
+hipError_t launch_chunk_attention(const RowsArgs &a, hipStream_t stream);
 
 hipError_t launch_rotary(const RotaryArgs &a, hipStream_t stream);
 hipError_t launch_rotary_append(const RotaryArgs &a, hipStream_t stream);

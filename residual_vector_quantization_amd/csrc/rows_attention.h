@@ -1,0 +1,977 @@
+// Attention of each clip's packed queries over keys that lie elsewhere: in the
+// pages of a cache (a chunk of new frames) or packed (an encoder's states).
+//
+//   x_ij = scale q_i . k_j over the keys j that query i sees,
+//   w = softmax(x), out_i = sum_j w_ij v_j, lse_i = log sum_j exp(x_ij)
+//
+// The query heads that share a key head are rows of the same matrix products:
+// row r of a block is query r / heads and head r % heads, so that a key is read
+// once for all of them. Two kinds of workgroups share one launch, as the
+// lengths of the clips' queries are known on the device alone:
+// - few_rows takes a whole clip of up to 16 kSets rows and is bound by HBM. Its
+//   wavefronts take 32 keys in turn, which go from memory into registers and
+//   from there into 16-wide products with the rows as columns:
+//     S^T [key][row] = K Q^T,  O^T [dim][row] = V^T P^T.
+//   Only keys that some row sees are gone over (sinks, then the window), and
+//   the keys of S^T's rows are numbered so that a lane's scores belong to the 8
+//   keys of its V^T operand.
+// - tile_rows takes 128 rows, 32 a wavefront, of a clip with more, goes over
+//   tiles of 64 keys in the LDS and is bound by the matrix cores, with 32-wide
+//   products of the same form; while a tile is worked on, the next is on its way.
+// Where clips and heads make few workgroups, the keys of a row are split over
+// several; each leaves its maximum, sum and accumulator in the workspace and a
+// second launch (join_rows) joins them in order.
+//
+// Running maxima move only when a score exceeds them by more than 2^kSlack.
+// Weights enter the second product in the inputs' type, rounded once (half a step of
+// theirs beside the result's own); in float16 times 2^kShift, so that many small
+// ones beside a large one do not sink below its exponents. Their sum is of the
+// unrounded ones, in float32, as are maxima and accumulators.
+//
+// Values that a row does not see: its weights there are 0, but 0 times a value
+// that is not finite is not 0. Where rows of a workgroup see different keys and a
+// result is not finite, few_rows makes a pass for each query of its own, with
+// only what that query sees; tile_rows repeats its pass to find, for every result,
+// whether keys that are seen have an infinity of either sign there (a NaN is
+// both), and once more with these values taken as 0.
+#pragma once
+
+#include <float.h>
+#include <limits.h>
+#include <stdint.h>
+
+#include <hip/hip_runtime.h>
+
+#include "attention_device.h"
+#include "attention_internal.h"
+#include "attention_tiles.h"
+#include "cache_index.h"
+
+namespace rvq {
+namespace rows {
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kTileQueries = 32 * kWaves;   // rows of tile_rows
+constexpr int kKeys = 32;                   // keys a wavefront of few_rows takes at a time
+constexpr float kSlack = 8.0f;              // how far (powers of two) a score may exceed the running maximum
+constexpr int kMaxSplits = 256;
+
+struct Plan {
+    int group, chunks;          // query heads a key head; blocks of them that rows are made of
+    int few_limit;              // few_rows takes the clips with at most so many queries, tile_rows the others
+    int tile_queries;           // queries of a workgroup of tile_rows
+    int few_splits, tile_splits;
+    bool any_few;               // whether few_rows has workgroups
+    int tile_slots;             // blocks of queries of tile_rows, all clips
+    int mark;                   // how they are found: see block_of
+    float factor;               // scale in powers of two
+    Divisor page;
+    float *few, *tile;          // partial results
+    int64_t few_rows, tile_rows;
+};
+
+// Partial results of `rows` rows in `splits` splits: { max, sum } of each, then the accumulators.
+__host__ __device__ inline int64_t stats_floats(int64_t slots) { return (2 * slots + 3) / 4 * 4; }
+
+__device__ inline int heads_first(const Plan &p, int chunk) { return p.group * chunk / p.chunks; }
+
+// The last b in [0, n) with cu[b] / per + b <= slot (0 if there is none), searched by a whole wavefront, 64 entries at a
+// time: one read for up to 64 clips, two for 4096.
+__device__ inline int clip_of_slot_wide(const int32_t *cu, int n, int slot, int per)
+{
+    const int lane = threadIdx.x & 63;
+    int lo = 0, size = n;
+    while (size > 1) {
+        const int step = (size + 63) / 64, b = lo + lane * step;
+        const bool before = b < lo + size && cu[b] / per + b <= slot;
+        const int count = __popcll(__ballot(before));
+        if (count == 0) break;
+        size = min(step, lo + size - (lo + (count - 1) * step));
+        lo += (count - 1) * step;
+    }
+    return lo;
+}
+
+// The last b in [0, n) with cu[b] <= row, likewise.
+__device__ inline int clip_of_row_wide(const int32_t *cu, int n, int row)
+{
+    const int lane = threadIdx.x & 63;
+    int lo = 0, size = n;
+    while (size > 1) {
+        const int step = (size + 63) / 64, b = lo + lane * step;
+        const bool before = b < lo + size && cu[b] <= row;
+        const int count = __popcll(__ballot(before));
+        if (count == 0) break;
+        size = min(step, lo + size - (lo + (count - 1) * step));
+        lo += (count - 1) * step;
+    }
+    return lo;
+}
+
+// Clips and their blocks of tile_queries queries are numbered without reading their lengths. mark 0: clip b owns the
+// numbers cu[b] / tile_queries + b .., enough for its queries, q_tokens / tile_queries + n_clips + 1 in all. Where clips
+// are many and short, few have more than few_limit queries: every such clip has a row that is a multiple of mark =
+// few_limit + 1, at least as many of them as blocks (mark is at most half of tile_queries), and those rows' numbers are
+// its blocks'; others find that they are not needed.
+
+// A clip's queries and how many keys it has.
+struct ClipRows {
+    int q0, nq, nk;
+    bool beyond;       // more keys than the table can hold: nothing is read and results are NaN
+};
+
+// ---------------------------------------------------------------- where keys lie
+
+// Pages of a cache. A query at position p sees the frames j <= p of its window and the sinks.
+template <typename T, int kD>
+struct Paged {
+    static constexpr bool kAll = false;
+    const T *keys, *values;
+    const int32_t *row;
+    Divisor page;
+    int table_ld, n_pages, kv_heads, kv;
+
+    __device__ static ClipRows clip(const RowsArgs &a, int b)
+    {
+        ClipRows r;
+        if (a.cu_q) clip_range(a.cu_q, b, a.q_tokens, r.q0, r.nq);
+        else r.q0 = b, r.nq = 1;
+        r.nk = max(a.lens[b], 0);
+        r.beyond = r.nk > static_cast<int64_t>(a.table_ld) * a.page_size;
+        return r;
+    }
+    __device__ Paged(const RowsArgs &a, const Plan &p, int b, int kv_head)
+        : keys(static_cast<const T *>(a.k_pool)), values(static_cast<const T *>(a.v_pool)),
+          row(a.table + static_cast<int64_t>(b) * a.table_ld), page(p.page), table_ld(a.table_ld), n_pages(a.n_pages),
+          kv_heads(a.kv_heads), kv(kv_head) {}
+    __device__ uint32_t find(int position) const { return cache_row(row, position, page, table_ld, n_pages, kv_heads, kv); }
+    __device__ const T *key(uint32_t at) const { return keys + static_cast<uint64_t>(at) * kD; }
+    __device__ const T *value(uint32_t at) const { return values + static_cast<uint64_t>(at) * kD; }
+};
+
+// Packed rows. Every query sees all of its clip's keys.
+template <typename T, int kD>
+struct Packed {
+    static constexpr bool kAll = true;
+    const T *keys, *values;
+    int64_t key_stride, value_stride;
+
+    __device__ static ClipRows clip(const RowsArgs &a, int b)
+    {
+        ClipRows r;
+        int k0;
+        if (a.cu_q) clip_range(a.cu_q, b, a.q_tokens, r.q0, r.nq);
+        else r.q0 = b, r.nq = 1;
+        clip_range(a.cu_k, b, a.k_tokens, k0, r.nk);
+        r.beyond = false;
+        return r;
+    }
+    __device__ Packed(const RowsArgs &a, const Plan &, int b, int kv_head) : key_stride(a.k.token), value_stride(a.v.token)
+    {
+        int k0, nk;
+        clip_range(a.cu_k, b, a.k_tokens, k0, nk);
+        keys = static_cast<const T *>(a.k.data) + k0 * key_stride + kv_head * a.k.head;
+        values = static_cast<const T *>(a.v.data) + k0 * value_stride + kv_head * a.v.head;
+    }
+    __device__ uint32_t find(int position) const { return static_cast<uint32_t>(position); }
+    __device__ const T *key(uint32_t at) const { return keys + static_cast<int64_t>(at) * key_stride; }
+    __device__ const T *value(uint32_t at) const { return values + static_cast<int64_t>(at) * value_stride; }
+};
+
+template <typename Keys>
+__device__ inline int position_of(const ClipRows &r, int i) { return Keys::kAll ? r.nk - 1 : r.nk - r.nq + i; }
+
+// The frames that some query between positions p_first and p_last sees: sinks, then the window.
+__device__ inline Seen seen_between(int p_first, int p_last, int window, int sinks)
+{
+    Seen s = {0, 0, 0};
+    if (p_last < 0) return s;
+    const int64_t low = static_cast<int64_t>(p_first) - window + 1;
+    s.low = low > 0 ? static_cast<int>(low) : 0;
+    s.first = min(min(sinks, s.low), p_last + 1);
+    s.count = s.first + max(0, p_last + 1 - s.low);
+    return s;
+}
+
+// ---------------------------------------------------------------- few rows
+
+// kN values of 8 keys, as the kN operands of 8 keys at one dim.
+template <typename T, int kN>
+struct Block8 {
+    T x[8][kN];
+
+    __device__ inline void load(int i, const T *p)
+    {
+#pragma unroll
+        for (int w = 0; w < static_cast<int>(kN * sizeof(T) / 8); ++w)
+            reinterpret_cast<u32x2 *>(x[i])[w] = reinterpret_cast<const u32x2 *>(p)[w];
+    }
+    __device__ inline void clear(int i)
+    {
+#pragma unroll
+        for (int n = 0; n < kN; ++n) x[i][n] = static_cast<T>(0.0f);
+    }
+    __device__ inline vec8<T> at(int n) const
+    {
+        vec8<T> r;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = x[i][n];
+        return r;
+    }
+};
+
+// Maximum and sum over the four lane groups that hold one row.
+__device__ inline float groups_max(float x)
+{
+    x = fmaxf(x, __shfl_xor(x, 16));
+    return fmaxf(x, __shfl_xor(x, 32));
+}
+__device__ inline float groups_sum(float x)
+{
+    x += __shfl_xor(x, 16);
+    return x + __shfl_xor(x, 32);
+}
+
+template <int kD> constexpr int kFewBytes = kWaves * 16 * (kD + 4 + 2) * 4;
+
+template <typename T, int kD, typename Keys, int kSets>
+__device__ inline void few_rows(const RowsArgs &a, const Plan &p, int block, char *s_mem)
+{
+    constexpr int kSteps = kD / 32;      // products along the head dim
+    constexpr int kN = kD / 16;          // dims a lane holds of a value row
+    constexpr float kShift = kNarrow<T> ? 15.0f - kSlack : 0.0f;      // weights are below 2^(kSlack + kShift)
+    float (*s_out)[16][kD + 4] = reinterpret_cast<float (*)[16][kD + 4]>(s_mem);
+    float (*s_max)[16] = reinterpret_cast<float (*)[16]>(s_mem + kWaves * 16 * (kD + 4) * 4);
+    float (*s_sum)[16] = s_max + kWaves;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 15, g = lane >> 4;
+    // heads change fastest, then splits, then clips
+    const int columns = a.kv_heads * p.chunks;
+    const int rest = block / columns, column = block - rest * columns;
+    const int kv = column / p.chunks, chunk = column - kv * p.chunks;
+    const int clip = rest / p.few_splits, split = rest - clip * p.few_splits;
+    const ClipRows r = Keys::clip(a, clip);
+    if (r.nq == 0 || r.nq > p.few_limit) return;
+    const int heads = heads_first(p, chunk + 1) - heads_first(p, chunk), head0 = kv * p.group + heads_first(p, chunk);
+    const Keys keys(a, p, clip, kv);
+
+    // this lane's row of every set
+    int query[kSets], head[kSets];
+    vec8<T> q[kSets][kSteps];
+#pragma unroll
+    for (int s = 0; s < kSets; ++s) {
+        const int at = min(16 * s + c, r.nq * heads - 1);
+        query[s] = at / heads;
+        head[s] = head0 + at - query[s] * heads;
+        const T *from = static_cast<const T *>(a.q.data) + static_cast<int64_t>(r.q0 + query[s]) * a.q.token + head[s] * a.q.head;
+#pragma unroll
+        for (int t = 0; t < kSteps; ++t) q[s][t] = load8(from + 32 * t + 8 * g);
+    }
+    const int sets = (r.nq * heads + 15) / 16;       // the others hold no row
+
+    f32x4 o[kSets][kN];
+    float m[kSets], l[kSets];
+    // over the keys that the queries first .. last see; rows of others come out without sense
+    auto pass = [&](int first, int last) {
+        const int p_first = position_of<Keys>(r, first), p_last = position_of<Keys>(r, last);
+        const Seen seen = seen_between(r.beyond ? -1 : p_first, r.beyond ? -1 : p_last, a.window, a.sinks);
+        // positions up to `through` are seen by all of the queries if they are above `from` (or sinks)
+        const int through = p_first, from = below_window(p_last, a.window);
+#pragma unroll
+        for (int s = 0; s < kSets; ++s) {
+            m[s] = -INFINITY;
+            l[s] = r.beyond ? __builtin_nanf("") : 0.0f;
+#pragma unroll
+            for (int n = 0; n < kN; ++n) o[s][n] = f32x4{};
+        }
+        const int tiles = (seen.count + kKeys - 1) / kKeys;
+        const int per = (tiles + p.few_splits - 1) / p.few_splits;
+        const int end = min(tiles, (split + 1) * per);
+        // lane n holds the place of the tile's key n % 32
+        auto find = [&](int tile) -> uint32_t {
+            const int nth = tile * kKeys + (lane & 31);
+            if (tile >= end || nth >= seen.count) return kPastEnd;
+            return keys.find(seen_position(seen, nth));
+        };
+        int tile = split * per + wave;
+        uint32_t mine = find(tile);
+        for (; tile < end; tile += kWaves) {
+            const bool there = __all(mine < kPastEnd), lost = __any(mine == kNoPage);
+            vec8<T> k[2][kSteps];
+            Block8<T, kN> v;
+            uint32_t kr[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) kr[b] = __shfl(mine, 8 * (c >> 2) + 4 * b + (c & 3));
+            if (there) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int t = 0; t < kSteps; ++t) k[b][t] = load8(keys.key(kr[b]) + 32 * t + 8 * g);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v.load(i, keys.value(__shfl(mine, 8 * g + i)) + kN * c);
+            } else {
+                // keys that are not there are zeros: their weights are 0, and nothing is read for them
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int t = 0; t < kSteps; ++t) {
+                        k[b][t] = vec8<T>{};
+                        if (kr[b] < kPastEnd) k[b][t] = load8(keys.key(kr[b]) + 32 * t + 8 * g);
+                    }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t at = __shfl(mine, 8 * g + i);
+                    v.clear(i);
+                    if (at < kPastEnd) v.load(i, keys.value(at) + kN * c);
+                }
+            }
+            const uint32_t next = find(tile + kWaves);
+            // all keys of the tile are there and seen by every row
+            const int j_first = seen_position(seen, tile * kKeys), j_last = seen_position(seen, min(tile * kKeys + kKeys, seen.count) - 1);
+            const bool whole = there && (Keys::kAll || (j_last <= through && (j_first > from || j_last < a.sinks)));
+#pragma unroll
+            for (int s = 0; s < kSets; ++s) {
+                if (kSets > 1 && s >= sets) break;
+                if (kSets > 1) __builtin_amdgcn_sched_barrier(0);
+                // scores in powers of two: key 8 g + 4 b + i of the tile, row c
+                f32x4 x[2] = {};
+#pragma unroll
+                for (int t = 0; t < kSteps; ++t)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) x[b] = mma16(k[b][t], q[s][t], x[b]);
+                float top = -INFINITY;
+                if (!whole) {
+                    const int position = position_of<Keys>(r, query[s]), low = below_window(position, a.window);
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int nth = tile * kKeys + 8 * g + 4 * b + i, j = seen_position(seen, nth);
+                            const bool sees = nth < seen.count && (Keys::kAll || (j <= position && (j > low || j < a.sinks)));
+                            x[b][i] = sees ? x[b][i] : -INFINITY;
+                        }
+                }
+                if (!Keys::kAll && lost) {     // rare; their scores are 0 where they are seen
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (__shfl(mine, 8 * g + 4 * b + i) == kNoPage) {
+                                if (x[b][i] != -INFINITY) l[s] = __builtin_nanf("");
+                                x[b][i] = -INFINITY;
+                            }
+                }
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top = fmaxf(top, x[b][i]);
+                top *= p.factor;
+                if (__any(top > m[s] + kSlack)) {
+                    top = groups_max(top);
+                    if (top > m[s] + kSlack) {
+                        const float keep = fast_exp2(m[s] - top);
+                        m[s] = top;
+                        l[s] *= keep;
+#pragma unroll
+                        for (int n = 0; n < kN; ++n) o[s][n] *= keep;
+                    }
+                }
+                const float safe = m[s] == -INFINITY ? 0.0f : m[s] - kShift;
+                vec8<T> w;
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float e = fast_exp2(__builtin_fmaf(x[b][i], p.factor, -safe));
+                        l[s] += e;
+                        w[4 * b + i] = static_cast<T>(e);
+                    }
+#pragma unroll
+                for (int n = 0; n < kN; ++n) o[s][n] = mma16(v.at(n), w, o[s][n]);
+            }
+            mine = next;
+        }
+    };
+    // joins the wavefronts and writes the rows of queries first .. last
+    auto finish = [&](int first, int last) {
+#pragma unroll
+        for (int s = 0; s < kSets; ++s) {
+            if (s >= sets) break;
+            if (s > 0) __syncthreads();
+            const float sum = groups_sum(l[s]);
+            if (g == 0) {
+                s_max[wave][c] = m[s];
+                s_sum[wave][c] = sum;
+            }
+#pragma unroll
+            for (int n = 0; n < kN; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s_out[wave][c][kN * (4 * g + i) + n] = o[s][n][i];
+            __syncthreads();
+            const int count = min(16, r.nq * heads - 16 * s);
+            for (int at = threadIdx.x; at < count * kD; at += kThreads) {
+                const int row = at / kD, d = at - row * kD, i = (16 * s + row) / heads, h = head0 + (16 * s + row) - i * heads;
+                if (i < first || i > last) continue;
+                float top = -INFINITY, total = 0.0f, y = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) top = fmaxf(top, s_max[w][row]);
+                const float safe = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) {
+                    const float f = fast_exp2(s_max[w][row] - safe);
+                    total += s_sum[w][row] * f;
+                    y += s_out[w][row][d] * f;
+                }
+                if (p.few_splits == 1) {
+                    T *out = static_cast<T *>(a.out.data) + static_cast<int64_t>(r.q0 + i) * a.out.token + h * a.out.head;
+                    out[d] = static_cast<T>(total == 0.0f ? 0.0f : y / total);
+                    if (a.lse && d == 0)
+                        a.lse[static_cast<int64_t>(h) * a.q_tokens + r.q0 + i] =
+                            total == 0.0f ? -INFINITY : (top - kShift + log2f(total)) * kLn2;
+                } else {
+                    const int64_t slot = ((static_cast<int64_t>(clip) * p.few_limit + i) * a.q_heads + h) * p.few_splits + split;
+                    p.few[stats_floats(p.few_rows * p.few_splits) + slot * kD + d] = y;
+                    if (d == 0) {
+                        p.few[2 * slot] = top - kShift;
+                        p.few[2 * slot + 1] = total;
+                    }
+                }
+            }
+        }
+    };
+    // all queries at once, or, after a result that is not finite, one after another
+    bool each = Keys::kAll || r.nq == 1;
+    for (int first = 0, last = r.nq - 1;;) {
+        pass(first, last);
+        if (!each) {
+            each = true;
+            bool odd = false;
+#pragma unroll
+            for (int s = 0; s < kSets; ++s)
+#pragma unroll
+                for (int n = 0; n < kN; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) odd = odd || !(fabsf(o[s][n][i]) <= FLT_MAX);
+            if (__syncthreads_or(odd)) {
+                last = 0;
+                continue;
+            }
+        }
+        finish(first, last);
+        if (last == r.nq - 1) break;
+        first = ++last;
+        __syncthreads();      // what was left in the LDS has been read
+    }
+}
+
+// ---------------------------------------------------------------- tiles of many rows
+
+// As copy16, from an address of 64 bits in each lane.
+__device__ inline void copy16_from(const void *src, void *dst)
+{
+    const unsigned m0 = static_cast<unsigned>(reinterpret_cast<size_t>((lds_void *)dst));
+    asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(m0) : "memory");
+}
+
+// Tiles of keys and values that go by, as Feed, from where they lie. start sets out for a tile, turn waits for it and
+// sets out for the next. gone: a bit for each of the current tile's keys that is not there (what lies in its place is
+// some other row).
+template <typename T, int kD, typename Keys> struct Tiles;
+
+template <typename T, int kD>
+struct Tiles<T, kD, Packed<T, kD>> {
+    typedef Feed<T, kD, kWaves> Memory;
+    typedef typename Memory::Rows Rows;
+    static constexpr int kBytes = Memory::kBytes;
+    Memory feed;
+    const Packed<T, kD> &keys;
+    const KeyRange &range;
+    int last;
+
+    __device__ Tiles(char *s, const Packed<T, kD> &from, const KeyRange &r, int last_position)
+        : feed(s, from.key_stride, from.value_stride), keys(from), range(r), last(last_position) {}
+    __device__ void start(int t, int) { feed.start(keys.keys, keys.values, range.start(t), last + 1); }
+    template <int kBuffer>
+    __device__ uint64_t turn(Constant<kBuffer> buffer, int t, int end)
+    {
+        feed.turn(buffer, t + 1 < end, keys.keys, keys.values, range.start(t + 1), last + 1);
+        return 0;
+    }
+    template <int kBuffer> __device__ char *tile_keys(Constant<kBuffer> b) const { return feed.tile_one(b); }
+    template <int kBuffer> __device__ char *tile_values(Constant<kBuffer> b) const { return feed.tile_two(b); }
+};
+
+// From pages: lane n holds the place of the next tile's key n, looked up one tile ahead of the copies that need it.
+template <typename T, int kD>
+struct PagedPlaces {
+    const Paged<T, kD> &keys;
+    const KeyRange &range;
+    int last;
+    uint32_t next;
+    uint64_t gone;
+
+    __device__ PagedPlaces(const Paged<T, kD> &from, const KeyRange &r, int last_position)
+        : keys(from), range(r), last(last_position), next(0), gone(0) {}
+    // keys behind the last one that is seen: that one again
+    __device__ void look(int t, int end)
+    {
+        if (t < end) next = keys.find(min(range.start(t) + static_cast<int>(threadIdx.x & 63), last));
+    }
+    // row 0 of the pools in the place of keys that are not there
+    __device__ void take()
+    {
+        gone = __ballot(next == kNoPage);
+        if (next == kNoPage) next = 0;
+    }
+};
+
+template <typename T, int kD>
+struct Tiles<T, kD, Paged<T, kD>> {
+    typedef Tile<T, kD, kWaves> Rows;
+    static constexpr int kBytes = 4 * Rows::kBytes;
+    PagedPlaces<T, kD> places;
+    char *s;
+
+    __device__ Tiles(char *memory, const Paged<T, kD> &from, const KeyRange &r, int last_position)
+        : places(from, r, last_position), s(memory) {}
+    __device__ void load(int buffer)
+    {
+        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        places.take();
+        char *to = s + buffer * 2 * Rows::kBytes;
+#pragma unroll
+        for (int n = 0; n < Rows::kCopies; ++n) {
+            const int at = (n * kWaves + wave) * 64 + lane, row = at / Rows::kRowPieces;
+            const uint64_t offset = static_cast<uint64_t>(__shfl(places.next, row)) * Rows::kRowBytes + Rows::place(row, at % Rows::kRowPieces) * 16;
+            copy16_from(reinterpret_cast<const char *>(places.keys.keys) + offset, to + (n * kWaves + wave) * 1024);
+            copy16_from(reinterpret_cast<const char *>(places.keys.values) + offset, to + Rows::kBytes + (n * kWaves + wave) * 1024);
+        }
+    }
+    __device__ void start(int t, int end)
+    {
+        places.look(t, end);
+        load(0);
+        places.look(t + 1, end);
+    }
+    template <int kBuffer>
+    __device__ uint64_t turn(Constant<kBuffer>, int t, int end)
+    {
+        const uint64_t gone = places.gone;
+        wait_copies();
+        __syncthreads();
+        if (t + 1 < end) {
+            load(1 - kBuffer);
+            places.look(t + 2, end);
+        }
+        return gone;
+    }
+    template <int kBuffer> __device__ char *tile_keys(Constant<kBuffer>) const { return s + kBuffer * 2 * Rows::kBytes; }
+    template <int kBuffer> __device__ char *tile_values(Constant<kBuffer>) const { return s + (kBuffer * 2 + 1) * Rows::kBytes; }
+};
+
+template <int kD>
+struct Tiles<float, kD, Paged<float, kD>> {
+    typedef SplitTile<kD, kWaves> Rows;
+    static constexpr int kBytes = 2 * Rows::kBytes;
+    PagedPlaces<float, kD> places;
+    typename Rows::Loader one, two;
+    char *s;
+
+    __device__ Tiles(char *memory, const Paged<float, kD> &from, const KeyRange &r, int last_position)
+        : places(from, r, last_position), one(0), two(0), s(memory) {}
+    __device__ void load()
+    {
+        places.take();
+#pragma unroll
+        for (int n = 0; n < Rows::kUnits; ++n) {
+            const int at = n * kThreads + threadIdx.x, row = at / (kD / 8), piece = at % (kD / 8);
+            const uint32_t place = __shfl(places.next, row);
+            one.x[n] = load8(places.keys.key(place) + 8 * piece);
+            two.x[n] = load8(places.keys.value(place) + 8 * piece);
+        }
+    }
+    __device__ void start(int t, int end)
+    {
+        places.look(t, end);
+        load();
+        places.look(t + 1, end);
+    }
+    template <int kBuffer>
+    __device__ uint64_t turn(Constant<kBuffer>, int t, int end)
+    {
+        const uint64_t gone = places.gone;
+        __syncthreads();
+        one.store(s);
+        two.store(s + Rows::kBytes);
+        __syncthreads();
+        if (t + 1 < end) {
+            load();
+            places.look(t + 2, end);
+        }
+        return gone;
+    }
+    template <int kBuffer> __device__ char *tile_keys(Constant<kBuffer>) const { return s; }
+    template <int kBuffer> __device__ char *tile_values(Constant<kBuffer>) const { return s + Rows::kBytes; }
+};
+
+template <typename T, int kD, typename Keys>
+__device__ inline void tile_rows(const RowsArgs &a, const Plan &p, int block, char *s_mem)
+{
+    typedef Tiles<T, kD, Keys> Source;
+    typedef typename Source::Rows Rows;
+    constexpr float kShift = kNarrow<T> ? 15.0f - kSlack : 0.0f;      // weights are below 2^(kSlack + kShift)
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 31, half = lane >> 5;
+    // heads change fastest, then splits; the last queries of a clip, which see most, start first
+    const int columns = a.kv_heads * p.chunks;
+    const int rest = block / columns, column = block - rest * columns;
+    const int kv = column / p.chunks, chunk = column - kv * p.chunks;
+    const int slot = p.tile_slots - 1 - rest / p.tile_splits, split = rest % p.tile_splits;
+    const int clip = p.mark ? clip_of_row_wide(a.cu_q, a.n_clips, slot * p.mark)
+                            : clip_of_slot_wide(a.cu_q, a.n_clips, slot, p.tile_queries);
+    const ClipRows r = Keys::clip(a, clip);
+    const int64_t nth = p.mark ? slot - (r.q0 + p.mark - 1) / p.mark : slot - (a.cu_q[clip] / p.tile_queries + clip);
+    if (nth < 0 || nth * p.tile_queries >= r.nq || r.nq <= p.few_limit) return;
+    const int i0 = static_cast<int>(nth) * p.tile_queries;
+    const int heads = heads_first(p, chunk + 1) - heads_first(p, chunk), head0 = kv * p.group + heads_first(p, chunk);
+    const Keys keys(a, p, clip, kv);
+
+    const int used = min(p.tile_queries, r.nq - i0) * heads;      // rows
+    const int row = min(32 * wave + c, used - 1);
+    const bool real = 32 * wave + c < used;
+    const int query = i0 + row / heads, head = head0 + row % heads;
+    const int position = position_of<Keys>(r, query);
+    const int p_last = r.beyond ? -1 : position_of<Keys>(r, i0 + (used - 1) / heads);
+    const KeyRange range = keys_seen(r.beyond ? -1 : position_of<Keys>(r, i0), p_last, a.window, a.sinks);
+    const int per = (range.tiles + p.tile_splits - 1) / p.tile_splits;
+    const int begin = min(split * per, range.tiles), end = min(begin + per, range.tiles);
+    // this wavefront's first and last position; one without a row of its own sees no tile
+    const int w_first = position_of<Keys>(r, i0 + min(32 * wave, used - 1) / heads);
+    const int w_last = 32 * wave < used ? position_of<Keys>(r, i0 + min(32 * wave + 31, used - 1) / heads) : -1;
+    // positions above these are in the window of this query, of the wavefront's first and of its last
+    const int p_low = below_window(position, a.window), w_low = below_window(w_first, a.window);
+    const int w_high = below_window(w_last, a.window);
+
+    const T *own = static_cast<const T *>(a.q.data) + static_cast<int64_t>(r.q0 + query) * a.q.token + head * a.q.head;
+    Operand<T> q[kD / 16];
+#pragma unroll
+    for (int t = 0; t < kD / 16; ++t) q[t] = Operand<T>(load8(own + 16 * t + 8 * half));
+#pragma unroll
+    for (int t = 0; t < kD / 16; ++t) arrive(q[t]);
+    Source source(s_mem, keys, range, p_last);
+
+    f32x16 o[kD / 32];
+    float m, l;
+    bool bad = r.beyond;
+
+    // One tile of keys. The buffer's number is a constant, so that LDS addresses are; markers and clean (the values
+    // of a tile are rewritten) make the later passes.
+    auto tile = [&](int t, auto buffer, auto markers, auto clean) {
+        const uint64_t gone = source.turn(buffer, t, end);
+        char *s_k = source.tile_keys(buffer), *s_v = source.tile_values(buffer);
+        if (clean.value) {
+            only_finite<Rows, kD, kThreads>(s_v, markers.value);
+            __syncthreads();
+        }
+        const int j0 = range.start(t);
+        // nothing of these keys is seen by this wavefront
+        if (j0 > w_last || (j0 + kTileRows - 1 <= w_low && j0 >= a.sinks)) return;
+        f32x16 x[2] = {};
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int n = 0; n < kD / 16; ++n) x[b] = mma32(Rows::along(s_k, 32 * b + c, 2 * n + half), q[n], x[b]);
+        if constexpr (clean.value && sizeof(T) == 4) {
+            // scores that the split made NaN, again by float32 products: they may be infinite
+            bool odd = false;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) odd = odd || x[i >> 4][i & 15] != x[i >> 4][i & 15];
+            if (__any(odd)) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    f32x16 y = {};
+                    uint32_t at = keys.find(min(j0 + 32 * b + c, p_last));
+                    if (at == kNoPage) at = 0;
+                    const T *key = keys.key(at) + 8 * half;
+                    for (int n = 0; n < kD / 16; ++n) y = mma32(load8(key + 16 * n), load8(own + 16 * n + 8 * half), y);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[b][i] = x[b][i] != x[b][i] ? y[i] : x[b][i];
+                }
+            }
+        }
+        if (!(j0 + kTileRows - 1 <= w_first && (j0 > w_high || j0 + kTileRows - 1 < a.sinks))) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int j = j0 + 32 * b + 8 * (i >> 2) + 4 * half + (i & 3);
+                    x[b][i] = j <= position && (j > p_low || j < a.sinks) ? x[b][i] : -INFINITY;
+                }
+        }
+        if (gone != 0) {      // rare
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const uint32_t some = static_cast<uint32_t>(gone >> 32 * b) >> 4 * half;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int j = j0 + 32 * b + 8 * (i >> 2) + 4 * half + (i & 3);
+                    const bool lost = some >> (8 * (i >> 2) + (i & 3)) & 1;
+                    bad = bad || (lost && j <= position && (j > p_low || j < a.sinks));
+                    x[b][i] = lost ? -INFINITY : x[b][i];
+                }
+            }
+        }
+        float top = x[0][0];
+#pragma unroll
+        for (int i = 1; i < 32; ++i) top = fmaxf(top, x[i >> 4][i & 15]);
+        top *= p.factor;
+        if (__any(top > m + kSlack)) {
+            top = fmaxf(top, __shfl_xor(top, 32));
+            if (top > m + kSlack) {
+                const float keep = fast_exp2(m - top);
+                m = top;
+                l *= keep;
+                if (!markers.value) {
+#pragma unroll
+                    for (int n = 0; n < kD / 32; ++n) o[n] *= keep;
+                }
+            }
+        }
+        const float safe = m == -INFINITY ? 0.0f : m - kShift;
+        float sum[4] = {};
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            vec8<T> w[2];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float e = fast_exp2(__builtin_fmaf(x[b][i], p.factor, -safe));
+                sum[i & 3] += e;
+                if (markers.value) e = x[b][i] == -INFINITY ? 0.0f : 1.0f;
+                w[i >> 3][i & 7] = static_cast<T>(e);
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const Operand<T> weights(w[s]);
+#pragma unroll
+                for (int n = 0; n < kD / 32; ++n) o[n] = mma32(Rows::across(s_v, n, 2 * b + s), weights, o[n]);
+            }
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        if (markers.value) {
+            // counts of a tile and the one before stay below 1 / kMinus: whole and broken part apart
+#pragma unroll
+            for (int n = 0; n < kD / 32; ++n)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[n][i] = (o[n][i] >= 1.0f ? 1.0f : 0.0f) + (o[n][i] > floorf(o[n][i]) ? kMinus : 0.0f);
+        }
+    };
+    auto pass = [&](auto markers, auto clean) {
+        if (begin < end) source.start(begin, end);
+#pragma unroll
+        for (int n = 0; n < kD / 32; ++n) o[n] = f32x16{};
+        m = -INFINITY;
+        l = 0.0f;
+        for (int t = begin; t < end; t += 2) {
+            tile(t, Constant<0>{}, markers, clean);
+            if (t + 1 < end) tile(t + 1, Constant<1>{}, markers, clean);
+        }
+    };
+
+    pass(Constant<0>{}, Constant<0>{});
+    bool odd = false;
+#pragma unroll
+    for (int n = 0; n < kD / 32; ++n)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) odd = odd || !(fabsf(o[n][i]) <= FLT_MAX);
+    if (__syncthreads_or(odd)) {
+        pass(Constant<1>{}, Constant<1>{});
+        uint32_t up[kD / 64] = {}, down[kD / 64] = {};
+#pragma unroll
+        for (int n = 0; n < kD / 32; ++n)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                up[n >> 1] |= static_cast<uint32_t>(o[n][i] >= 1.0f) << (16 * (n & 1) + i);
+                down[n >> 1] |= static_cast<uint32_t>(o[n][i] > floorf(o[n][i])) << (16 * (n & 1) + i);
+            }
+        __syncthreads();     // the tiles are no longer read
+        pass(Constant<0>{}, Constant<1>{});
+#pragma unroll
+        for (int n = 0; n < kD / 32; ++n)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const bool plus = up[n >> 1] >> (16 * (n & 1) + i) & 1, minus = down[n >> 1] >> (16 * (n & 1) + i) & 1;
+                if (plus || minus) o[n][i] = plus && minus ? __builtin_nanf("") : plus ? INFINITY : -INFINITY;
+            }
+    }
+    l += __shfl_xor(l, 32);
+    bad = __shfl_xor(static_cast<int>(bad), 32) || bad;      // in this order: all lanes take part
+    if (!real) return;
+    if (bad) l = __builtin_nanf("");
+    if (p.tile_splits > 1) {
+        const int64_t at = (static_cast<int64_t>(r.q0 + query) * a.q_heads + head) * p.tile_splits + split;
+        float *out = p.tile + stats_floats(p.tile_rows * p.tile_splits) + at * kD;
+#pragma unroll
+        for (int n = 0; n < kD / 32; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<f32x4 *>(out + 32 * n + 8 * i + 4 * half) = f32x4{o[n][4 * i], o[n][4 * i + 1], o[n][4 * i + 2], o[n][4 * i + 3]};
+        if (half == 0) {
+            p.tile[2 * at] = m - kShift;
+            p.tile[2 * at + 1] = l;
+        }
+        return;
+    }
+    const float inverse = l == 0.0f ? 0.0f : 1.0f / l;
+    T *out = static_cast<T *>(a.out.data) + static_cast<int64_t>(r.q0 + query) * a.out.token + head * a.out.head;
+#pragma unroll
+    for (int n = 0; n < kD / 32; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            T y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = static_cast<T>(o[n][4 * i + e] * inverse);
+            store4(out + 32 * n + 8 * i + 4 * half, y);
+        }
+    if (a.lse && half == 0)
+        a.lse[static_cast<int64_t>(head) * a.q_tokens + r.q0 + query] = l == 0.0f ? -INFINITY : (m - kShift + log2f(l)) * kLn2;
+}
+
+// ---------------------------------------------------------------- launches
+
+// The tiles' workgroups come first: they last longer.
+template <typename T, int kD, typename Keys, int kSets>
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
+void all_rows(RowsArgs a, Plan p, int tile_groups)
+{
+    constexpr int kTileBytes = Tiles<T, kD, Keys>::kBytes;
+    __shared__ __attribute__((aligned(16))) char s_mem[kTileBytes > kFewBytes<kD> ? kTileBytes : kFewBytes<kD>];
+    const int block = blockIdx.x;
+    if (block < tile_groups) tile_rows<T, kD, Keys>(a, p, block, s_mem);
+    else few_rows<T, kD, Keys, kSets>(a, p, block - tile_groups, s_mem);
+}
+
+template <typename T, int kD, typename Keys, int kSets>
+__global__ __launch_bounds__(kThreads)
+void only_few_rows(RowsArgs a, Plan p)
+{
+    __shared__ __attribute__((aligned(16))) char s_mem[kFewBytes<kD>];
+    few_rows<T, kD, Keys, kSets>(a, p, blockIdx.x, s_mem);
+}
+
+// One wavefront a query and head: lanes find the largest maximum and the scaled sums over the splits, then add up the
+// accumulators, a lane kD / 64 dims.
+template <typename T, int kD, typename Keys>
+__global__ __launch_bounds__(64)
+void join_rows(RowsArgs a, Plan p)
+{
+    const int token = blockIdx.x, head = blockIdx.y, lane = threadIdx.x;
+    const int clip = a.cu_q ? clip_of_row_wide(a.cu_q, a.n_clips, token) : token;
+    const ClipRows r = Keys::clip(a, clip);
+    const int i = token - r.q0;
+    if (i < 0 || i >= r.nq) return;
+    const bool few = r.nq <= p.few_limit;
+    const int splits = few ? p.few_splits : p.tile_splits;
+    if (splits == 1) return;
+    const float *part = few ? p.few : p.tile;
+    const int64_t row = few ? (static_cast<int64_t>(clip) * p.few_limit + i) * a.q_heads + head : static_cast<int64_t>(token) * a.q_heads + head;
+    const float *stats = part + 2 * row * splits;
+    const float *sums = part + stats_floats((few ? p.few_rows : p.tile_rows) * splits) + row * splits * kD;
+    __shared__ float s_factor[kMaxSplits];
+    float top = -INFINITY;
+    for (int s = lane; s < splits; s += 64) top = fmaxf(top, stats[2 * s]);
+#pragma unroll
+    for (int x = 32; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
+    const float safe = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f;
+    for (int s = lane; s < splits; s += 64) {
+        const float f = fast_exp2(stats[2 * s] - safe);
+        s_factor[s] = f;
+        sum += stats[2 * s + 1] * f;
+    }
+    sum = wave_sum(sum);
+    __syncthreads();
+    float y[kD / 64] = {};
+#pragma unroll 8
+    for (int s = 0; s < splits; ++s)
+#pragma unroll
+        for (int n = 0; n < kD / 64; ++n) y[n] += sums[s * kD + 64 * n + lane] * s_factor[s];
+    T *out = static_cast<T *>(a.out.data) + static_cast<int64_t>(token) * a.out.token + head * a.out.head;
+#pragma unroll
+    for (int n = 0; n < kD / 64; ++n) out[64 * n + lane] = static_cast<T>(sum == 0.0f ? 0.0f : y[n] / sum);
+    if (a.lse && lane == 0) a.lse[static_cast<int64_t>(head) * a.q_tokens + token] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+// How the rows are shared out. It depends on shapes alone, so that the workspace's size is known beforehand. keys: the
+// most that a clip can have.
+inline Plan plan(const RowsArgs &a, int64_t keys, int64_t &floats)
+{
+    constexpr int64_t kWanted = 2048, kWantedTiles = 512;      // workgroups that fill the chip
+    Plan p = {};
+    p.group = a.q_heads / a.kv_heads;
+    p.chunks = (p.group + 31) / 32;
+    const int heads = (p.group + p.chunks - 1) / p.chunks;
+    const int64_t columns = static_cast<int64_t>(a.kv_heads) * p.chunks;
+    const int64_t average = a.n_clips ? (a.q_tokens + a.n_clips - 1) / a.n_clips : 0;
+    // 16 rows of few_rows where they do for most clips, 32 otherwise
+    const int rows = heads <= 16 && average * heads <= 16 ? 16 : 32;
+    p.few_limit = rows / heads;
+    const bool none_few = a.n_clips == 1 && a.q_tokens > p.few_limit, all_few = !a.cu_q || a.q_tokens <= p.few_limit;
+    if (none_few) p.few_limit = 0;
+    p.few_splits = p.tile_splits = 1;
+    p.tile_queries = kTileQueries / heads;
+    if (!none_few) {
+        const int64_t tiles = (keys + kKeys - 1) / kKeys, base = a.n_clips * columns;
+        int64_t n = base > 0 ? kWanted / base : 1;
+        const int64_t most = tiles <= 4 * kWaves ? 1 : tiles / kWaves;
+        n = n < most ? n : most;
+        p.few_splits = static_cast<int>(n < 1 ? 1 : n < kMaxSplits ? n : kMaxSplits);
+        p.any_few = true;
+    }
+    if (!all_few) {
+        const int64_t slots = a.q_tokens / p.tile_queries + a.n_clips + 1, marked = a.q_tokens / (p.few_limit + 1) + 1;
+        if (p.any_few && marked < slots) p.mark = p.few_limit + 1;
+        p.tile_slots = static_cast<int>(p.mark ? marked : slots);
+        const int64_t tiles = (keys + kTileRows - 1) / kTileRows;
+        int64_t n = kWantedTiles / ((a.q_tokens / p.tile_queries + 1) * columns);
+        n = n < tiles / 8 ? n : tiles / 8;
+        p.tile_splits = static_cast<int>(n < 1 ? 1 : n < kMaxSplits ? n : kMaxSplits);
+    }
+    p.few_rows = p.few_splits > 1 ? static_cast<int64_t>(a.n_clips) * p.few_limit * a.q_heads : 0;
+    p.tile_rows = p.tile_splits > 1 ? a.q_tokens * a.q_heads : 0;
+    p.factor = fmaxf(a.scale * kLog2e, FLT_MIN);   // scale 0: equal weights, and 0 times -inf does not arise
+    const int64_t few = stats_floats(p.few_rows * p.few_splits) + p.few_rows * p.few_splits * a.dim;
+    const int64_t tile = stats_floats(p.tile_rows * p.tile_splits) + p.tile_rows * p.tile_splits * a.dim;
+    p.few = static_cast<float *>(a.workspace);
+    p.tile = p.few + few;
+    floats = few + tile;
+    return p;
+}
+
+template <typename T, int kD, typename Keys>
+hipError_t run(const RowsArgs &a, Plan p, hipStream_t stream)
+{
+    const int64_t columns = static_cast<int64_t>(a.kv_heads) * p.chunks;
+    const int64_t few = p.any_few ? static_cast<int64_t>(a.n_clips) * p.few_splits * columns : 0;
+    const int64_t tile = p.tile_slots * static_cast<int64_t>(p.tile_splits) * columns;
+    if (!fits(few + tile, kThreads) || !fits(a.q_tokens * a.q_heads, 64)) return hipErrorNotSupported;
+    const bool one = p.few_limit * ((p.group + p.chunks - 1) / p.chunks) <= 16;
+    const unsigned n = static_cast<unsigned>(few + tile);
+    if (tile == 0 && one) only_few_rows<T, kD, Keys, 1><<<n, kThreads, 0, stream>>>(a, p);
+    else if (one) all_rows<T, kD, Keys, 1><<<n, kThreads, 0, stream>>>(a, p, static_cast<int>(tile));
+    else all_rows<T, kD, Keys, 2><<<n, kThreads, 0, stream>>>(a, p, static_cast<int>(tile));
+    if (p.few_splits > 1 || p.tile_splits > 1)
+        join_rows<T, kD, Keys><<<dim3(static_cast<unsigned>(a.q_tokens), a.q_heads), 64, 0, stream>>>(a, p);
+    return hipGetLastError();
+}
+
+template <template <typename, int> class Keys>
+hipError_t launch(const RowsArgs &a, const Plan &p, hipStream_t stream)
+{
+    if (a.dtype == RVQ_F32) return a.dim == 64 ? run<float, 64, Keys<float, 64>>(a, p, stream) : run<float, 128, Keys<float, 128>>(a, p, stream);
+    if (a.dtype == RVQ_F16) return a.dim == 64 ? run<f16_t, 64, Keys<f16_t, 64>>(a, p, stream) : run<f16_t, 128, Keys<f16_t, 128>>(a, p, stream);
+    return a.dim == 64 ? run<bf16_t, 64, Keys<bf16_t, 64>>(a, p, stream) : run<bf16_t, 128, Keys<bf16_t, 128>>(a, p, stream);
+}
+
+}  // namespace rows
+}  // namespace rvq
