@@ -1,6 +1,6 @@
 /*
  * rvq_attention.h -- C ABI of the streaming-attention operators of librvq:
- * windowed attention with its gradient, attention of one new frame over a
+ * windowed and cross attention with their gradients, attention of one new frame over a
  * paged key-value cache and of a chunk of new frames over it, rotary positions,
  * and the upkeep of the cache's pages.
  *
@@ -122,6 +122,34 @@ RVQ_API rvq_status rvq_window_attention_backward(const rvq_attention_shape *shap
                                                  const rvq_heads *out, const float *lse,
                                                  const rvq_heads *dq, const rvq_heads *dk, const rvq_heads *dv,
                                                  void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * rvq_cross_attention -- every query sees all keys of its clip: attention to
+ * an encoder's states, or without a mask within clips. The shape as above, but
+ * that window and sinks are not read and that queries and keys of a clip have
+ * no common positions; cu_q may be NULL: one query a clip, q_tokens ==
+ * n_clips (the next frame of every clip). A clip without keys has output 0,
+ * lse -inf and gradient 0. k_tokens may be 0.
+ *
+ *   workspace       device memory of at least rvq_cross_attention_bytes(shape)
+ *                   bytes, 16-byte aligned (NULL where that is 0)
+ *
+ * Padded batches: a clip's rows have to follow one another, so rows of padding
+ * may stand behind the last clip or before the first only.
+ *
+ * rvq_cross_attention_backward -- its gradients, as rvq_window_attention_backward;
+ * cu_q must be given.
+ */
+RVQ_API int64_t rvq_cross_attention_bytes(const rvq_attention_shape *shape);
+RVQ_API rvq_status rvq_cross_attention(const rvq_attention_shape *shape, const rvq_heads *q, const rvq_heads *k,
+                                       const rvq_heads *v, const rvq_heads *out, float *lse, void *workspace,
+                                       int64_t workspace_bytes, void *stream);
+RVQ_API int64_t rvq_cross_attention_backward_bytes(const rvq_attention_shape *shape);
+RVQ_API rvq_status rvq_cross_attention_backward(const rvq_attention_shape *shape, const rvq_heads *dout,
+                                                const rvq_heads *q, const rvq_heads *k, const rvq_heads *v,
+                                                const rvq_heads *out, const float *lse,
+                                                const rvq_heads *dq, const rvq_heads *dk, const rvq_heads *dv,
+                                                void *workspace, int64_t workspace_bytes, void *stream);
 
 /*
  * A paged key-value cache. Pools hold pages [n_pages, kv_heads, page_size,

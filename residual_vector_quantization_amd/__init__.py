@@ -31,8 +31,8 @@ Functions (same names as the C entry points):
 * ``rvq_cosine_prepare(codebooks)`` -> unit codewords (float64);
   ``rvq_cosine_encode(h, w_in, b_in, units, table, n_stages=None)`` -> ``(codes, latent, residual)``
 * ``rvq_version()``, ``rvq_status_string(status)``
-* the streaming-attention operators of ``include/rvq_attention.h`` (windowed attention and its gradient,
-  attention over a paged cache, the cache's pages, rotary positions): see ``attention.py``
+* the streaming-attention operators of ``include/rvq_attention.h`` (windowed and cross attention and their
+  gradients, attention over a paged cache, the cache's pages, rotary positions): see ``attention.py``
 
 ``prepared`` is ``rvq_prepare_codebooks``' output for the same codebooks; passing it selects
 the encode that reads the prepared layout (same results, faster).
@@ -576,6 +576,8 @@ def rvq_cosine_encode(h: torch.Tensor, w_in: torch.Tensor, b_in: Optional[torch.
 from .attention import (EXPORTED_ATTENTION, rvq_cache_append, rvq_cache_attention,  # noqa: E402,F401
                         rvq_cache_attention_bytes, rvq_cache_chunk_attention, rvq_cache_chunk_attention_bytes,
                         rvq_cache_compact, rvq_cache_copy, rvq_cache_fork,
-                        rvq_cache_free, rvq_cache_reserve, rvq_cache_scratch_bytes, rvq_rotary, rvq_rotary_append,
+                        rvq_cache_free, rvq_cache_reserve, rvq_cache_scratch_bytes, rvq_cross_attention,
+                        rvq_cross_attention_backward, rvq_cross_attention_backward_bytes, rvq_cross_attention_bytes,
+                        rvq_rotary, rvq_rotary_append,
                         rvq_rotary_frequencies, rvq_window_attention,
                         rvq_window_attention_backward, rvq_window_attention_backward_bytes)

@@ -6,6 +6,8 @@ workspaces come from ``torch.empty``, raw pointers and the current HIP stream go
 * ``rvq_window_attention(q, k, v, cu_q, cu_k=None, window=None, sinks=0, scale=None)`` -> ``(out, lse)``
 * ``rvq_window_attention_backward(dout, q, k, v, out, lse, cu_q, cu_k=None, window=None, sinks=0, scale=None)``
   -> ``(dq, dk, dv)``
+* ``rvq_cross_attention(q, k, v, cu_q, cu_k, scale=None)`` -> ``(out, lse)``
+* ``rvq_cross_attention_backward(dout, q, k, v, out, lse, cu_q, cu_k, scale=None)`` -> ``(dq, dk, dv)``
 * ``rvq_cache_append(k, v, k_pool, v_pool, table, lens, cu=None)``
 * ``rvq_cache_attention(q, k_pool, v_pool, table, lens, window=None, sinks=0, scale=None)`` -> ``out``
 * ``rvq_cache_chunk_attention(q, k_pool, v_pool, table, lens, cu=None, window=None, sinks=0, scale=None)``
@@ -44,7 +46,9 @@ EXPORTED_ATTENTION = ("rvq_window_attention", "rvq_window_attention_backward", "
                       "rvq_cache_append", "rvq_cache_attention", "rvq_cache_attention_bytes",
                       "rvq_cache_scratch_bytes", "rvq_cache_reserve", "rvq_cache_fork", "rvq_cache_free",
                       "rvq_cache_compact", "rvq_cache_copy", "rvq_rotary_frequencies", "rvq_rotary",
-                      "rvq_rotary_append", "rvq_cache_chunk_attention", "rvq_cache_chunk_attention_bytes")
+                      "rvq_rotary_append", "rvq_cache_chunk_attention", "rvq_cache_chunk_attention_bytes",
+                      "rvq_cross_attention", "rvq_cross_attention_bytes", "rvq_cross_attention_backward",
+                      "rvq_cross_attention_backward_bytes")
 
 DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 SCALINGS = {None: 0, "linear": 1, "base": 2, "ramp": 3}
@@ -92,6 +96,11 @@ def _lib() -> ctypes.CDLL:
             ("rvq_window_attention", ctypes.c_int, [shape, heads, heads, heads, heads, vp, vp]),
             ("rvq_window_attention_backward_bytes", i64, [shape]),
             ("rvq_window_attention_backward", ctypes.c_int,
+             [shape, heads, heads, heads, heads, heads, vp, heads, heads, heads, vp, i64, vp]),
+            ("rvq_cross_attention_bytes", i64, [shape]),
+            ("rvq_cross_attention", ctypes.c_int, [shape, heads, heads, heads, heads, vp, vp, i64, vp]),
+            ("rvq_cross_attention_backward_bytes", i64, [shape]),
+            ("rvq_cross_attention_backward", ctypes.c_int,
              [shape, heads, heads, heads, heads, heads, vp, heads, heads, heads, vp, i64, vp]),
             ("rvq_cache_append", ctypes.c_int, [cache, heads, heads, i64, vp, vp, vp, vp, vp, vp]),
             ("rvq_cache_attention_bytes", i64, [cache, i32]),
@@ -213,10 +222,10 @@ def rvq_window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q
     return out, lse
 
 
-def _backward_bytes(shape: bytes) -> int:
-    size = _lib().rvq_window_attention_backward_bytes(shape)
+def _size(name: str, *args) -> int:
+    size = getattr(_lib(), name)(*args)
     if size < 0:
-        raise RVQError("rvq_window_attention_backward_bytes", size, rvq_status_string(size))
+        raise RVQError(name, size, rvq_status_string(size))
     return size
 
 
@@ -224,7 +233,7 @@ def rvq_window_attention_backward_bytes(q: torch.Tensor, k: torch.Tensor, v: tor
                                         cu_k: Optional[torch.Tensor] = None, window: Optional[int] = None,
                                         sinks: int = 0) -> int:
     """Workspace of ``rvq_window_attention_backward`` for these arguments."""
-    return _backward_bytes(_attention_args(q, k, v, cu_q, cu_k, window, sinks, None)[0])
+    return _size("rvq_window_attention_backward_bytes", _attention_args(q, k, v, cu_q, cu_k, window, sinks, None)[0])
 
 
 def rvq_window_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -235,7 +244,14 @@ def rvq_window_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.
     """Gradients ``(dq, dk, dv)`` of ``rvq_window_attention``; ``out`` and ``lse`` are its results, the other
     arguments as it had them. ``grads`` may pass the three outputs preallocated (for example slices of one tensor),
     ``workspace`` a uint8 tensor of ``rvq_window_attention_backward_bytes``."""
-    shape, q_heads, k_heads, v_heads, (tq, hq, dim) = _attention_args(q, k, v, cu_q, cu_k, window, sinks, scale)
+    shape, q_heads, k_heads, v_heads, _ = _attention_args(q, k, v, cu_q, cu_k, window, sinks, scale)
+    return _backward("rvq_window_attention_backward", shape, dout, (q, k, v), (q_heads, k_heads, v_heads), out, lse, grads,
+                     workspace)
+
+
+def _backward(name, shape, dout, inputs, input_heads, out, lse, grads, workspace):
+    (q, k, v), (q_heads, k_heads, v_heads) = inputs, input_heads
+    tq, hq, dim = q.shape
     dtype, dev = q.dtype, q.device
     dout_heads = _require_heads(dout, "dout", dtype, dev, hq, dim, tq)
     out_heads = _require_heads(out, "out", dtype, dev, hq, dim, tq)
@@ -250,13 +266,80 @@ def rvq_window_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.
     dk_heads = _require_heads(dk, "dk", dtype, dev, hk, dim, tk)
     dv_heads = _require_heads(dv, "dv", dtype, dev, hk, dim, tk)
     if workspace is None:
-        workspace = q.new_empty(_backward_bytes(shape), dtype=torch.uint8)
+        workspace = q.new_empty(_size(name + "_bytes", shape), dtype=torch.uint8)
     _require(workspace, "workspace", torch.uint8, 1, dev)
-    st = _lib().rvq_window_attention_backward(shape, dout_heads, q_heads, k_heads, v_heads, out_heads, lse.data_ptr(),
-                                              dq_heads, dk_heads, dv_heads, workspace.data_ptr(), workspace.numel(),
-                                              _stream(q))
-    _check("rvq_window_attention_backward", st)
+    st = getattr(_lib(), name)(shape, dout_heads, q_heads, k_heads, v_heads, out_heads, lse.data_ptr(), dq_heads, dk_heads,
+                               dv_heads, workspace.data_ptr(), workspace.numel(), _stream(q))
+    _check(name, st)
     return dq, dk, dv
+
+
+def _cross_args(q, k, v, cu_q, cu_k, scale):
+    """The checked call: (shape, q, k, v) as C structures, and q's sizes."""
+    dtype, dev = _float_type(q, "q"), q.device
+    q_heads = _require_heads(q, "q", dtype, dev)
+    tq, hq, dim = q.shape
+    k_heads = _require_heads(k, "k", dtype, dev, dim=dim)
+    tk, hk, _ = k.shape
+    v_heads = _require_heads(v, "v", dtype, dev, hk, dim, tk)
+    if hk == 0 or hq % hk != 0:
+        raise ValueError(f"q's heads ({hq}) must be a multiple of k's ({hk})")
+    n = _offsets(cu_k, "cu_k", dev)
+    if cu_q is not None:
+        _offsets(cu_q, "cu_q", dev, n)
+    elif tq != n:
+        raise ValueError("without cu_q, q must have one row per clip")
+    shape = _pack_attention(DTYPES[dtype], n, hq, hk, dim, 0, -1, tq, tk, 0 if cu_q is None else cu_q.data_ptr(),
+                            cu_k.data_ptr(), 1.0 / math.sqrt(dim) if scale is None else scale)
+    return shape, q_heads, k_heads, v_heads, (tq, hq, dim)
+
+
+def rvq_cross_attention_bytes(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: Optional[torch.Tensor],
+                              cu_k: torch.Tensor) -> int:
+    """Workspace of ``rvq_cross_attention`` for these arguments."""
+    return _size("rvq_cross_attention_bytes", _cross_args(q, k, v, cu_q, cu_k, None)[0])
+
+
+def rvq_cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: Optional[torch.Tensor],
+                        cu_k: torch.Tensor, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None):
+    """Attention of packed clips' queries to all of their clips' keys.
+
+    ``q`` [Tq, Hq, D], ``k`` and ``v`` [Tk, Hk, D]; ``cu_q`` / ``cu_k`` int32 [clips + 1] are the clips' first rows
+    (``cu_q`` None: one query a clip). Returns ``(out [Tq, Hq, D], lse [Hq, Tq] float32)``, 0 and -inf for a clip
+    without keys. ``out`` and ``workspace`` (uint8, ``rvq_cross_attention_bytes``) may be preallocated. Rows outside
+    every clip are not written.
+    """
+    shape, q_heads, k_heads, v_heads, size = _cross_args(q, k, v, cu_q, cu_k, scale)
+    if out is None:
+        out = q.new_empty(size)
+    out_heads = _require_heads(out, "out", q.dtype, q.device, size[1], size[2], size[0])
+    lse = q.new_empty((size[1], size[0]), dtype=torch.float32)
+    if workspace is None:
+        workspace = q.new_empty(_size("rvq_cross_attention_bytes", shape), dtype=torch.uint8)
+    _require(workspace, "workspace", torch.uint8, 1, q.device)
+    st = _lib().rvq_cross_attention(shape, q_heads, k_heads, v_heads, out_heads, lse.data_ptr(), workspace.data_ptr(),
+                                    workspace.numel(), _stream(q))
+    _check("rvq_cross_attention", st)
+    return out, lse
+
+
+def rvq_cross_attention_backward_bytes(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
+                                       cu_k: torch.Tensor) -> int:
+    """Workspace of ``rvq_cross_attention_backward`` for these arguments."""
+    return _size("rvq_cross_attention_backward_bytes", _cross_args(q, k, v, cu_q, cu_k, None)[0])
+
+
+def rvq_cross_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                                 out: torch.Tensor, lse: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor,
+                                 scale: Optional[float] = None, grads=None, workspace: Optional[torch.Tensor] = None):
+    """Gradients ``(dq, dk, dv)`` of ``rvq_cross_attention``, as ``rvq_window_attention_backward``; ``cu_q`` must be
+    given (``torch.arange(clips + 1)`` for one query a clip)."""
+    if cu_q is None:
+        raise ValueError("the gradient needs cu_q")
+    shape, q_heads, k_heads, v_heads, _ = _cross_args(q, k, v, cu_q, cu_k, scale)
+    return _backward("rvq_cross_attention_backward", shape, dout, (q, k, v), (q_heads, k_heads, v_heads), out, lse, grads,
+                     workspace)
 
 
 def _require_pools(k_pool: torch.Tensor, v_pool: torch.Tensor, dims) -> None:
@@ -354,18 +437,11 @@ def rvq_cache_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Ten
     return out
 
 
-def _chunk_bytes(shape: bytes, q_heads: int, tokens: int) -> int:
-    size = _lib().rvq_cache_chunk_attention_bytes(shape, q_heads, tokens)
-    if size < 0:
-        raise RVQError("rvq_cache_chunk_attention_bytes", size, rvq_status_string(size))
-    return size
-
-
 def rvq_cache_chunk_attention_bytes(k_pool: torch.Tensor, table: torch.Tensor, q_heads: int, tokens: int) -> int:
     """Workspace of ``rvq_cache_chunk_attention`` for these pools, this table and ``tokens`` rows of ``q_heads`` heads."""
     _require_pools(k_pool, k_pool, (4,))
     _require(table, "table", torch.int32, 2, k_pool.device)
-    return _chunk_bytes(_cache_shape(k_pool, *table.shape), q_heads, tokens)
+    return _size("rvq_cache_chunk_attention_bytes", _cache_shape(k_pool, *table.shape), q_heads, tokens)
 
 
 def rvq_cache_chunk_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, table: torch.Tensor,
@@ -400,7 +476,7 @@ def rvq_cache_chunk_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: tor
     lse = q.new_empty((hq, n), dtype=torch.float32)
     shape = _cache_shape(k_pool, clips, cols)
     if workspace is None:
-        workspace = q.new_empty(_chunk_bytes(shape, hq, n), dtype=torch.uint8)
+        workspace = q.new_empty(_size("rvq_cache_chunk_attention_bytes", shape, hq, n), dtype=torch.uint8)
     _require(workspace, "workspace", torch.uint8, 1, dev)
     st = _lib().rvq_cache_chunk_attention(shape, hq, n, _ptr(cu), q_heads, k_pool.data_ptr(), v_pool.data_ptr(),
                                           table.data_ptr(), lens.data_ptr(), _window(window), sinks,

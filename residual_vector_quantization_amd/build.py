@@ -22,7 +22,7 @@ PROBE_SOURCES = ["probes.hip"]
 SOURCES = ["rvq_api.hip", "encode.hip", "encode_bf16.hip", "encode_f16.hip", "decode.hip", "linear.hip", "projected.hip",
            "cosine.hip", "noalloc.hip", "attention_api.hip", "attention.hip",
            "attention_backward.hip", "cache_attention.hip", "cache_pages.hip", "rotary.hip",
-           "chunk_attention.hip"]
+           "chunk_attention.hip", "cross_attention.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

@@ -82,6 +82,42 @@ rvq::AttentionArgs attention_args(const rvq_attention_shape *s)
     return a;
 }
 
+rvq_status check_cross(const rvq_attention_shape *s)
+{
+    if (!s) return RVQ_ERR_INVALID_ARG;
+    rvq_attention_shape read = *s;
+    read.sinks = 0;
+    const rvq_status st = check_attention(&read);
+    return st == RVQ_OK && !s->cu_q && s->n_clips != 0 && s->q_tokens != s->n_clips ? RVQ_ERR_INVALID_ARG : st;
+}
+
+// Every query sees all keys.
+rvq::AttentionArgs cross_args(const rvq_attention_shape *s)
+{
+    rvq::AttentionArgs a = attention_args(s);
+    a.window = INT_MAX;
+    a.sinks = 0;
+    a.all = true;
+    return a;
+}
+
+rvq::RowsArgs cross_rows(const rvq_attention_shape *s)
+{
+    rvq::RowsArgs a = {};
+    a.dtype = s->dtype;
+    a.dim = s->dim;
+    a.n_clips = s->n_clips;
+    a.q_heads = s->q_heads;
+    a.kv_heads = s->kv_heads;
+    a.window = INT_MAX;
+    a.scale = s->scale;
+    a.q_tokens = s->q_tokens;
+    a.k_tokens = s->k_tokens;
+    a.cu_q = s->cu_q;
+    a.cu_k = s->cu_k;
+    return a;
+}
+
 rvq_status check_cache(const rvq_cache_shape *s)
 {
     if (!s || s->n_clips < 0 || s->kv_heads <= 0 || s->dim <= 0 || s->page_size <= 0 || s->n_pages < 0 ||
@@ -155,6 +191,40 @@ bool scratch(const void *p, int64_t given, int64_t wanted)
     return wanted == 0 || (p && aligned(p, 16) && given >= wanted);
 }
 
+rvq_status attention_backward(const rvq_attention_shape *shape, bool all, int64_t wanted, const rvq_heads *dout,
+                              const rvq_heads *q, const rvq_heads *k, const rvq_heads *v, const rvq_heads *out,
+                              const float *lse, const rvq_heads *dq, const rvq_heads *dk, const rvq_heads *dv,
+                              void *workspace, int64_t workspace_bytes, void *stream)
+{
+    if (wanted < 0) return static_cast<rvq_status>(wanted);
+    if (shape->n_clips == 0 || (shape->q_tokens == 0 && shape->k_tokens == 0)) return RVQ_OK;
+    if (!ints(shape->cu_q) || !ints(shape->cu_k) || !scratch(workspace, workspace_bytes, wanted))
+        return RVQ_ERR_INVALID_ARG;
+    rvq::AttentionArgs a = all ? cross_args(shape) : attention_args(shape);
+    if (a.q_tokens > 0) {
+        if (!good_heads(q, a.dtype) || !good_heads(dout, a.dtype) || !good_heads(out, a.dtype) || !lse ||
+            !aligned(lse, 4) || !good_output(dq, a.dtype, a.q_heads, a.dim, a.q_tokens))
+            return RVQ_ERR_INVALID_ARG;
+        a.q = heads(q);
+        a.dout = heads(dout);
+        a.out = heads(out);
+        a.dq = heads(dq);
+        a.lse = const_cast<float *>(lse);   // read only in the backward pass
+    }
+    if (a.k_tokens > 0) {
+        if (!good_heads(k, a.dtype) || !good_heads(v, a.dtype) ||
+            !good_output(dk, a.dtype, a.kv_heads, a.dim, a.k_tokens) ||
+            !good_output(dv, a.dtype, a.kv_heads, a.dim, a.k_tokens))
+            return RVQ_ERR_INVALID_ARG;
+        a.k = heads(k);
+        a.v = heads(v);
+        a.dk = heads(dk);
+        a.dv = heads(dv);
+    }
+    a.workspace = workspace;
+    return from_hip(rvq::launch_window_attention_backward(a, static_cast<hipStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -193,34 +263,55 @@ RVQ_API rvq_status rvq_window_attention_backward(const rvq_attention_shape *shap
                                                  const rvq_heads *dq, const rvq_heads *dk, const rvq_heads *dv,
                                                  void *workspace, int64_t workspace_bytes, void *stream)
 {
-    const int64_t wanted = rvq_window_attention_backward_bytes(shape);
+    return attention_backward(shape, false, rvq_window_attention_backward_bytes(shape), dout, q, k, v, out, lse, dq, dk, dv, workspace,
+                              workspace_bytes, stream);
+}
+
+RVQ_API int64_t rvq_cross_attention_bytes(const rvq_attention_shape *shape)
+{
+    const rvq_status st = check_cross(shape);
+    return st != RVQ_OK ? st : rvq::cross_attention_bytes(cross_rows(shape));
+}
+
+RVQ_API rvq_status rvq_cross_attention(const rvq_attention_shape *shape, const rvq_heads *q, const rvq_heads *k,
+                                       const rvq_heads *v, const rvq_heads *out, float *lse, void *workspace,
+                                       int64_t workspace_bytes, void *stream)
+{
+    const int64_t wanted = rvq_cross_attention_bytes(shape);
     if (wanted < 0) return static_cast<rvq_status>(wanted);
-    if (shape->n_clips == 0 || (shape->q_tokens == 0 && shape->k_tokens == 0)) return RVQ_OK;
-    if (!ints(shape->cu_q) || !ints(shape->cu_k) || !scratch(workspace, workspace_bytes, wanted))
+    if (shape->n_clips == 0 || shape->q_tokens == 0) return RVQ_OK;
+    if ((shape->cu_q && !aligned(shape->cu_q, 4)) || !ints(shape->cu_k) || !good_heads(q, shape->dtype) ||
+        !good_output(out, shape->dtype, shape->q_heads, shape->dim, shape->q_tokens) || (lse && !aligned(lse, 4)) ||
+        !scratch(workspace, workspace_bytes, wanted))
         return RVQ_ERR_INVALID_ARG;
-    rvq::AttentionArgs a = attention_args(shape);
-    if (a.q_tokens > 0) {
-        if (!good_heads(q, a.dtype) || !good_heads(dout, a.dtype) || !good_heads(out, a.dtype) || !lse ||
-            !aligned(lse, 4) || !good_output(dq, a.dtype, a.q_heads, a.dim, a.q_tokens))
-            return RVQ_ERR_INVALID_ARG;
-        a.q = heads(q);
-        a.dout = heads(dout);
-        a.out = heads(out);
-        a.dq = heads(dq);
-        a.lse = const_cast<float *>(lse);   // read only in the backward pass
-    }
+    rvq::RowsArgs a = cross_rows(shape);
+    a.k = a.v = heads(q);      // not read without keys
     if (a.k_tokens > 0) {
-        if (!good_heads(k, a.dtype) || !good_heads(v, a.dtype) ||
-            !good_output(dk, a.dtype, a.kv_heads, a.dim, a.k_tokens) ||
-            !good_output(dv, a.dtype, a.kv_heads, a.dim, a.k_tokens))
-            return RVQ_ERR_INVALID_ARG;
+        if (!good_heads(k, shape->dtype) || !good_heads(v, shape->dtype)) return RVQ_ERR_INVALID_ARG;
         a.k = heads(k);
         a.v = heads(v);
-        a.dk = heads(dk);
-        a.dv = heads(dv);
     }
+    a.q = heads(q);
+    a.out = heads(out);
+    a.lse = lse;
     a.workspace = workspace;
-    return from_hip(rvq::launch_window_attention_backward(a, static_cast<hipStream_t>(stream)));
+    return from_hip(rvq::launch_cross_attention(a, static_cast<hipStream_t>(stream)));
+}
+
+RVQ_API int64_t rvq_cross_attention_backward_bytes(const rvq_attention_shape *shape)
+{
+    const rvq_status st = check_cross(shape);
+    return st != RVQ_OK ? st : rvq::window_attention_backward_bytes(cross_args(shape));
+}
+
+RVQ_API rvq_status rvq_cross_attention_backward(const rvq_attention_shape *shape, const rvq_heads *dout,
+                                                const rvq_heads *q, const rvq_heads *k, const rvq_heads *v,
+                                                const rvq_heads *out, const float *lse,
+                                                const rvq_heads *dq, const rvq_heads *dk, const rvq_heads *dv,
+                                                void *workspace, int64_t workspace_bytes, void *stream)
+{
+    return attention_backward(shape, true, rvq_cross_attention_backward_bytes(shape), dout, q, k, v, out, lse, dq, dk, dv, workspace,
+                              workspace_bytes, stream);
 }
 
 RVQ_API int64_t rvq_cache_attention_bytes(const rvq_cache_shape *shape, int32_t q_heads)

@@ -1,4 +1,4 @@
-// Gradient of the windowed attention with sinks.
+// Gradient of the windowed attention with sinks, and of cross attention, where every query sees all keys.
 //
 //   x_ij = scale q_i . k_j,  w_ij = exp(x_ij - lse_i),  delta_i = dout_i . out_i
 //   dw_ij = dout_i . v_j,  dx_ij = w_ij (dw_ij - delta_i)
@@ -224,11 +224,11 @@ void dq_tiles(AttentionArgs a, Work work, float factor)
     const int i0 = (slot - (a.cu_q[clip] / kRows + clip)) * kRows;
     if (i0 < 0 || i0 >= nq) return;
 
-    const int back = nk - nq;
     const int row = i0 + 32 * wave + c;
-    const int p = row + back;
-    const KeyRange range = keys_seen(i0 + back, min(i0 + kRows, nq) - 1 + back, a.window, a.sinks);
-    const int w_first = i0 + 32 * wave + back, w_last = min(i0 + 32 * wave + 31, nq - 1) + back;
+    auto position = [&](int i) { return a.all ? nk - 1 : i + nk - nq; };
+    const int p = position(row);
+    const KeyRange range = keys_seen(position(i0), position(min(i0 + kRows, nq) - 1), a.window, a.sinks);
+    const int w_first = position(i0 + 32 * wave), w_last = position(min(i0 + 32 * wave + 31, nq - 1));
     const int p_low = below_window(p, a.window), w_low = below_window(w_first, a.window);
     const int w_high = below_window(w_last, a.window);
     const int64_t at = q0 + min(row, nq - 1);
@@ -344,7 +344,7 @@ void dq_tiles(AttentionArgs a, Work work, float factor)
             if (t + 1 < range.tiles) tile(t + 1, Constant<1>{}, which);
         }
     };
-    if (sizeof(T) == 2 && min(static_cast<int64_t>(a.window) + a.sinks, static_cast<int64_t>(min(i0 + kRows, nq) + back)) <= kFewKeys) {
+    if (sizeof(T) == 2 && min(static_cast<int64_t>(a.window) + a.sinks, static_cast<int64_t>(position(min(i0 + kRows, nq) - 1) + 1)) <= kFewKeys) {
         pass(Constant<2>{});
         lack += __shfl_xor(lack, 32);
         minus_delta -= lack * unshift;
@@ -394,7 +394,8 @@ __device__ inline void dkv_group(const AttentionArgs &a, const Work &work, float
     const int64_t first = (slot - (cu[clip] / kPer + clip)) * static_cast<int64_t>(kPer);
     if (first < 0 || first >= (kFar ? nq : nk) || nk == 0) return;
 
-    const int back = nk - nq;
+    // a.all: queries at positions from 0 on, which all see all keys
+    const int back = a.all ? 0 : nk - nq;
     const int j_tile = kFar ? 0 : static_cast<int>(first);       // the workgroup's first key
     const int key = j_tile + (kFar ? 32 * (wave >> 1) : 32 * wave) + c;
     // positions that see the workgroup's keys: below near_end through the window, all later ones see the sinks
@@ -406,16 +407,19 @@ __device__ inline void dkv_group(const AttentionArgs &a, const Work &work, float
         if (key < min(a.sinks, nk)) hi = nk;
     } else {
         const bool all = !work.split && j_tile < a.sinks;
-        i_first = max(0, j_tile - back);
-        i_end = (all ? nk : near_end) - back;
+        i_first = a.all ? 0 : max(0, j_tile - back);
+        i_end = a.all ? nq : (all ? nk : near_end) - back;
         if (key < nk) hi = static_cast<int>(min(static_cast<int64_t>(all && key < a.sinks ? INT_MAX : static_cast<int64_t>(key) + a.window), static_cast<int64_t>(nk)));
         // with the sinks split off, their queries up to near_end still belong here
         if (work.split && key < min(a.sinks, nk)) hi = near_end;
+        if (a.all && key < nk) hi = nq;
     }
     const int i_start = i_first / kTileRows * kTileRows;
     const int per_head = i_end > i_first ? (i_end - i_start + kTileRows - 1) / kTileRows : 0;
     const int tiles = per_head * heads;
-    const int key_first = __builtin_amdgcn_readfirstlane(key - c), key_last = key_first + 31;
+    // positions from which this lane's key, the wavefront's first and its last are seen
+    const int low = a.all ? 0 : key;
+    const int key_first = __builtin_amdgcn_readfirstlane(a.all ? 0 : key - c), key_last = a.all ? 0 : key_first + 31;
     // below this position all of the wavefront's keys are seen, from the other on none
     int hi_all = hi, hi_any = hi;
 #pragma unroll
@@ -545,7 +549,7 @@ __device__ inline void dkv_group(const AttentionArgs &a, const Work &work, float
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const int p = p0 + 8 * (r >> 2) + 4 * half + (r & 3);
-                    bool sees = p >= key && p < hi;
+                    bool sees = p >= low && p < hi;
                     if (kFar) sees = sees && p - back >= i_first && p - back < i_end;
                     x[r] = sees ? x[r] : 0.0f;
                     y[r] = sees ? y[r] : 0.0f;

@@ -26,6 +26,7 @@ struct AttentionArgs {
     float *lse;                   // nullable in the forward pass
     Heads dout, dq, dk, dv;       // backward only
     void *workspace;
+    bool all;                     // backward only: every query sees all of its clip's keys (window unbounded, no sinks)
 };
 
 struct CacheAttentionArgs {
@@ -80,6 +81,9 @@ hipError_t launch_window_attention_backward(const AttentionArgs &a, hipStream_t 
 
 int64_t chunk_attention_bytes(const RowsArgs &a);                    // of the shape alone; more with cu_q than without
 hipError_t launch_chunk_attention(const RowsArgs &a, hipStream_t stream);
+
+int64_t cross_attention_bytes(const RowsArgs &a);
+hipError_t launch_cross_attention(const RowsArgs &a, hipStream_t stream);
 
 hipError_t launch_rotary(const RotaryArgs &a, hipStream_t stream);
 hipError_t launch_rotary_append(const RotaryArgs &a, hipStream_t stream);
