@@ -25,7 +25,8 @@ int64_t cross_attention_bytes(const RowsArgs &a)
 hipError_t launch_cross_attention(const RowsArgs &a, hipStream_t stream)
 {
     int64_t floats;
-    const rows::Plan p = rows::plan(a, some_keys(a), floats);
+    rows::Plan p = rows::plan(a, some_keys(a), floats);
+    p.by_chiplet = true;
     return rows::launch<rows::Packed>(a, p, stream);
 }
 

@@ -50,6 +50,8 @@
 namespace rvq {
 namespace rows {
 
+#define RVQ_INLINE __device__ inline __attribute__((always_inline))
+
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kTileQueries = 32 * kWaves;   // rows of tile_rows
@@ -59,12 +61,14 @@ constexpr int kMaxSplits = 256;
 
 struct Plan {
     int group, chunks;          // query heads a key head; blocks of them that rows are made of
-    int few_limit;              // few_rows takes the clips with at most so many queries, tile_rows the others
+    int few_limit;              // queries that few_rows takes at a time
+    bool any_few, all_few;      // whether few_rows takes the clips with at most so many, and whether all others too
     int tile_queries;           // queries of a workgroup of tile_rows
     int few_splits, tile_splits;
-    bool any_few;               // whether few_rows has workgroups
     int tile_slots;             // blocks of queries of tile_rows, all clips
-    int mark;                   // how they are found: see block_of
+    int mark;                   // how they are found, see below
+    bool join_clips;            // join_rows goes by clips and their first few_limit queries, not by rows
+    bool by_chiplet;            // how few_rows' workgroups are numbered, see there
     float factor;               // scale in powers of two
     Divisor page;
     float *few, *tile;          // partial results
@@ -78,7 +82,7 @@ __device__ inline int heads_first(const Plan &p, int chunk) { return p.group * c
 
 // The last b in [0, n) with cu[b] / per + b <= slot (0 if there is none), searched by a whole wavefront, 64 entries at a
 // time: one read for up to 64 clips, two for 4096.
-__device__ inline int clip_of_slot_wide(const int32_t *cu, int n, int slot, int per)
+RVQ_INLINE int clip_of_slot_wide(const int32_t *cu, int n, int slot, int per)
 {
     const int lane = threadIdx.x & 63;
     int lo = 0, size = n;
@@ -94,7 +98,7 @@ __device__ inline int clip_of_slot_wide(const int32_t *cu, int n, int slot, int 
 }
 
 // The last b in [0, n) with cu[b] <= row, likewise.
-__device__ inline int clip_of_row_wide(const int32_t *cu, int n, int row)
+RVQ_INLINE int clip_of_row_wide(const int32_t *cu, int n, int row)
 {
     const int lane = threadIdx.x & 63;
     int lo = 0, size = n;
@@ -132,7 +136,7 @@ struct Paged {
     Divisor page;
     int table_ld, n_pages, kv_heads, kv;
 
-    __device__ static ClipRows clip(const RowsArgs &a, int b)
+    RVQ_INLINE static ClipRows clip(const RowsArgs &a, int b)
     {
         ClipRows r;
         if (a.cu_q) clip_range(a.cu_q, b, a.q_tokens, r.q0, r.nq);
@@ -141,13 +145,13 @@ struct Paged {
         r.beyond = r.nk > static_cast<int64_t>(a.table_ld) * a.page_size;
         return r;
     }
-    __device__ Paged(const RowsArgs &a, const Plan &p, int b, int kv_head)
+    RVQ_INLINE Paged(const RowsArgs &a, const Plan &p, int b, int kv_head)
         : keys(static_cast<const T *>(a.k_pool)), values(static_cast<const T *>(a.v_pool)),
           row(a.table + static_cast<int64_t>(b) * a.table_ld), page(p.page), table_ld(a.table_ld), n_pages(a.n_pages),
           kv_heads(a.kv_heads), kv(kv_head) {}
-    __device__ uint32_t find(int position) const { return cache_row(row, position, page, table_ld, n_pages, kv_heads, kv); }
-    __device__ const T *key(uint32_t at) const { return keys + static_cast<uint64_t>(at) * kD; }
-    __device__ const T *value(uint32_t at) const { return values + static_cast<uint64_t>(at) * kD; }
+    RVQ_INLINE uint32_t find(int position) const { return cache_row(row, position, page, table_ld, n_pages, kv_heads, kv); }
+    RVQ_INLINE const T *key(uint32_t at) const { return keys + static_cast<uint64_t>(at) * kD; }
+    RVQ_INLINE const T *value(uint32_t at) const { return values + static_cast<uint64_t>(at) * kD; }
 };
 
 // Packed rows. Every query sees all of its clip's keys.
@@ -157,7 +161,7 @@ struct Packed {
     const T *keys, *values;
     int64_t key_stride, value_stride;
 
-    __device__ static ClipRows clip(const RowsArgs &a, int b)
+    RVQ_INLINE static ClipRows clip(const RowsArgs &a, int b)
     {
         ClipRows r;
         int k0;
@@ -167,23 +171,23 @@ struct Packed {
         r.beyond = false;
         return r;
     }
-    __device__ Packed(const RowsArgs &a, const Plan &, int b, int kv_head) : key_stride(a.k.token), value_stride(a.v.token)
+    RVQ_INLINE Packed(const RowsArgs &a, const Plan &, int b, int kv_head) : key_stride(a.k.token), value_stride(a.v.token)
     {
         int k0, nk;
         clip_range(a.cu_k, b, a.k_tokens, k0, nk);
         keys = static_cast<const T *>(a.k.data) + k0 * key_stride + kv_head * a.k.head;
         values = static_cast<const T *>(a.v.data) + k0 * value_stride + kv_head * a.v.head;
     }
-    __device__ uint32_t find(int position) const { return static_cast<uint32_t>(position); }
-    __device__ const T *key(uint32_t at) const { return keys + static_cast<int64_t>(at) * key_stride; }
-    __device__ const T *value(uint32_t at) const { return values + static_cast<int64_t>(at) * value_stride; }
+    RVQ_INLINE uint32_t find(int position) const { return static_cast<uint32_t>(position); }
+    RVQ_INLINE const T *key(uint32_t at) const { return keys + static_cast<int64_t>(at) * key_stride; }
+    RVQ_INLINE const T *value(uint32_t at) const { return values + static_cast<int64_t>(at) * value_stride; }
 };
 
 template <typename Keys>
-__device__ inline int position_of(const ClipRows &r, int i) { return Keys::kAll ? r.nk - 1 : r.nk - r.nq + i; }
+RVQ_INLINE int position_of(const ClipRows &r, int i) { return Keys::kAll ? r.nk - 1 : r.nk - r.nq + i; }
 
 // The frames that some query between positions p_first and p_last sees: sinks, then the window.
-__device__ inline Seen seen_between(int p_first, int p_last, int window, int sinks)
+RVQ_INLINE Seen seen_between(int p_first, int p_last, int window, int sinks)
 {
     Seen s = {0, 0, 0};
     if (p_last < 0) return s;
@@ -236,7 +240,7 @@ __device__ inline float groups_sum(float x)
 template <int kD> constexpr int kFewBytes = kWaves * 16 * (kD + 4 + 2) * 4;
 
 template <typename T, int kD, typename Keys, int kSets>
-__device__ inline void few_rows(const RowsArgs &a, const Plan &p, int block, char *s_mem)
+RVQ_INLINE void few_rows(const RowsArgs &a, const Plan &p, int block, char *s_mem)
 {
     constexpr int kSteps = kD / 32;      // products along the head dim
     constexpr int kN = kD / 16;          // dims a lane holds of a value row
@@ -246,222 +250,239 @@ __device__ inline void few_rows(const RowsArgs &a, const Plan &p, int block, cha
     float (*s_sum)[16] = s_max + kWaves;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
-    // heads change fastest, then splits, then clips
+    // Heads change fastest, then splits, then clips. Workgroups go to the 8 chiplets in turn; where a key's heads lie
+    // side by side, all heads of a clip's split go to one of them, so that its cache sees whole keys, not every
+    // eighth head's part of them, which would use few of its channels.
     const int columns = a.kv_heads * p.chunks;
-    const int rest = block / columns, column = block - rest * columns;
+    const int rest = p.by_chiplet ? block / (8 * columns) * 8 + block % 8 : block / columns;
+    const int column = p.by_chiplet ? block / 8 % columns : block - rest * columns;
     const int kv = column / p.chunks, chunk = column - kv * p.chunks;
     const int clip = rest / p.few_splits, split = rest - clip * p.few_splits;
+    if (clip >= a.n_clips) return;
     const ClipRows r = Keys::clip(a, clip);
-    if (r.nq == 0 || r.nq > p.few_limit) return;
+    if (r.nq == 0 || (!p.all_few && r.nq > p.few_limit)) return;
     const int heads = heads_first(p, chunk + 1) - heads_first(p, chunk), head0 = kv * p.group + heads_first(p, chunk);
     const Keys keys(a, p, clip, kv);
 
-    // this lane's row of every set
-    int query[kSets], head[kSets];
-    vec8<T> q[kSets][kSteps];
-#pragma unroll
-    for (int s = 0; s < kSets; ++s) {
-        const int at = min(16 * s + c, r.nq * heads - 1);
-        query[s] = at / heads;
-        head[s] = head0 + at - query[s] * heads;
-        const T *from = static_cast<const T *>(a.q.data) + static_cast<int64_t>(r.q0 + query[s]) * a.q.token + head[s] * a.q.head;
-#pragma unroll
-        for (int t = 0; t < kSteps; ++t) q[s][t] = load8(from + 32 * t + 8 * g);
-    }
-    const int sets = (r.nq * heads + 15) / 16;       // the others hold no row
-
-    f32x4 o[kSets][kN];
-    float m[kSets], l[kSets];
-    // over the keys that the queries first .. last see; rows of others come out without sense
-    auto pass = [&](int first, int last) {
-        const int p_first = position_of<Keys>(r, first), p_last = position_of<Keys>(r, last);
-        const Seen seen = seen_between(r.beyond ? -1 : p_first, r.beyond ? -1 : p_last, a.window, a.sinks);
-        // positions up to `through` are seen by all of the queries if they are above `from` (or sinks)
-        const int through = p_first, from = below_window(p_last, a.window);
+    for (int base = 0; base < r.nq; base += p.few_limit) {
+        const int count = min(p.few_limit, r.nq - base);     // queries of this turn
+        // this lane's row of every set
+        int query[kSets], head[kSets];
+        vec8<T> q[kSets][kSteps];
 #pragma unroll
         for (int s = 0; s < kSets; ++s) {
-            m[s] = -INFINITY;
-            l[s] = r.beyond ? __builtin_nanf("") : 0.0f;
+            const int at = min(16 * s + c, count * heads - 1);
+            query[s] = base + at / heads;
+            head[s] = head0 + at - (query[s] - base) * heads;
+            const T *from = static_cast<const T *>(a.q.data) + static_cast<int64_t>(r.q0 + query[s]) * a.q.token + head[s] * a.q.head;
 #pragma unroll
-            for (int n = 0; n < kN; ++n) o[s][n] = f32x4{};
+            for (int t = 0; t < kSteps; ++t) q[s][t] = load8(from + 32 * t + 8 * g);
         }
-        const int tiles = (seen.count + kKeys - 1) / kKeys;
-        const int per = (tiles + p.few_splits - 1) / p.few_splits;
-        const int end = min(tiles, (split + 1) * per);
-        // lane n holds the place of the tile's key n % 32
-        auto find = [&](int tile) -> uint32_t {
-            const int nth = tile * kKeys + (lane & 31);
-            if (tile >= end || nth >= seen.count) return kPastEnd;
-            return keys.find(seen_position(seen, nth));
-        };
-        int tile = split * per + wave;
-        uint32_t mine = find(tile);
-        for (; tile < end; tile += kWaves) {
-            const bool there = __all(mine < kPastEnd), lost = __any(mine == kNoPage);
-            vec8<T> k[2][kSteps];
-            Block8<T, kN> v;
-            uint32_t kr[2];
-#pragma unroll
-            for (int b = 0; b < 2; ++b) kr[b] = __shfl(mine, 8 * (c >> 2) + 4 * b + (c & 3));
-            if (there) {
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int t = 0; t < kSteps; ++t) k[b][t] = load8(keys.key(kr[b]) + 32 * t + 8 * g);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v.load(i, keys.value(__shfl(mine, 8 * g + i)) + kN * c);
-            } else {
-                // keys that are not there are zeros: their weights are 0, and nothing is read for them
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int t = 0; t < kSteps; ++t) {
-                        k[b][t] = vec8<T>{};
-                        if (kr[b] < kPastEnd) k[b][t] = load8(keys.key(kr[b]) + 32 * t + 8 * g);
-                    }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t at = __shfl(mine, 8 * g + i);
-                    v.clear(i);
-                    if (at < kPastEnd) v.load(i, keys.value(at) + kN * c);
-                }
-            }
-            const uint32_t next = find(tile + kWaves);
-            // all keys of the tile are there and seen by every row
-            const int j_first = seen_position(seen, tile * kKeys), j_last = seen_position(seen, min(tile * kKeys + kKeys, seen.count) - 1);
-            const bool whole = there && (Keys::kAll || (j_last <= through && (j_first > from || j_last < a.sinks)));
+        const int sets = (count * heads + 15) / 16;       // the others hold no row
+
+        f32x4 o[kSets][kN];
+        float m[kSets], l[kSets];
+        // over the keys that the queries first .. last see; rows of others come out without sense
+        auto pass = [&](int first, int last) __attribute__((always_inline)) {
+            const int p_first = position_of<Keys>(r, first), p_last = position_of<Keys>(r, last);
+            const Seen seen = seen_between(r.beyond ? -1 : p_first, r.beyond ? -1 : p_last, a.window, a.sinks);
+            // positions up to `through` are seen by all of the queries if they are above `from` (or sinks)
+            const int through = p_first, from = below_window(p_last, a.window);
 #pragma unroll
             for (int s = 0; s < kSets; ++s) {
-                if (kSets > 1 && s >= sets) break;
-                if (kSets > 1) __builtin_amdgcn_sched_barrier(0);
-                // scores in powers of two: key 8 g + 4 b + i of the tile, row c
-                f32x4 x[2] = {};
+                m[s] = -INFINITY;
+                l[s] = r.beyond ? __builtin_nanf("") : 0.0f;
 #pragma unroll
-                for (int t = 0; t < kSteps; ++t)
+                for (int n = 0; n < kN; ++n) o[s][n] = f32x4{};
+            }
+            const int tiles = (seen.count + kKeys - 1) / kKeys;
+            const int per = (tiles + p.few_splits - 1) / p.few_splits;
+            const int end = min(tiles, (split + 1) * per);
+            // lane n holds the place of the tile's key n % 32
+            auto find = [&](int tile) -> uint32_t {
+                const int nth = tile * kKeys + (lane & 31);
+                if (tile >= end || nth >= seen.count) return kPastEnd;
+                return keys.find(seen_position(seen, nth));
+            };
+            struct Part {
+                int tile;
+                uint32_t mine;         // of the keys' places, this lane's
+                vec8<T> k[2][kSteps];
+                Block8<T, kN> v;
+            };
+            // sets out for a tile's keys and values; row 0 in the place of keys that are not there, so that nothing branches
+            auto load = [&](Part &d, int tile, uint32_t mine) __attribute__((always_inline)) {
+                d.tile = tile;
+                d.mine = mine;
+                const uint32_t at = mine < kPastEnd ? mine : 0;
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) x[b] = mma16(k[b][t], q[s][t], x[b]);
-                float top = -INFINITY;
-                if (!whole) {
-                    const int position = position_of<Keys>(r, query[s]), low = below_window(position, a.window);
+                for (int b = 0; b < 2; ++b) {
+                    const T *key = keys.key(__shfl(at, 8 * (c >> 2) + 4 * b + (c & 3))) + 8 * g;
+#pragma unroll
+                    for (int t = 0; t < kSteps; ++t) d.k[b][t] = load8(key + 32 * t);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d.v.load(i, keys.value(__shfl(at, 8 * g + i)) + kN * c);
+            };
+            auto use = [&](Part &d) __attribute__((always_inline)) {
+                const bool there = __all(d.mine < kPastEnd), lost = __any(d.mine == kNoPage);
+                if (!there) {
+                    // keys that are not there are zeros: their weights are 0
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+                        if (__shfl(d.mine, 8 * (c >> 2) + 4 * b + (c & 3)) >= kPastEnd)
+#pragma unroll
+                            for (int t = 0; t < kSteps; ++t) d.k[b][t] = vec8<T>{};
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (__shfl(d.mine, 8 * g + i) >= kPastEnd) d.v.clear(i);
+                }
+                // all keys of the tile are there and seen by every row
+                const int j_first = seen_position(seen, d.tile * kKeys), j_last = seen_position(seen, min(d.tile * kKeys + kKeys, seen.count) - 1);
+                const bool whole = there && (Keys::kAll || (j_last <= through && (j_first > from || j_last < a.sinks)));
+#pragma unroll
+                for (int s = 0; s < kSets; ++s) {
+                    if (kSets > 1 && s >= sets) break;
+                    if (kSets > 1) __builtin_amdgcn_sched_barrier(0);
+                    // scores in powers of two: key 8 g + 4 b + i of the tile, row c
+                    f32x4 x[2] = {};
+#pragma unroll
+                    for (int t = 0; t < kSteps; ++t)
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) x[b] = mma16(d.k[b][t], q[s][t], x[b]);
+                    float top = -INFINITY;
+                    if (!whole) {
+                        const int position = position_of<Keys>(r, query[s]), low = below_window(position, a.window);
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int nth = d.tile * kKeys + 8 * g + 4 * b + i, j = seen_position(seen, nth);
+                                const bool sees = nth < seen.count && (Keys::kAll || (j <= position && (j > low || j < a.sinks)));
+                                x[b][i] = sees ? x[b][i] : -INFINITY;
+                            }
+                    }
+                    if (!Keys::kAll && lost) {     // rare; their scores are 0 where they are seen
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (__shfl(d.mine, 8 * g + 4 * b + i) == kNoPage) {
+                                    if (x[b][i] != -INFINITY) l[s] = __builtin_nanf("");
+                                    x[b][i] = -INFINITY;
+                                }
+                    }
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) top = fmaxf(top, x[b][i]);
+                    top *= p.factor;
+                    if (__any(top > m[s] + kSlack)) {
+                        top = groups_max(top);
+                        if (top > m[s] + kSlack) {
+                            const float keep = fast_exp2(m[s] - top);
+                            m[s] = top;
+                            l[s] *= keep;
+#pragma unroll
+                            for (int n = 0; n < kN; ++n) o[s][n] *= keep;
+                        }
+                    }
+                    const float safe = m[s] == -INFINITY ? 0.0f : m[s] - kShift;
+                    vec8<T> w;
 #pragma unroll
                     for (int b = 0; b < 2; ++b)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const int nth = tile * kKeys + 8 * g + 4 * b + i, j = seen_position(seen, nth);
-                            const bool sees = nth < seen.count && (Keys::kAll || (j <= position && (j > low || j < a.sinks)));
-                            x[b][i] = sees ? x[b][i] : -INFINITY;
+                            const float e = fast_exp2(__builtin_fmaf(x[b][i], p.factor, -safe));
+                            l[s] += e;
+                            w[4 * b + i] = static_cast<T>(e);
                         }
+#pragma unroll
+                    for (int n = 0; n < kN; ++n) o[s][n] = mma16(d.v.at(n), w, o[s][n]);
                 }
-                if (!Keys::kAll && lost) {     // rare; their scores are 0 where they are seen
-#pragma unroll
-                    for (int b = 0; b < 2; ++b)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (__shfl(mine, 8 * g + 4 * b + i) == kNoPage) {
-                                if (x[b][i] != -INFINITY) l[s] = __builtin_nanf("");
-                                x[b][i] = -INFINITY;
-                            }
-                }
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) top = fmaxf(top, x[b][i]);
-                top *= p.factor;
-                if (__any(top > m[s] + kSlack)) {
-                    top = groups_max(top);
-                    if (top > m[s] + kSlack) {
-                        const float keep = fast_exp2(m[s] - top);
-                        m[s] = top;
-                        l[s] *= keep;
-#pragma unroll
-                        for (int n = 0; n < kN; ++n) o[s][n] *= keep;
-                    }
-                }
-                const float safe = m[s] == -INFINITY ? 0.0f : m[s] - kShift;
-                vec8<T> w;
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float e = fast_exp2(__builtin_fmaf(x[b][i], p.factor, -safe));
-                        l[s] += e;
-                        w[4 * b + i] = static_cast<T>(e);
-                    }
-#pragma unroll
-                for (int n = 0; n < kN; ++n) o[s][n] = mma16(v.at(n), w, o[s][n]);
+            };
+            Part part;
+            int tile = split * per + wave;
+            uint32_t next = find(tile);
+            for (; tile < end; tile += kWaves) {
+                load(part, tile, next);
+                next = find(tile + kWaves);
+                use(part);
             }
-            mine = next;
-        }
-    };
-    // joins the wavefronts and writes the rows of queries first .. last
-    auto finish = [&](int first, int last) {
+        };
+        // joins the wavefronts and writes the rows of queries first .. last
+        auto finish = [&](int first, int last) __attribute__((always_inline)) {
 #pragma unroll
-        for (int s = 0; s < kSets; ++s) {
-            if (s >= sets) break;
-            if (s > 0) __syncthreads();
-            const float sum = groups_sum(l[s]);
-            if (g == 0) {
-                s_max[wave][c] = m[s];
-                s_sum[wave][c] = sum;
-            }
-#pragma unroll
-            for (int n = 0; n < kN; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s_out[wave][c][kN * (4 * g + i) + n] = o[s][n][i];
-            __syncthreads();
-            const int count = min(16, r.nq * heads - 16 * s);
-            for (int at = threadIdx.x; at < count * kD; at += kThreads) {
-                const int row = at / kD, d = at - row * kD, i = (16 * s + row) / heads, h = head0 + (16 * s + row) - i * heads;
-                if (i < first || i > last) continue;
-                float top = -INFINITY, total = 0.0f, y = 0.0f;
-#pragma unroll
-                for (int w = 0; w < kWaves; ++w) top = fmaxf(top, s_max[w][row]);
-                const float safe = top == -INFINITY ? 0.0f : top;
-#pragma unroll
-                for (int w = 0; w < kWaves; ++w) {
-                    const float f = fast_exp2(s_max[w][row] - safe);
-                    total += s_sum[w][row] * f;
-                    y += s_out[w][row][d] * f;
+            for (int s = 0; s < kSets; ++s) {
+                if (s >= sets) break;
+                if (s > 0) __syncthreads();
+                const float sum = groups_sum(l[s]);
+                if (g == 0) {
+                    s_max[wave][c] = m[s];
+                    s_sum[wave][c] = sum;
                 }
-                if (p.few_splits == 1) {
-                    T *out = static_cast<T *>(a.out.data) + static_cast<int64_t>(r.q0 + i) * a.out.token + h * a.out.head;
-                    out[d] = static_cast<T>(total == 0.0f ? 0.0f : y / total);
-                    if (a.lse && d == 0)
-                        a.lse[static_cast<int64_t>(h) * a.q_tokens + r.q0 + i] =
-                            total == 0.0f ? -INFINITY : (top - kShift + log2f(total)) * kLn2;
-                } else {
-                    const int64_t slot = ((static_cast<int64_t>(clip) * p.few_limit + i) * a.q_heads + h) * p.few_splits + split;
-                    p.few[stats_floats(p.few_rows * p.few_splits) + slot * kD + d] = y;
-                    if (d == 0) {
-                        p.few[2 * slot] = top - kShift;
-                        p.few[2 * slot + 1] = total;
-                    }
-                }
-            }
-        }
-    };
-    // all queries at once, or, after a result that is not finite, one after another
-    bool each = Keys::kAll || r.nq == 1;
-    for (int first = 0, last = r.nq - 1;;) {
-        pass(first, last);
-        if (!each) {
-            each = true;
-            bool odd = false;
-#pragma unroll
-            for (int s = 0; s < kSets; ++s)
 #pragma unroll
                 for (int n = 0; n < kN; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) odd = odd || !(fabsf(o[s][n][i]) <= FLT_MAX);
-            if (__syncthreads_or(odd)) {
-                last = 0;
-                continue;
+                    for (int i = 0; i < 4; ++i) s_out[wave][c][kN * (4 * g + i) + n] = o[s][n][i];
+                __syncthreads();
+                const int rows = min(16, count * heads - 16 * s);
+                for (int at = threadIdx.x; at < rows * kD; at += kThreads) {
+                    const int row = at / kD, d = at - row * kD, nth = (16 * s + row) / heads;
+                    const int i = base + nth, h = head0 + (16 * s + row) - nth * heads;
+                    if (i < first || i > last) continue;
+                    float top = -INFINITY, total = 0.0f, y = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, s_max[w][row]);
+                    const float safe = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+                    for (int w = 0; w < kWaves; ++w) {
+                        const float f = fast_exp2(s_max[w][row] - safe);
+                        total += s_sum[w][row] * f;
+                        y += s_out[w][row][d] * f;
+                    }
+                    if (p.few_splits == 1) {
+                        T *out = static_cast<T *>(a.out.data) + static_cast<int64_t>(r.q0 + i) * a.out.token + h * a.out.head;
+                        out[d] = static_cast<T>(total == 0.0f ? 0.0f : y / total);
+                        if (a.lse && d == 0)
+                            a.lse[static_cast<int64_t>(h) * a.q_tokens + r.q0 + i] =
+                                total == 0.0f ? -INFINITY : (top - kShift + log2f(total)) * kLn2;
+                    } else {
+                        const int64_t at_row = p.all_few ? r.q0 + i : static_cast<int64_t>(clip) * p.few_limit + i;
+                        const int64_t slot = (at_row * a.q_heads + h) * p.few_splits + split;
+                        p.few[stats_floats(p.few_rows * p.few_splits) + slot * kD + d] = y;
+                        if (d == 0) {
+                            p.few[2 * slot] = top - kShift;
+                            p.few[2 * slot + 1] = total;
+                        }
+                    }
+                }
             }
+        };
+        // all queries at once, or, after a result that is not finite, one after another
+        bool each = Keys::kAll || count == 1;
+        for (int first = base, last = base + count - 1;;) {
+            pass(first, last);
+            if (!each) {
+                each = true;
+                bool odd = false;
+#pragma unroll
+                for (int s = 0; s < kSets; ++s)
+#pragma unroll
+                    for (int n = 0; n < kN; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) odd = odd || !(fabsf(o[s][n][i]) <= FLT_MAX);
+                if (__syncthreads_or(odd)) {
+                    last = first;
+                    continue;
+                }
+            }
+            finish(first, last);
+            if (last == base + count - 1) break;
+            first = ++last;
+            __syncthreads();      // what was left in the LDS has been read
         }
-        finish(first, last);
-        if (last == r.nq - 1) break;
-        first = ++last;
-        __syncthreads();      // what was left in the LDS has been read
+        if (base + count < r.nq) __syncthreads();
     }
 }
 
@@ -485,15 +506,15 @@ struct Tiles<T, kD, Packed<T, kD>> {
     typedef typename Memory::Rows Rows;
     static constexpr int kBytes = Memory::kBytes;
     Memory feed;
-    const Packed<T, kD> &keys;
-    const KeyRange &range;
+    const Packed<T, kD> keys;
+    const KeyRange range;
     int last;
 
-    __device__ Tiles(char *s, const Packed<T, kD> &from, const KeyRange &r, int last_position)
+    RVQ_INLINE Tiles(char *s, const Packed<T, kD> &from, const KeyRange &r, int last_position)
         : feed(s, from.key_stride, from.value_stride), keys(from), range(r), last(last_position) {}
-    __device__ void start(int t, int) { feed.start(keys.keys, keys.values, range.start(t), last + 1); }
+    RVQ_INLINE void start(int t, int) { feed.start(keys.keys, keys.values, range.start(t), last + 1); }
     template <int kBuffer>
-    __device__ uint64_t turn(Constant<kBuffer> buffer, int t, int end)
+    RVQ_INLINE uint64_t turn(Constant<kBuffer> buffer, int t, int end)
     {
         feed.turn(buffer, t + 1 < end, keys.keys, keys.values, range.start(t + 1), last + 1);
         return 0;
@@ -505,21 +526,21 @@ struct Tiles<T, kD, Packed<T, kD>> {
 // From pages: lane n holds the place of the next tile's key n, looked up one tile ahead of the copies that need it.
 template <typename T, int kD>
 struct PagedPlaces {
-    const Paged<T, kD> &keys;
-    const KeyRange &range;
+    const Paged<T, kD> keys;
+    const KeyRange range;
     int last;
     uint32_t next;
     uint64_t gone;
 
-    __device__ PagedPlaces(const Paged<T, kD> &from, const KeyRange &r, int last_position)
+    RVQ_INLINE PagedPlaces(const Paged<T, kD> &from, const KeyRange &r, int last_position)
         : keys(from), range(r), last(last_position), next(0), gone(0) {}
     // keys behind the last one that is seen: that one again
-    __device__ void look(int t, int end)
+    RVQ_INLINE void look(int t, int end)
     {
         if (t < end) next = keys.find(min(range.start(t) + static_cast<int>(threadIdx.x & 63), last));
     }
     // row 0 of the pools in the place of keys that are not there
-    __device__ void take()
+    RVQ_INLINE void take()
     {
         gone = __ballot(next == kNoPage);
         if (next == kNoPage) next = 0;
@@ -533,9 +554,9 @@ struct Tiles<T, kD, Paged<T, kD>> {
     PagedPlaces<T, kD> places;
     char *s;
 
-    __device__ Tiles(char *memory, const Paged<T, kD> &from, const KeyRange &r, int last_position)
+    RVQ_INLINE Tiles(char *memory, const Paged<T, kD> &from, const KeyRange &r, int last_position)
         : places(from, r, last_position), s(memory) {}
-    __device__ void load(int buffer)
+    RVQ_INLINE void load(int buffer)
     {
         const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         places.take();
@@ -548,14 +569,14 @@ struct Tiles<T, kD, Paged<T, kD>> {
             copy16_from(reinterpret_cast<const char *>(places.keys.values) + offset, to + Rows::kBytes + (n * kWaves + wave) * 1024);
         }
     }
-    __device__ void start(int t, int end)
+    RVQ_INLINE void start(int t, int end)
     {
         places.look(t, end);
         load(0);
         places.look(t + 1, end);
     }
     template <int kBuffer>
-    __device__ uint64_t turn(Constant<kBuffer>, int t, int end)
+    RVQ_INLINE uint64_t turn(Constant<kBuffer>, int t, int end)
     {
         const uint64_t gone = places.gone;
         wait_copies();
@@ -578,9 +599,9 @@ struct Tiles<float, kD, Paged<float, kD>> {
     typename Rows::Loader one, two;
     char *s;
 
-    __device__ Tiles(char *memory, const Paged<float, kD> &from, const KeyRange &r, int last_position)
+    RVQ_INLINE Tiles(char *memory, const Paged<float, kD> &from, const KeyRange &r, int last_position)
         : places(from, r, last_position), one(0), two(0), s(memory) {}
-    __device__ void load()
+    RVQ_INLINE void load()
     {
         places.take();
 #pragma unroll
@@ -591,14 +612,14 @@ struct Tiles<float, kD, Paged<float, kD>> {
             two.x[n] = load8(places.keys.value(place) + 8 * piece);
         }
     }
-    __device__ void start(int t, int end)
+    RVQ_INLINE void start(int t, int end)
     {
         places.look(t, end);
         load();
         places.look(t + 1, end);
     }
     template <int kBuffer>
-    __device__ uint64_t turn(Constant<kBuffer>, int t, int end)
+    RVQ_INLINE uint64_t turn(Constant<kBuffer>, int t, int end)
     {
         const uint64_t gone = places.gone;
         __syncthreads();
@@ -616,7 +637,7 @@ struct Tiles<float, kD, Paged<float, kD>> {
 };
 
 template <typename T, int kD, typename Keys>
-__device__ inline void tile_rows(const RowsArgs &a, const Plan &p, int block, char *s_mem)
+RVQ_INLINE void tile_rows(const RowsArgs &a, const Plan &p, int block, char *s_mem)
 {
     typedef Tiles<T, kD, Keys> Source;
     typedef typename Source::Rows Rows;
@@ -667,7 +688,7 @@ __device__ inline void tile_rows(const RowsArgs &a, const Plan &p, int block, ch
 
     // One tile of keys. The buffer's number is a constant, so that LDS addresses are; markers and clean (the values
     // of a tile are rewritten) make the later passes.
-    auto tile = [&](int t, auto buffer, auto markers, auto clean) {
+    auto tile = [&](int t, auto buffer, auto markers, auto clean) __attribute__((always_inline)) {
         const uint64_t gone = source.turn(buffer, t, end);
         char *s_k = source.tile_keys(buffer), *s_v = source.tile_values(buffer);
         if (clean.value) {
@@ -766,7 +787,7 @@ __device__ inline void tile_rows(const RowsArgs &a, const Plan &p, int block, ch
                 for (int i = 0; i < 16; ++i) o[n][i] = (o[n][i] >= 1.0f ? 1.0f : 0.0f) + (o[n][i] > floorf(o[n][i]) ? kMinus : 0.0f);
         }
     };
-    auto pass = [&](auto markers, auto clean) {
+    auto pass = [&](auto markers, auto clean) __attribute__((always_inline)) {
         if (begin < end) source.start(begin, end);
 #pragma unroll
         for (int n = 0; n < kD / 32; ++n) o[n] = f32x16{};
@@ -852,53 +873,61 @@ void all_rows(RowsArgs a, Plan p, int tile_groups)
 }
 
 template <typename T, int kD, typename Keys, int kSets>
-__global__ __launch_bounds__(kThreads)
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
 void only_few_rows(RowsArgs a, Plan p)
 {
     __shared__ __attribute__((aligned(16))) char s_mem[kFewBytes<kD>];
     few_rows<T, kD, Keys, kSets>(a, p, blockIdx.x, s_mem);
 }
 
-// One wavefront a query and head: lanes find the largest maximum and the scaled sums over the splits, then add up the
-// accumulators, a lane kD / 64 dims.
+// One wavefront a query and kJoined of its heads, kD / 4 lanes each: they find the largest maximum and the scaled sums
+// over the splits, then add up the accumulators in order, 4 dims a lane.
+template <int kD> constexpr int kJoined = 256 / kD;
+
 template <typename T, int kD, typename Keys>
 __global__ __launch_bounds__(64)
 void join_rows(RowsArgs a, Plan p)
 {
-    const int token = blockIdx.x, head = blockIdx.y, lane = threadIdx.x;
-    const int clip = a.cu_q ? clip_of_row_wide(a.cu_q, a.n_clips, token) : token;
+    constexpr int kLanes = kD / 4;
+    const int lane = threadIdx.x & (kLanes - 1), nth = threadIdx.x / kLanes;
+    int clip = blockIdx.x;
+    if (p.join_clips) clip = blockIdx.x / p.few_limit;
+    else if (a.cu_q) clip = clip_of_row_wide(a.cu_q, a.n_clips, blockIdx.x);
     const ClipRows r = Keys::clip(a, clip);
-    const int i = token - r.q0;
+    const int i = p.join_clips ? blockIdx.x - clip * p.few_limit : blockIdx.x - r.q0, token = r.q0 + i;
     if (i < 0 || i >= r.nq) return;
-    const bool few = r.nq <= p.few_limit;
+    const bool few = p.all_few || r.nq <= p.few_limit;
     const int splits = few ? p.few_splits : p.tile_splits;
     if (splits == 1) return;
+    const int own = blockIdx.y * kJoined<kD> + nth, head = min(own, a.q_heads - 1);
     const float *part = few ? p.few : p.tile;
-    const int64_t row = few ? (static_cast<int64_t>(clip) * p.few_limit + i) * a.q_heads + head : static_cast<int64_t>(token) * a.q_heads + head;
+    const int64_t row = (few && !p.all_few ? static_cast<int64_t>(clip) * p.few_limit + i : token) * a.q_heads + head;
     const float *stats = part + 2 * row * splits;
-    const float *sums = part + stats_floats((few ? p.few_rows : p.tile_rows) * splits) + row * splits * kD;
-    __shared__ float s_factor[kMaxSplits];
+    const float *sums = part + stats_floats((few ? p.few_rows : p.tile_rows) * splits) + row * splits * kD + 4 * lane;
+    __shared__ float s_factor[kJoined<kD>][kMaxSplits];
     float top = -INFINITY;
-    for (int s = lane; s < splits; s += 64) top = fmaxf(top, stats[2 * s]);
+    for (int s = lane; s < splits; s += kLanes) top = fmaxf(top, stats[2 * s]);
 #pragma unroll
-    for (int x = 32; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
+    for (int x = kLanes / 2; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
     const float safe = top == -INFINITY ? 0.0f : top;
     float sum = 0.0f;
-    for (int s = lane; s < splits; s += 64) {
+    for (int s = lane; s < splits; s += kLanes) {
         const float f = fast_exp2(stats[2 * s] - safe);
-        s_factor[s] = f;
+        s_factor[nth][s] = f;
         sum += stats[2 * s + 1] * f;
     }
-    sum = wave_sum(sum);
+#pragma unroll
+    for (int x = kLanes / 2; x > 0; x >>= 1) sum += __shfl_xor(sum, x);
     __syncthreads();
-    float y[kD / 64] = {};
+    f32x4 y = {};
 #pragma unroll 8
-    for (int s = 0; s < splits; ++s)
-#pragma unroll
-        for (int n = 0; n < kD / 64; ++n) y[n] += sums[s * kD + 64 * n + lane] * s_factor[s];
+    for (int s = 0; s < splits; ++s) y += *reinterpret_cast<const f32x4 *>(sums + s * kD) * s_factor[nth][s];
+    if (own >= a.q_heads) return;
     T *out = static_cast<T *>(a.out.data) + static_cast<int64_t>(token) * a.out.token + head * a.out.head;
+    T z[4];
 #pragma unroll
-    for (int n = 0; n < kD / 64; ++n) out[64 * n + lane] = static_cast<T>(sum == 0.0f ? 0.0f : y[n] / sum);
+    for (int n = 0; n < 4; ++n) z[n] = static_cast<T>(sum == 0.0f ? 0.0f : y[n] / sum);
+    store4(out + 4 * lane, z);
     if (a.lse && lane == 0) a.lse[static_cast<int64_t>(head) * a.q_tokens + token] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
@@ -906,7 +935,8 @@ void join_rows(RowsArgs a, Plan p)
 // most that a clip can have.
 inline Plan plan(const RowsArgs &a, int64_t keys, int64_t &floats)
 {
-    constexpr int64_t kWanted = 2048, kWantedTiles = 512;      // workgroups that fill the chip
+    constexpr int64_t kWanted = 4096, kTurns = 3;
+    const int64_t wanted_tiles = a.dtype == RVQ_F32 ? 768 : 512, least_tiles = a.dtype == RVQ_F32 ? 2 : 4;      // workgroups that fill the chip
     Plan p = {};
     p.group = a.q_heads / a.kv_heads;
     p.chunks = (p.group + 31) / 32;
@@ -916,28 +946,30 @@ inline Plan plan(const RowsArgs &a, int64_t keys, int64_t &floats)
     // 16 rows of few_rows where they do for most clips, 32 otherwise
     const int rows = heads <= 16 && average * heads <= 16 ? 16 : 32;
     p.few_limit = rows / heads;
-    const bool none_few = a.n_clips == 1 && a.q_tokens > p.few_limit, all_few = !a.cu_q || a.q_tokens <= p.few_limit;
-    if (none_few) p.few_limit = 0;
+    // one clip alone has either many or few; so few rows in all that tile_rows' workgroups do not pay
+    p.all_few = !a.cu_q || a.q_tokens <= (a.n_clips == 1 ? 1 : 4) * p.few_limit;
+    p.any_few = p.all_few || a.n_clips != 1;
+    if (!p.any_few) p.few_limit = 0;
     p.few_splits = p.tile_splits = 1;
     p.tile_queries = kTileQueries / heads;
-    if (!none_few) {
+    if (p.any_few) {
         const int64_t tiles = (keys + kKeys - 1) / kKeys, base = a.n_clips * columns;
         int64_t n = base > 0 ? kWanted / base : 1;
-        const int64_t most = tiles <= 4 * kWaves ? 1 : tiles / kWaves;
+        const int64_t most = tiles <= 4 * kWaves ? 1 : tiles / (kWaves * kTurns);
         n = n < most ? n : most;
         p.few_splits = static_cast<int>(n < 1 ? 1 : n < kMaxSplits ? n : kMaxSplits);
-        p.any_few = true;
     }
-    if (!all_few) {
+    if (!p.all_few) {
         const int64_t slots = a.q_tokens / p.tile_queries + a.n_clips + 1, marked = a.q_tokens / (p.few_limit + 1) + 1;
         if (p.any_few && marked < slots) p.mark = p.few_limit + 1;
         p.tile_slots = static_cast<int>(p.mark ? marked : slots);
         const int64_t tiles = (keys + kTileRows - 1) / kTileRows;
-        int64_t n = kWantedTiles / ((a.q_tokens / p.tile_queries + 1) * columns);
-        n = n < tiles / 8 ? n : tiles / 8;
+        int64_t n = wanted_tiles / ((a.q_tokens / p.tile_queries + 1) * columns);
+        n = n < tiles / least_tiles ? n : tiles / least_tiles;
         p.tile_splits = static_cast<int>(n < 1 ? 1 : n < kMaxSplits ? n : kMaxSplits);
     }
-    p.few_rows = p.few_splits > 1 ? static_cast<int64_t>(a.n_clips) * p.few_limit * a.q_heads : 0;
+    p.join_clips = !p.all_few && p.tile_splits == 1 && static_cast<int64_t>(a.n_clips) * p.few_limit < a.q_tokens;
+    p.few_rows = p.few_splits > 1 ? (p.all_few ? a.q_tokens : static_cast<int64_t>(a.n_clips) * p.few_limit) * a.q_heads : 0;
     p.tile_rows = p.tile_splits > 1 ? a.q_tokens * a.q_heads : 0;
     p.factor = fmaxf(a.scale * kLog2e, FLT_MIN);   // scale 0: equal weights, and 0 times -inf does not arise
     const int64_t few = stats_floats(p.few_rows * p.few_splits) + p.few_rows * p.few_splits * a.dim;
@@ -952,16 +984,18 @@ template <typename T, int kD, typename Keys>
 hipError_t run(const RowsArgs &a, Plan p, hipStream_t stream)
 {
     const int64_t columns = static_cast<int64_t>(a.kv_heads) * p.chunks;
-    const int64_t few = p.any_few ? static_cast<int64_t>(a.n_clips) * p.few_splits * columns : 0;
+    // whole rounds of the chiplets
+    const int64_t blocks = static_cast<int64_t>(a.n_clips) * p.few_splits, few = !p.any_few ? 0 : (p.by_chiplet ? (blocks + 7) / 8 * 8 : blocks) * columns;
     const int64_t tile = p.tile_slots * static_cast<int64_t>(p.tile_splits) * columns;
     if (!fits(few + tile, kThreads) || !fits(a.q_tokens * a.q_heads, 64)) return hipErrorNotSupported;
     const bool one = p.few_limit * ((p.group + p.chunks - 1) / p.chunks) <= 16;
     const unsigned n = static_cast<unsigned>(few + tile);
-    if (tile == 0 && one) only_few_rows<T, kD, Keys, 1><<<n, kThreads, 0, stream>>>(a, p);
+    if (p.all_few && one) only_few_rows<T, kD, Keys, 1><<<n, kThreads, 0, stream>>>(a, p);
     else if (one) all_rows<T, kD, Keys, 1><<<n, kThreads, 0, stream>>>(a, p, static_cast<int>(tile));
     else all_rows<T, kD, Keys, 2><<<n, kThreads, 0, stream>>>(a, p, static_cast<int>(tile));
     if (p.few_splits > 1 || p.tile_splits > 1)
-        join_rows<T, kD, Keys><<<dim3(static_cast<unsigned>(a.q_tokens), a.q_heads), 64, 0, stream>>>(a, p);
+        join_rows<T, kD, Keys><<<dim3(p.join_clips ? a.n_clips * p.few_limit : static_cast<unsigned>(a.q_tokens),
+                                      (a.q_heads + kJoined<kD> - 1) / kJoined<kD>), 64, 0, stream>>>(a, p);
     return hipGetLastError();
 }
 
