@@ -388,7 +388,8 @@ RVQ_INLINE void few_rows(const RowsArgs &a, const Plan &p, int block, char *s_me
                         }
                     }
                     const float safe = m[s] == -INFINITY ? 0.0f : m[s] - kShift;
-                    vec8<T> w;
+                    // weights in two parts where they are rounded: the second product is not what the time goes to
+                    vec8<T> w, rest;
 #pragma unroll
                     for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -396,9 +397,14 @@ RVQ_INLINE void few_rows(const RowsArgs &a, const Plan &p, int block, char *s_me
                             const float e = fast_exp2(__builtin_fmaf(x[b][i], p.factor, -safe));
                             l[s] += e;
                             w[4 * b + i] = static_cast<T>(e);
+                            if constexpr (sizeof(T) == 2) rest[4 * b + i] = static_cast<T>(e - to_float(w[4 * b + i]));
                         }
 #pragma unroll
-                    for (int n = 0; n < kN; ++n) o[s][n] = mma16(d.v.at(n), w, o[s][n]);
+                    for (int n = 0; n < kN; ++n) {
+                        const vec8<T> v = d.v.at(n);
+                        if constexpr (sizeof(T) == 2) o[s][n] = mma16(v, rest, o[s][n]);
+                        o[s][n] = mma16(v, w, o[s][n]);
+                    }
                 }
             };
             Part part;
