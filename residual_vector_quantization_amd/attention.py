@@ -131,6 +131,16 @@ def _stream(t: torch.Tensor) -> int:
     return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
+def _launch(name: str, device: torch.device, *args) -> None:
+    """The call on the tensors' own device: a default stream is that of the device that is current."""
+    if torch._C._cuda_getDevice() == device.index:
+        st = getattr(_lib(), name)(*args)
+    else:
+        with torch.cuda.device(device):
+            st = getattr(_lib(), name)(*args)
+    _check(name, st)
+
+
 def _require_heads(t: torch.Tensor, name: str, dtype: torch.dtype, device, heads: Optional[int] = None,
                    dim: Optional[int] = None, tokens: Optional[int] = None) -> bytes:
     """A [tokens, heads, dim] tensor with contiguous rows, as the C structure; the C call checks strides and
@@ -268,9 +278,8 @@ def _backward(name, shape, dout, inputs, input_heads, out, lse, grads, workspace
     if workspace is None:
         workspace = q.new_empty(_size(name + "_bytes", shape), dtype=torch.uint8)
     _require(workspace, "workspace", torch.uint8, 1, dev)
-    st = getattr(_lib(), name)(shape, dout_heads, q_heads, k_heads, v_heads, out_heads, lse.data_ptr(), dq_heads, dk_heads,
-                               dv_heads, workspace.data_ptr(), workspace.numel(), _stream(q))
-    _check(name, st)
+    _launch(name, dev, shape, dout_heads, q_heads, k_heads, v_heads, out_heads, lse.data_ptr(), dq_heads, dk_heads,
+            dv_heads, workspace.data_ptr(), workspace.numel(), _stream(q))
     return dq, dk, dv
 
 
@@ -318,9 +327,8 @@ def rvq_cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q:
     if workspace is None:
         workspace = q.new_empty(_size("rvq_cross_attention_bytes", shape), dtype=torch.uint8)
     _require(workspace, "workspace", torch.uint8, 1, q.device)
-    st = _lib().rvq_cross_attention(shape, q_heads, k_heads, v_heads, out_heads, lse.data_ptr(), workspace.data_ptr(),
-                                    workspace.numel(), _stream(q))
-    _check("rvq_cross_attention", st)
+    _launch("rvq_cross_attention", q.device, shape, q_heads, k_heads, v_heads, out_heads, lse.data_ptr(),
+            workspace.data_ptr(), workspace.numel(), _stream(q))
     return out, lse
 
 
@@ -478,11 +486,9 @@ def rvq_cache_chunk_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: tor
     if workspace is None:
         workspace = q.new_empty(_size("rvq_cache_chunk_attention_bytes", shape, hq, n), dtype=torch.uint8)
     _require(workspace, "workspace", torch.uint8, 1, dev)
-    st = _lib().rvq_cache_chunk_attention(shape, hq, n, _ptr(cu), q_heads, k_pool.data_ptr(), v_pool.data_ptr(),
-                                          table.data_ptr(), lens.data_ptr(), _window(window), sinks,
-                                          1.0 / math.sqrt(dim) if scale is None else scale, out_heads, lse.data_ptr(),
-                                          workspace.data_ptr(), workspace.numel(), _stream(k_pool))
-    _check("rvq_cache_chunk_attention", st)
+    _launch("rvq_cache_chunk_attention", dev, shape, hq, n, _ptr(cu), q_heads, k_pool.data_ptr(), v_pool.data_ptr(),
+            table.data_ptr(), lens.data_ptr(), _window(window), sinks, 1.0 / math.sqrt(dim) if scale is None else scale,
+            out_heads, lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(k_pool))
     return out, lse
 
 
@@ -561,9 +567,8 @@ def rvq_rotary(q: Optional[torch.Tensor], k: Optional[torch.Tensor], frequencies
         if k_out is None:
             k_out = k.new_empty(k.shape)
         k_to = k_heads if k_out is k else _require_heads(k_out, "k_out", dtype, dev, hk, dim, tokens)
-    st = _lib().rvq_rotary(rotation, DTYPES[dtype], tokens, hq, hk, dim, clips, _ptr(cu), _ptr(first),
-                           _ptr(positions), x_heads if hq else None, k_heads if hk else None, q_to, k_to, _stream(x))
-    _check("rvq_rotary", st)
+    _launch("rvq_rotary", dev, rotation, DTYPES[dtype], tokens, hq, hk, dim, clips, _ptr(cu), _ptr(first),
+            _ptr(positions), x_heads if hq else None, k_heads if hk else None, q_to, k_to, _stream(x))
     return (None if q is None else q_out), (None if k is None else k_out)
 
 
@@ -596,10 +601,8 @@ def rvq_rotary_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tenso
         to = q_heads if out is q else _require_heads(out, "out", dtype, dev, hq, dim, n)
     elif out is not None:
         raise ValueError("out needs q")
-    st = _lib().rvq_rotary_append(_cache_shape(k_pool, clips, cols), rotation, hq, q_heads, k_heads, v_heads, n,
-                                  _ptr(cu), table.data_ptr(), lens.data_ptr(), to, k_pool.data_ptr(),
-                                  v_pool.data_ptr(), _stream(k_pool))
-    _check("rvq_rotary_append", st)
+    _launch("rvq_rotary_append", dev, _cache_shape(k_pool, clips, cols), rotation, hq, q_heads, k_heads, v_heads, n,
+            _ptr(cu), table.data_ptr(), lens.data_ptr(), to, k_pool.data_ptr(), v_pool.data_ptr(), _stream(k_pool))
     return out
 
 

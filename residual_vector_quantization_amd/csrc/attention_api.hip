@@ -45,6 +45,13 @@ bool good_output(const rvq_heads *h, int32_t dtype, int32_t heads, int32_t dim, 
     return heads_inside || tokens_inside;
 }
 
+// An output that starts where its input does has to be that input.
+bool same_or_apart(const rvq_heads *out, const rvq_heads *in, int32_t heads, int64_t tokens)
+{
+    return out->data != in->data || ((heads == 1 || out->head_stride == in->head_stride) &&
+                                     (tokens == 1 || out->token_stride == in->token_stride));
+}
+
 rvq::Heads heads(const rvq_heads *h) { return rvq::Heads{h->data, h->token_stride, h->head_stride}; }
 
 int clamp_window(int64_t window) { return window < 0 || window > INT_MAX ? INT_MAX : static_cast<int>(window); }
@@ -460,12 +467,16 @@ RVQ_API rvq_status rvq_rotary(const rvq_rotation *rotation, int32_t dtype, int64
     if (positions ? !aligned(positions, 4) : !ints(cu) || (first && !aligned(first, 4))) return RVQ_ERR_INVALID_ARG;
     rvq::RotaryArgs a = rotary_args(rotation, dtype, dim, n_tokens, n_clips);
     if (q_heads > 0) {
-        if (!good_heads(q, dtype) || !good_output(q_out, dtype, q_heads, dim, n_tokens)) return RVQ_ERR_INVALID_ARG;
+        if (!good_heads(q, dtype) || !good_output(q_out, dtype, q_heads, dim, n_tokens) ||
+            !same_or_apart(q_out, q, q_heads, n_tokens))
+            return RVQ_ERR_INVALID_ARG;
         a.q = heads(q);
         a.q_out = heads(q_out);
     }
     if (kv_heads > 0) {
-        if (!good_heads(k, dtype) || !good_output(k_out, dtype, kv_heads, dim, n_tokens)) return RVQ_ERR_INVALID_ARG;
+        if (!good_heads(k, dtype) || !good_output(k_out, dtype, kv_heads, dim, n_tokens) ||
+            !same_or_apart(k_out, k, kv_heads, n_tokens))
+            return RVQ_ERR_INVALID_ARG;
         a.k = heads(k);
         a.k_out = heads(k_out);
     }
@@ -495,7 +506,8 @@ RVQ_API rvq_status rvq_rotary_append(const rvq_cache_shape *shape, const rvq_rot
         return RVQ_ERR_INVALID_ARG;
     rvq::RotaryArgs a = rotary_args(rotation, shape->dtype, shape->dim, n_tokens, shape->n_clips);
     if (q_heads > 0) {
-        if (!good_heads(q, shape->dtype) || !good_output(q_out, shape->dtype, q_heads, shape->dim, n_tokens))
+        if (!good_heads(q, shape->dtype) || !good_output(q_out, shape->dtype, q_heads, shape->dim, n_tokens) ||
+            !same_or_apart(q_out, q, q_heads, n_tokens))
             return RVQ_ERR_INVALID_ARG;
         a.q = heads(q);
         a.q_out = heads(q_out);

@@ -941,8 +941,15 @@ void join_rows(RowsArgs a, Plan p)
 // most that a clip can have.
 inline Plan plan(const RowsArgs &a, int64_t keys, int64_t &floats)
 {
+    // few_rows: up to kWanted workgroups, each with kTurns tiles a wavefront or more, as every split of a row writes its
+    // accumulator (8 clips of 4 frames over up to 4000, 8 query heads a key head of 128: kTurns 1, 2, 3, 4 take 53, 39, 32,
+    // 42 us; 12 clips of up to 45000 frames: 512, 1024, 2048, 4096, 8192 workgroups take 293, 266, 255, 246, 262 us).
+    // tile_rows: as many workgroups as the chip holds at once, 2 a CU in 16 bits (256 frames over 8000: 256, 384, 512, 768
+    // workgroups take 84, 72, 62, 74 us), with least_tiles tiles each. Float32 takes six products for one, so that its
+    // workgroups' starts and ends weigh less (16 clips of 400 over 4000, dim 128: 512, 768, 1024 take 445, 407, 410 us; 6
+    // clips of 50 frames over 250 seen: splits of 8, 3, 2, 1 tiles take 26.6, 22.3, 20.6, 22.7 us).
     constexpr int64_t kWanted = 4096, kTurns = 3;
-    const int64_t wanted_tiles = a.dtype == RVQ_F32 ? 768 : 512, least_tiles = a.dtype == RVQ_F32 ? 2 : 4;      // workgroups that fill the chip
+    const int64_t wanted_tiles = a.dtype == RVQ_F32 ? 768 : 512, least_tiles = a.dtype == RVQ_F32 ? 2 : 4;
     Plan p = {};
     p.group = a.q_heads / a.kv_heads;
     p.chunks = (p.group + 31) / 32;
@@ -993,15 +1000,16 @@ hipError_t run(const RowsArgs &a, Plan p, hipStream_t stream)
     // whole rounds of the chiplets
     const int64_t blocks = static_cast<int64_t>(a.n_clips) * p.few_splits, few = !p.any_few ? 0 : (p.by_chiplet ? (blocks + 7) / 8 * 8 : blocks) * columns;
     const int64_t tile = p.tile_slots * static_cast<int64_t>(p.tile_splits) * columns;
-    if (!fits(few + tile, kThreads) || !fits(a.q_tokens * a.q_heads, 64)) return hipErrorNotSupported;
+    const bool join = p.few_splits > 1 || p.tile_splits > 1;
+    const int64_t join_rows_x = p.join_clips ? static_cast<int64_t>(a.n_clips) * p.few_limit : a.q_tokens;
+    const int join_heads = (a.q_heads + kJoined<kD> - 1) / kJoined<kD>;
+    if (!fits(few + tile, kThreads) || (join && !fits(join_rows_x * join_heads, 64))) return hipErrorNotSupported;
     const bool one = p.few_limit * ((p.group + p.chunks - 1) / p.chunks) <= 16;
     const unsigned n = static_cast<unsigned>(few + tile);
     if (p.all_few && one) only_few_rows<T, kD, Keys, 1><<<n, kThreads, 0, stream>>>(a, p);
     else if (one) all_rows<T, kD, Keys, 1><<<n, kThreads, 0, stream>>>(a, p, static_cast<int>(tile));
     else all_rows<T, kD, Keys, 2><<<n, kThreads, 0, stream>>>(a, p, static_cast<int>(tile));
-    if (p.few_splits > 1 || p.tile_splits > 1)
-        join_rows<T, kD, Keys><<<dim3(p.join_clips ? a.n_clips * p.few_limit : static_cast<unsigned>(a.q_tokens),
-                                      (a.q_heads + kJoined<kD> - 1) / kJoined<kD>), 64, 0, stream>>>(a, p);
+    if (join) join_rows<T, kD, Keys><<<dim3(static_cast<unsigned>(join_rows_x), join_heads), 64, 0, stream>>>(a, p);
     return hipGetLastError();
 }
 
