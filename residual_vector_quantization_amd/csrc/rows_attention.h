@@ -868,7 +868,7 @@ RVQ_INLINE void tile_rows(const RowsArgs &a, const Plan &p, int block, char *s_m
 
 // The tiles' workgroups come first: they last longer.
 template <typename T, int kD, typename Keys, int kSets>
-__global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? (kD == 64 ? 3 : 2) : 1)
 void all_rows(RowsArgs a, Plan p, int tile_groups)
 {
     constexpr int kTileBytes = Tiles<T, kD, Keys>::kBytes;
@@ -945,7 +945,9 @@ inline Plan plan(const RowsArgs &a, int64_t keys, int64_t &floats)
     // accumulator (8 clips of 4 frames over up to 4000, 8 query heads a key head of 128: kTurns 1, 2, 3, 4 take 53, 39, 32,
     // 42 us; 12 clips of up to 45000 frames: 512, 1024, 2048, 4096, 8192 workgroups take 293, 266, 255, 246, 262 us).
     // tile_rows: as many workgroups as the chip holds at once, 2 a CU in 16 bits (256 frames over 8000: 256, 384, 512, 768
-    // workgroups take 84, 72, 62, 74 us), with least_tiles tiles each. Float32 takes six products for one, so that its
+    // workgroups take 84, 72, 62, 74 us), with least_tiles tiles each. In dim 64 it holds 3, which pays where keys are many
+    // (2 clips of 1024 frames over 8000, 16 heads over 4: 256, 512, 768 workgroups take 202, 125, 111 us; 27 tiles a row in
+    // one workgroup and in two: 84 and 93 us). Float32 takes six products for one, so that its
     // workgroups' starts and ends weigh less (16 clips of 400 over 4000, dim 128: 512, 768, 1024 take 445, 407, 410 us; 6
     // clips of 50 frames over 250 seen: splits of 8, 3, 2, 1 tiles take 26.6, 22.3, 20.6, 22.7 us).
     constexpr int64_t kWanted = 4096, kTurns = 3;
@@ -977,8 +979,14 @@ inline Plan plan(const RowsArgs &a, int64_t keys, int64_t &floats)
         if (p.any_few && marked < slots) p.mark = p.few_limit + 1;
         p.tile_slots = static_cast<int>(p.mark ? marked : slots);
         const int64_t tiles = (keys + kTileRows - 1) / kTileRows;
-        int64_t n = wanted_tiles / ((a.q_tokens / p.tile_queries + 1) * columns);
+        const int64_t full = a.q_tokens / p.tile_queries;      // blocks of queries, those at clips' ends not counted
+        const int64_t groups = (full > 0 ? full : 1) * columns;
+        int64_t n = wanted_tiles / groups;
         n = n < tiles / least_tiles ? n : tiles / least_tiles;
+        if (a.dtype != RVQ_F32 && a.dim == 64) {
+            const int64_t third = 768 / groups < tiles / 32 ? 768 / groups : tiles / 32;
+            n = n > third ? n : third;
+        }
         p.tile_splits = static_cast<int>(n < 1 ? 1 : n < kMaxSplits ? n : kMaxSplits);
     }
     p.join_clips = !p.all_few && p.tile_splits == 1 && static_cast<int64_t>(a.n_clips) * p.few_limit < a.q_tokens;
