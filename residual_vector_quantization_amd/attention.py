@@ -134,11 +134,22 @@ def _stream(t: torch.Tensor) -> int:
 def _launch(name: str, device: torch.device, *args) -> None:
     """The call on the tensors' own device: a default stream is that of the device that is current."""
     if torch._C._cuda_getDevice() == device.index:
-        st = getattr(_lib(), name)(*args)
+        st = getattr(_ready or _lib(), name)(*args)
     else:
         with torch.cuda.device(device):
-            st = getattr(_lib(), name)(*args)
-    _check(name, st)
+            st = getattr(_ready or _lib(), name)(*args)
+    if st:
+        _check(name, st)
+
+
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _new_heads(like: torch.Tensor, tokens: int, heads: int, dim: int):
+    """A new [tokens, heads, dim] tensor, and it as the C structure."""
+    t = like.new_empty((tokens, heads, dim))
+    return t, _pack_heads(t.data_ptr(), heads * dim if tokens > 1 else 0, dim if heads > 1 else 0)
 
 
 def _require_heads(t: torch.Tensor, name: str, dtype: torch.dtype, device, heads: Optional[int] = None,
@@ -283,6 +294,15 @@ def _backward(name, shape, dout, inputs, input_heads, out, lse, grads, workspace
     return dq, dk, dv
 
 
+def _workspace(given: Optional[torch.Tensor], like: torch.Tensor, name: str, *args):
+    """The workspace that was given, or a new one where the operator needs any; and its size."""
+    if given is not None:
+        _require(given, "workspace", torch.uint8, 1, like.device)
+        return given, given.numel()
+    size = _size(name, *args)
+    return (like.new_empty(size, dtype=torch.uint8) if size else None), size
+
+
 def _cross_args(q, k, v, cu_q, cu_k, scale):
     """The checked call: (shape, q, k, v) as C structures, and q's sizes."""
     dtype, dev = _float_type(q, "q"), q.device
@@ -320,15 +340,15 @@ def rvq_cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q:
     every clip are not written.
     """
     shape, q_heads, k_heads, v_heads, size = _cross_args(q, k, v, cu_q, cu_k, scale)
+    dev = q.device
     if out is None:
-        out = q.new_empty(size)
-    out_heads = _require_heads(out, "out", q.dtype, q.device, size[1], size[2], size[0])
+        out, out_heads = _new_heads(q, *size)
+    else:
+        out_heads = _require_heads(out, "out", q.dtype, dev, size[1], size[2], size[0])
     lse = q.new_empty((size[1], size[0]), dtype=torch.float32)
-    if workspace is None:
-        workspace = q.new_empty(_size("rvq_cross_attention_bytes", shape), dtype=torch.uint8)
-    _require(workspace, "workspace", torch.uint8, 1, q.device)
-    _launch("rvq_cross_attention", q.device, shape, q_heads, k_heads, v_heads, out_heads, lse.data_ptr(),
-            workspace.data_ptr(), workspace.numel(), _stream(q))
+    work, work_bytes = _workspace(workspace, q, "rvq_cross_attention_bytes", shape)
+    _launch("rvq_cross_attention", dev, shape, q_heads, k_heads, v_heads, out_heads, lse.data_ptr(), _at(work), work_bytes,
+            _stream(q))
     return out, lse
 
 
@@ -479,16 +499,15 @@ def rvq_cache_chunk_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: tor
     if sinks < 0:
         raise ValueError(f"sinks={sinks} must not be negative")
     if out is None:
-        out = q.new_empty((n, hq, dim))
-    out_heads = _require_heads(out, "out", q.dtype, dev, hq, dim, n)
+        out, out_heads = _new_heads(q, n, hq, dim)
+    else:
+        out_heads = _require_heads(out, "out", q.dtype, dev, hq, dim, n)
     lse = q.new_empty((hq, n), dtype=torch.float32)
     shape = _cache_shape(k_pool, clips, cols)
-    if workspace is None:
-        workspace = q.new_empty(_size("rvq_cache_chunk_attention_bytes", shape, hq, n), dtype=torch.uint8)
-    _require(workspace, "workspace", torch.uint8, 1, dev)
-    _launch("rvq_cache_chunk_attention", dev, shape, hq, n, _ptr(cu), q_heads, k_pool.data_ptr(), v_pool.data_ptr(),
+    work, work_bytes = _workspace(workspace, q, "rvq_cache_chunk_attention_bytes", shape, hq, n)
+    _launch("rvq_cache_chunk_attention", dev, shape, hq, n, _at(cu), q_heads, k_pool.data_ptr(), v_pool.data_ptr(),
             table.data_ptr(), lens.data_ptr(), _window(window), sinks, 1.0 / math.sqrt(dim) if scale is None else scale,
-            out_heads, lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(k_pool))
+            out_heads, lse.data_ptr(), _at(work), work_bytes, _stream(k_pool))
     return out, lse
 
 
@@ -557,18 +576,22 @@ def rvq_rotary(q: Optional[torch.Tensor], k: Optional[torch.Tensor], frequencies
             if first.shape[0] != clips:
                 raise ValueError(f"first must have one entry per clip ({clips}), got {first.shape[0]}")
     q_out, k_out = (None, None) if out is None else out
-    hq, hk = 0 if q is None else q.shape[1], 0 if k is None else k.shape[1]
+    hq = hk = 0
     q_to = k_to = None
     if q is not None:
+        hq = q.shape[1]
         if q_out is None:
-            q_out = q.new_empty(q.shape)
-        q_to = x_heads if q_out is q else _require_heads(q_out, "q_out", dtype, dev, hq, dim, tokens)
+            q_out, q_to = _new_heads(q, tokens, hq, dim)
+        else:
+            q_to = x_heads if q_out is q else _require_heads(q_out, "q_out", dtype, dev, hq, dim, tokens)
     if k is not None:
+        hk = k.shape[1]
         if k_out is None:
-            k_out = k.new_empty(k.shape)
-        k_to = k_heads if k_out is k else _require_heads(k_out, "k_out", dtype, dev, hk, dim, tokens)
-    _launch("rvq_rotary", dev, rotation, DTYPES[dtype], tokens, hq, hk, dim, clips, _ptr(cu), _ptr(first),
-            _ptr(positions), x_heads if hq else None, k_heads if hk else None, q_to, k_to, _stream(x))
+            k_out, k_to = _new_heads(k, tokens, hk, dim)
+        else:
+            k_to = k_heads if k_out is k else _require_heads(k_out, "k_out", dtype, dev, hk, dim, tokens)
+    _launch("rvq_rotary", dev, rotation, DTYPES[dtype], tokens, hq, hk, dim, clips, _at(cu), _at(first),
+            _at(positions), x_heads if hq else None, k_heads if hk else None, q_to, k_to, _stream(x))
     return (None if q is None else q_out), (None if k is None else k_out)
 
 
@@ -597,12 +620,13 @@ def rvq_rotary_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tenso
         q_heads = _require_heads(q, "q", dtype, dev, dim=dim, tokens=n)
         hq = q.shape[1]
         if out is None:
-            out = q.new_empty(q.shape)
-        to = q_heads if out is q else _require_heads(out, "out", dtype, dev, hq, dim, n)
+            out, to = _new_heads(q, n, hq, dim)
+        else:
+            to = q_heads if out is q else _require_heads(out, "out", dtype, dev, hq, dim, n)
     elif out is not None:
         raise ValueError("out needs q")
     _launch("rvq_rotary_append", dev, _cache_shape(k_pool, clips, cols), rotation, hq, q_heads, k_heads, v_heads, n,
-            _ptr(cu), table.data_ptr(), lens.data_ptr(), to, k_pool.data_ptr(), v_pool.data_ptr(), _stream(k_pool))
+            _at(cu), table.data_ptr(), lens.data_ptr(), to, k_pool.data_ptr(), v_pool.data_ptr(), _stream(k_pool))
     return out
 
 
