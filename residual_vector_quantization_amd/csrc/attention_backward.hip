@@ -18,6 +18,8 @@
 // 286 us (27%; accumulators and operands take 400 registers, so 1 wavefront a
 // SIMD, and exponentials are not hidden behind another's products), sinks 6 us.
 // 8 clips of 2000 frames, all seen, 16 heads of 64 over 8, float16: 145 and 211 us.
+// Cross attention, 8 clips of up to 2000 queries over up to 1500 keys, 16 heads of 128
+// over 8, bfloat16: 115 and 202 us.
 //
 // Weights and dx enter the products in the inputs' type. bfloat16 has float32's
 // range, but float16 has 5 bits of exponent, so there weights are taken times
