@@ -134,6 +134,7 @@ RVQ_API rvq_status rvq_window_attention_backward(const rvq_attention_shape *shap
  *   workspace       device memory of at least rvq_cross_attention_bytes(shape)
  *                   bytes, 16-byte aligned (NULL where that is 0)
  *
+ * A value that is not finite reaches the results of its own clip alone.
  * Padded batches: a clip's rows have to follow one another, so rows of padding
  * may stand behind the last clip or before the first only.
  *

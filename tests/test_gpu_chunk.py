@@ -95,6 +95,49 @@ def test_many_clips():
     check("fp16", 64, 8, 1, 16, past[:70], [5 if b % 5 else 0 for b in range(70)])
 
 
+@pytest.mark.parametrize("typ", list(TYPES))
+def test_one_longer_clip_among_few_rows(typ):
+    """So few rows in all that one kind of workgroup takes them, a longer clip in turns; with its last values not finite,
+    and over keys that are split."""
+    check(typ, 64, 4, 2, 16, [40, 3, 90], [14, 1, 2], window=30, sinks=2)
+    check(typ, 128, 2, 1, 16, [5000, 10, 10], [14, 1, 1])
+    m, lens, new = rvq(), [54, 4, 92], [14, 1, 2]
+    k, v, table, _ = cache(typ, 64, 2, 16, lens)
+    q = torch.randn(17, 4, 64, generator=torch.Generator().manual_seed(3)).to(TYPES[typ]).to(DEV)
+    ref = want(q, k, v, table, lens, new, None, 0, 0.125)
+    v = v.clone()
+    v[table[0][53 // 16], :, 53 % 16, 7] = math.inf
+    v[table[0][51 // 16], 1, 51 % 16, 9] = math.nan
+    out, lse = m.rvq_cache_chunk_attention(q, k, v, ints(table), ints(lens), ints(offsets(new)))
+    fine = [i for i in range(17) if i not in (11, 12, 13)]
+    close("out", out[fine], tuple(x[fine] for x in ref["out"]))
+    close("lse", lse, ref["lse"])
+    odd = ~torch.isfinite(out[11:14]).cpu()
+    assert odd[2, :, 7].all() and odd[:, 2:, 9].all() and not odd[:, :2, 9].any() and not odd[:2, :, 7].any()
+    assert odd.sum() == 4 + 6
+
+
+def test_two_calls_at_once():
+    """On two streams, without anything in common."""
+    m = rvq()
+    sets = []
+    for seed, (past, new) in enumerate((([9000, 40], [2, 1]), ([700, 3000, 40], [100, 1, 60]))):
+        lens = [a + b for a, b in zip(past, new)]
+        k, v, table, _ = cache("bf16", 64, 2, 16, lens, seed=seed)
+        q = torch.randn(sum(new), 4, 64, device=DEV).to(torch.bfloat16)
+        args = (q, k, v, ints(table), ints(lens), ints(offsets(new)))
+        sets.append((args, m.rvq_cache_chunk_attention(*args), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for i in range(5):
+        got = []
+        for args, _, stream in sets:
+            with torch.cuda.stream(stream):
+                got.append(m.rvq_cache_chunk_attention(*args))
+        torch.cuda.synchronize()
+        for x, (_, y, _) in zip(got, sets):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+
+
 def test_other_scales():
     check("bf16", 64, 4, 2, 16, [300], [20], scale=2.5)
     check("fp32", 64, 4, 2, 16, [300], [5], scale=0.0)

@@ -62,6 +62,14 @@ def test_many_keys_and_many_queries(typ, dim):
 
 
 @pytest.mark.parametrize("typ", list(TYPES))
+def test_many_queries_of_few_keys(typ):
+    """The queries of a key are shared out among workgroups, within a head too."""
+    check(typ, 64, 1, 1, [3000], [20])
+    check(typ, 64, 3, 1, [1100, 1, 0, 700], [5, 1, 9, 0])
+    check(typ, 128, 2, 2, [900, 1300], [130, 3])
+
+
+@pytest.mark.parametrize("typ", list(TYPES))
 def test_one_query_each(typ):
     """With and without offsets; the gradient through offsets."""
     m, lens = rvq(), [300, 1, 0, 65, 64, 2500]
