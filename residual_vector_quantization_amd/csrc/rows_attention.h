@@ -98,37 +98,31 @@ __host__ __device__ inline int64_t stats_floats(int64_t slots) { return (2 * slo
 
 __device__ inline int heads_first(const Plan &p, int chunk) { return p.group * chunk / p.chunks; }
 
-// The last b in [0, n) with cu[b] / per + b <= slot (0 if there is none), searched by a whole wavefront, 64 entries at a
-// time: one read for up to 64 clips, two for 4096.
-RVQ_INLINE int clip_of_slot_wide(const int32_t *cu, int n, int slot, int per)
+// The last b in [0, n) that is before, which those up to some b are (0 if there is none), searched by a whole wavefront,
+// 64 at a time: one read of the offsets for up to 64 clips, two for 4096.
+template <typename Before>
+RVQ_INLINE int last_before(int n, Before before)
 {
     const int lane = threadIdx.x & 63;
     int lo = 0, size = n;
     while (size > 1) {
         const int step = (size + 63) / 64, b = lo + lane * step;
-        const bool before = b < lo + size && cu[b] / per + b <= slot;
-        const int count = __popcll(__ballot(before));
+        const int count = __popcll(__ballot(b < lo + size && before(b)));
         if (count == 0) break;
-        size = min(step, lo + size - (lo + (count - 1) * step));
+        size = min(step, size - (count - 1) * step);
         lo += (count - 1) * step;
     }
     return lo;
 }
 
-// The last b in [0, n) with cu[b] <= row, likewise.
+// As clip_of_slot and clip_of_row.
+RVQ_INLINE int clip_of_slot_wide(const int32_t *cu, int n, int slot, int per)
+{
+    return last_before(n, [=](int b) { return cu[b] / per + b <= slot; });
+}
 RVQ_INLINE int clip_of_row_wide(const int32_t *cu, int n, int row)
 {
-    const int lane = threadIdx.x & 63;
-    int lo = 0, size = n;
-    while (size > 1) {
-        const int step = (size + 63) / 64, b = lo + lane * step;
-        const bool before = b < lo + size && cu[b] <= row;
-        const int count = __popcll(__ballot(before));
-        if (count == 0) break;
-        size = min(step, lo + size - (lo + (count - 1) * step));
-        lo += (count - 1) * step;
-    }
-    return lo;
+    return last_before(n, [=](int b) { return cu[b] <= row; });
 }
 
 // Clips and their blocks of tile_queries queries are numbered without reading their lengths. mark 0: clip b owns the
@@ -356,7 +350,8 @@ RVQ_INLINE void few_rows(const RowsArgs &a, const Plan &p, int block, char *s_me
                         if (__shfl(d.mine, 8 * g + i) >= kPastEnd) d.v.clear(i);
                 }
                 // all keys of the tile are there and seen by every row
-                const int j_first = seen_position(seen, d.tile * kKeys), j_last = seen_position(seen, min(d.tile * kKeys + kKeys, seen.count) - 1);
+                const int j_first = seen_position(seen, d.tile * kKeys);
+                const int j_last = seen_position(seen, min(d.tile * kKeys + kKeys, seen.count) - 1);
                 const bool whole = there && (Keys::kAll || (j_last <= through && (j_first > from || j_last < a.sinks)));
 #pragma unroll
                 for (int s = 0; s < kSets; ++s) {
@@ -588,7 +583,8 @@ struct Tiles<T, kD, Paged<T, kD>> {
 #pragma unroll
         for (int n = 0; n < Rows::kCopies; ++n) {
             const int at = (n * kWaves + wave) * 64 + lane, row = at / Rows::kRowPieces;
-            const uint64_t offset = static_cast<uint64_t>(__shfl(places.next, row)) * Rows::kRowBytes + Rows::place(row, at % Rows::kRowPieces) * 16;
+            const uint64_t place = __shfl(places.next, row);
+            const uint64_t offset = place * Rows::kRowBytes + Rows::place(row, at % Rows::kRowPieces) * 16;
             copy16_from(reinterpret_cast<const char *>(places.keys.keys) + offset, to + (n * kWaves + wave) * 1024);
             copy16_from(reinterpret_cast<const char *>(places.keys.values) + offset, to + Rows::kBytes + (n * kWaves + wave) * 1024);
         }
@@ -860,7 +856,8 @@ RVQ_INLINE void tile_rows(const RowsArgs &a, const Plan &p, int block, char *s_m
         for (int n = 0; n < kD / 32; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<f32x4 *>(out + 32 * n + 8 * i + 4 * half) = f32x4{o[n][4 * i], o[n][4 * i + 1], o[n][4 * i + 2], o[n][4 * i + 3]};
+                *reinterpret_cast<f32x4 *>(out + 32 * n + 8 * i + 4 * half) =
+                    f32x4{o[n][4 * i], o[n][4 * i + 1], o[n][4 * i + 2], o[n][4 * i + 3]};
         if (half == 0) {
             p.tile[2 * at] = m - kShift;
             p.tile[2 * at + 1] = l;
@@ -952,7 +949,8 @@ void join_rows(RowsArgs a, Plan p)
 #pragma unroll
     for (int n = 0; n < 4; ++n) z[n] = static_cast<T>(sum == 0.0f ? 0.0f : y[n] / sum);
     store4(out + 4 * lane, z);
-    if (a.lse && lane == 0) a.lse[static_cast<int64_t>(head) * a.q_tokens + token] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    if (a.lse && lane == 0)
+        a.lse[static_cast<int64_t>(head) * a.q_tokens + token] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 // How the rows are shared out. It depends on shapes alone, so that the workspace's size is known beforehand. keys: the
@@ -979,15 +977,16 @@ inline Plan plan(const RowsArgs &a, int64_t keys, int64_t &floats)
     // 16 rows of few_rows where they do for most clips, 32 otherwise
     const int rows = heads <= 16 && average * heads <= 16 ? 16 : 32;
     p.few_limit = rows / heads;
-    // one clip alone has either many or few; so few rows in all that tile_rows' workgroups do not pay
-    p.all_few = !a.cu_q || a.q_tokens <= (a.n_clips == 1 ? 1 : 4) * p.few_limit;
+    // one clip alone has either many or few; few_rows takes all where there are so few that tile_rows' workgroups do not
+    // pay (8 clips of 4 frames, 8 query heads a key head: dim 64 20 -> 17 us, dim 128 36 -> 32)
+    p.all_few = !a.cu_q || a.q_tokens <= (a.n_clips == 1 ? 1 : 8) * p.few_limit;
     p.any_few = p.all_few || a.n_clips != 1;
     if (!p.any_few) p.few_limit = 0;
     p.few_splits = p.tile_splits = 1;
     p.tile_queries = kTileQueries / heads;
     if (p.any_few) {
         const int64_t tiles = (keys + kKeys - 1) / kKeys, base = a.n_clips * columns;
-        int64_t n = base > 0 ? kWanted / base : 1;
+        int64_t n = base > 0 ? (rows == 16 ? kWanted : 768) / base : 1;
         const int64_t most = tiles <= 4 * kWaves ? 1 : tiles / (kWaves * kTurns);
         n = n < most ? n : most;
         p.few_splits = static_cast<int>(n < 1 ? 1 : n < kMaxSplits ? n : kMaxSplits);
@@ -1024,7 +1023,8 @@ hipError_t run(const RowsArgs &a, Plan p, hipStream_t stream)
 {
     const int64_t columns = static_cast<int64_t>(a.kv_heads) * p.chunks;
     // whole rounds of the chiplets
-    const int64_t blocks = static_cast<int64_t>(a.n_clips) * p.few_splits, few = !p.any_few ? 0 : (p.by_chiplet ? (blocks + 7) / 8 * 8 : blocks) * columns;
+    const int64_t blocks = static_cast<int64_t>(a.n_clips) * p.few_splits;
+    const int64_t few = !p.any_few ? 0 : (p.by_chiplet ? (blocks + 7) / 8 * 8 : blocks) * columns;
     const int64_t tile = p.tile_slots * static_cast<int64_t>(p.tile_splits) * columns;
     const bool join = p.few_splits > 1 || p.tile_splits > 1;
     const int64_t join_rows_x = p.join_clips ? static_cast<int64_t>(a.n_clips) * p.few_limit : a.q_tokens;
@@ -1033,6 +1033,7 @@ hipError_t run(const RowsArgs &a, Plan p, hipStream_t stream)
     const bool one = p.few_limit * ((p.group + p.chunks - 1) / p.chunks) <= 16;
     const unsigned n = static_cast<unsigned>(few + tile);
     if (p.all_few && one) only_few_rows<T, kD, Keys, 1><<<n, kThreads, 0, stream>>>(a, p);
+    else if (p.all_few) only_few_rows<T, kD, Keys, 2><<<n, kThreads, 0, stream>>>(a, p);
     else if (one) all_rows<T, kD, Keys, 1><<<n, kThreads, 0, stream>>>(a, p, static_cast<int>(tile));
     else all_rows<T, kD, Keys, 2><<<n, kThreads, 0, stream>>>(a, p, static_cast<int>(tile));
     if (join) join_rows<T, kD, Keys><<<dim3(static_cast<unsigned>(join_rows_x), join_heads), 64, 0, stream>>>(a, p);
@@ -1042,8 +1043,10 @@ hipError_t run(const RowsArgs &a, Plan p, hipStream_t stream)
 template <template <typename, int> class Keys>
 hipError_t launch(const RowsArgs &a, const Plan &p, hipStream_t stream)
 {
-    if (a.dtype == RVQ_F32) return a.dim == 64 ? run<float, 64, Keys<float, 64>>(a, p, stream) : run<float, 128, Keys<float, 128>>(a, p, stream);
-    if (a.dtype == RVQ_F16) return a.dim == 64 ? run<f16_t, 64, Keys<f16_t, 64>>(a, p, stream) : run<f16_t, 128, Keys<f16_t, 128>>(a, p, stream);
+    if (a.dtype == RVQ_F32)
+        return a.dim == 64 ? run<float, 64, Keys<float, 64>>(a, p, stream) : run<float, 128, Keys<float, 128>>(a, p, stream);
+    if (a.dtype == RVQ_F16)
+        return a.dim == 64 ? run<f16_t, 64, Keys<f16_t, 64>>(a, p, stream) : run<f16_t, 128, Keys<f16_t, 128>>(a, p, stream);
     return a.dim == 64 ? run<bf16_t, 64, Keys<bf16_t, 64>>(a, p, stream) : run<bf16_t, 128, Keys<bf16_t, 128>>(a, p, stream);
 }
 

@@ -86,6 +86,14 @@ def test_long_caches_are_split_and_joined(typ, dim):
     check(typ, dim, 2, 1, 32, [3000, 700], [130, 1], window=2000, sinks=70)
 
 
+@pytest.mark.parametrize("typ,dim", [("bf16", 128), ("fp16", 64), ("fp32", 128), ("fp32", 64)])
+def test_two_sets_of_rows(typ, dim):
+    """17 to 32 rows a clip: alone, with a clip of more beside them, and a clip of many in turns."""
+    check(typ, dim, 8, 1, 16, [100, 700, 3], [4, 3, 4], window=300, sinks=2)
+    check(typ, dim, 16, 2, 16, [100] * 20, [4] * 17 + [40, 1, 3])
+    check(typ, dim, 8, 1, 16, [3000, 3], [29, 3])
+
+
 def test_many_clips():
     """Offsets searched in more than one step, and blocks of queries found by marks."""
     past = [(37 * b) % 90 for b in range(200)]
