@@ -249,7 +249,11 @@ __device__ inline float groups_sum(float x)
     return x + __shfl_xor(x, 32);
 }
 
-template <int kD> constexpr int kFewBytes = kWaves * 16 * (kD + 4 + 2) * 4;
+template <int kD> constexpr int kJoinBytes = kWaves * 16 * (kD + 4 + 2) * 4;
+// Where two sets of rows would not leave registers enough their queries stay in the LDS (48 clips of 4 frames over up to
+// 4000, 32 heads of 128 over 4: 102 -> 93 us, spilled registers 47 -> 27).
+template <typename T, int kD, int kSets> constexpr bool kStaged = kSets == 2 && kD == 128 && sizeof(T) == 2;
+template <typename T, int kD, int kSets> constexpr int kFewBytes = kJoinBytes<kD> + (kStaged<T, kD, kSets> ? kSets * kD / 32 * 1024 : 0);
 
 template <typename T, int kD, typename Keys, int kSets>
 RVQ_INLINE void few_rows(const RowsArgs &a, const Plan &p, int block, char *s_mem)
@@ -280,7 +284,9 @@ RVQ_INLINE void few_rows(const RowsArgs &a, const Plan &p, int block, char *s_me
         const int count = min(p.few_limit, r.nq - base);     // queries of this turn
         // this lane's row of every set
         int query[kSets], head[kSets];
-        vec8<T> q[kSets][kSteps];
+        constexpr bool kLds = kStaged<T, kD, kSets>;
+        vec8<T> *s_q = reinterpret_cast<vec8<T> *>(s_mem + kJoinBytes<kD>) + lane;      // [set][step][lane]
+        vec8<T> q[kLds ? 1 : kSets][kLds ? 1 : kSteps];
 #pragma unroll
         for (int s = 0; s < kSets; ++s) {
             const int at = min(16 * s + c, count * heads - 1);
@@ -288,8 +294,12 @@ RVQ_INLINE void few_rows(const RowsArgs &a, const Plan &p, int block, char *s_me
             head[s] = head0 + at - (query[s] - base) * heads;
             const T *from = static_cast<const T *>(a.q.data) + static_cast<int64_t>(r.q0 + query[s]) * a.q.token + head[s] * a.q.head;
 #pragma unroll
-            for (int t = 0; t < kSteps; ++t) q[s][t] = load8(from + 32 * t + 8 * g);
+            for (int t = 0; t < kSteps; ++t) {
+                if constexpr (!kLds) q[s][t] = load8(from + 32 * t + 8 * g);
+                else if (t == wave) s_q[(s * kSteps + t) * 64] = load8(from + 32 * t + 8 * g);
+            }
         }
+        if constexpr (kLds) __syncthreads();
         const int sets = (count * heads + 15) / 16;       // the others hold no row
 
         f32x4 o[kSets][kN];
@@ -362,7 +372,10 @@ RVQ_INLINE void few_rows(const RowsArgs &a, const Plan &p, int block, char *s_me
 #pragma unroll
                     for (int t = 0; t < kSteps; ++t)
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) x[b] = mma16(d.k[b][t], q[s][t], x[b]);
+                        for (int b = 0; b < 2; ++b) {
+                            if constexpr (kLds) x[b] = mma16(d.k[b][t], s_q[(s * kSteps + t) * 64], x[b]);
+                            else x[b] = mma16(d.k[b][t], q[s][t], x[b]);
+                        }
                     float top = -INFINITY;
                     if (!whole) {
                         const int position = position_of<Keys>(r, query[s]), low = below_window(position, a.window);
@@ -887,7 +900,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? (kD == 64 ? 3 : 2) : 1)
 void all_rows(RowsArgs a, Plan p, int tile_groups)
 {
     constexpr int kTileBytes = Tiles<T, kD, Keys>::kBytes;
-    __shared__ __attribute__((aligned(16))) char s_mem[kTileBytes > kFewBytes<kD> ? kTileBytes : kFewBytes<kD>];
+    constexpr int kRest = kFewBytes<T, kD, kSets>;
+    __shared__ __attribute__((aligned(16))) char s_mem[kTileBytes > kRest ? kTileBytes : kRest];
     const int block = blockIdx.x;
     if (block < tile_groups) tile_rows<T, kD, Keys>(a, p, block, s_mem);
     else few_rows<T, kD, Keys, kSets>(a, p, block - tile_groups, s_mem);
@@ -897,7 +911,7 @@ template <typename T, int kD, typename Keys, int kSets>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
 void only_few_rows(RowsArgs a, Plan p)
 {
-    __shared__ __attribute__((aligned(16))) char s_mem[kFewBytes<kD>];
+    __shared__ __attribute__((aligned(16))) char s_mem[kFewBytes<T, kD, kSets>];
     few_rows<T, kD, Keys, kSets>(a, p, blockIdx.x, s_mem);
 }
 
@@ -959,7 +973,9 @@ inline Plan plan(const RowsArgs &a, int64_t keys, int64_t &floats)
 {
     // few_rows: up to kWanted workgroups, each with kTurns tiles a wavefront or more, as every split of a row writes its
     // accumulator (8 clips of 4 frames over up to 4000, 8 query heads a key head of 128: kTurns 1, 2, 3, 4 take 53, 39, 32,
-    // 42 us; 12 clips of up to 45000 frames: 512, 1024, 2048, 4096, 8192 workgroups take 293, 266, 255, 246, 262 us).
+    // 42 us; 12 clips of up to 45000 frames: 512, 1024, 2048, 4096, 8192 workgroups take 293, 266, 255, 246, 262 us); with 32
+    // rows, which take more registers and write twice as much, up to 768 (the same drafts of 48 clips: 512, 1024, 2048, 4096
+    // take 106, 102, 121, 121 us; 24 single frames beside 8 chunks 75, 81, 82, 82).
     // tile_rows: as many workgroups as the chip holds at once, 2 a CU in 16 bits (256 frames over 8000: 256, 384, 512, 768
     // workgroups take 84, 72, 62, 74 us), with least_tiles tiles each. In dim 64 it holds 3, which pays where keys are many
     // (2 clips of 1024 frames over 8000, 16 heads over 4: 256, 512, 768 workgroups take 202, 125, 111 us; 27 tiles a row in
@@ -977,9 +993,11 @@ inline Plan plan(const RowsArgs &a, int64_t keys, int64_t &floats)
     // 16 rows of few_rows where they do for most clips, 32 otherwise
     const int rows = heads <= 16 && average * heads <= 16 ? 16 : 32;
     p.few_limit = rows / heads;
-    // one clip alone has either many or few; few_rows takes all where there are so few that tile_rows' workgroups do not
-    // pay (8 clips of 4 frames, 8 query heads a key head: dim 64 20 -> 17 us, dim 128 36 -> 32)
-    p.all_few = !a.cu_q || a.q_tokens <= (a.n_clips == 1 ? 1 : 8) * p.few_limit;
+    // One clip alone has either many or few. few_rows takes all where there are so few that tile_rows' workgroups do not
+    // pay: up to 4 turns, or 8 where that is no more than 64 queries (8 clips of 4 frames, 8 query heads a key head: dim 64
+    // 20 -> 17 us, dim 128 36 -> 33; 8 turns for 6 float32 clips of up to 50 queries, 8 heads: 20 -> 27 us).
+    const int64_t turns = 8 * p.few_limit <= 64 ? 8 : 4;
+    p.all_few = !a.cu_q || a.q_tokens <= (a.n_clips == 1 ? 1 : turns) * p.few_limit;
     p.any_few = p.all_few || a.n_clips != 1;
     if (!p.any_few) p.few_limit = 0;
     p.few_splits = p.tile_splits = 1;
