@@ -14,7 +14,9 @@
  * anything is enqueued, status codes of rvq_status. Shapes that take 2^24
  * workgroups or more are refused (RVQ_ERR_UNSUPPORTED). A workgroup is a head
  * of 128 frames or of a clip's rest in the windowed attention, 16 query heads
- * of a key head and clip in the cache attention, 8 new frames in an append.
+ * of a key head and clip in the cache attention, 128 queries and heads of a key
+ * head, or a clip's few ones, in chunk and cross attention (times the splits of
+ * their keys), 8 new frames in an append, 256 times 32 bytes in rotary positions.
  *
  * Which frames a frame sees. A frame at position p of its clip sees the
  * frames j <= p with p - j < window, and of those further back the first
@@ -28,7 +30,8 @@
  * mean square, or as float32); scores, softmax statistics and accumulators
  * are float32. Attention weights and score gradients are rounded once to the
  * inputs' type where they enter a matrix product of it (in float16 times a
- * power of two that keeps them within its range), outputs once at the end. No
+ * power of two that keeps them within its range; weights of chunk and cross
+ * attention as two parts where a clip has few queries), outputs once at the end. No
  * sum's order depends on timing: the same call gives the same bits.
  */
 #ifndef RVQ_ATTENTION_H
