@@ -48,6 +48,53 @@ RVQ_HOST_DEVICE inline Seen seen_frames(int len, int window, int sinks)
 
 RVQ_HOST_DEVICE inline int seen_position(const Seen &s, int nth) { return nth < s.first ? nth : nth - s.first + s.low; }
 
+// Whether a query at a position sees frame j.
+RVQ_HOST_DEVICE inline bool sees_frame(int position, int j, int window, int sinks)
+{
+    return j <= position && (position - j < window || j < sinks);
+}
+
+// The frames that some query between positions p_first and p_last sees: sinks, then the window.
+RVQ_HOST_DEVICE inline Seen seen_between(int p_first, int p_last, int window, int sinks)
+{
+    Seen s = {0, 0, 0};
+    if (p_last < 0) return s;
+    const int64_t low = static_cast<int64_t>(p_first) - window + 1;
+    s.low = low > 0 ? static_cast<int>(low) : 0;
+    const int before = sinks < s.low ? sinks : s.low;
+    s.first = before < p_last + 1 ? before : p_last + 1;
+    s.count = s.first + (p_last + 1 > s.low ? p_last + 1 - s.low : 0);
+    return s;
+}
+
+// How the frames that queries p_first .. p_last see are shared out among `splits` workgroups, in tiles of kSharedTile: split
+// n has the tiles n per .. (n + 1) per - 1. A workgroup that goes over its part again for one of the queries alone
+// leaves out what that one does not see, but keeps its part: others may not go over theirs again, and the splits of a
+// row have to hold every frame once.
+constexpr int kSharedTile = 32;
+
+struct Shared {
+    Seen seen;
+    int tiles, per;
+};
+
+RVQ_HOST_DEVICE inline Shared share(int p_first, int p_last, int window, int sinks, int splits)
+{
+    Shared s;
+    s.seen = seen_between(p_first, p_last, window, sinks);
+    s.tiles = (s.seen.count + kSharedTile - 1) / kSharedTile;
+    s.per = (s.tiles + splits - 1) / splits;
+    return s;
+}
+
+// Frame nth of them, or -1: there is none, or only the query at `position` counts (alone) and does not see it.
+RVQ_HOST_DEVICE inline int shared_frame(const Shared &s, int nth, bool alone, int position, int window, int sinks)
+{
+    if (nth >= s.seen.count) return -1;
+    const int j = seen_position(s.seen, nth);
+    return alone && !sees_frame(position, j, window, sinks) ? -1 : j;
+}
+
 // Row (of head dim values) of a position's frame in a pool, or kNoPage where the table holds no page for it.
 // `row` is the clip's row of the table. Pools have fewer than 2^32 - 2 rows.
 constexpr uint32_t kNoPage = 0xffffffffu;

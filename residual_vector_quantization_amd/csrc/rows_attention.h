@@ -48,8 +48,8 @@
 //
 // Values that a row does not see: its weights there are 0, but 0 times a value
 // that is not finite is not 0. Where rows of a workgroup see different keys and a
-// result is not finite, few_rows makes a pass for each query of its own, with
-// only what that query sees; tile_rows repeats its pass to find, for every result,
+// result is not finite, few_rows makes a pass for each query of its own, over the
+// same part of the keys with only what that query sees; tile_rows repeats its pass to find, for every result,
 // whether keys that are seen have an infinity of either sign there (a NaN is
 // both), and once more with these values taken as 0.
 #pragma once
@@ -73,7 +73,7 @@ namespace rows {
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kTileQueries = 32 * kWaves;   // rows of tile_rows
-constexpr int kKeys = 32;                   // keys a wavefront of few_rows takes at a time
+constexpr int kKeys = kSharedTile;          // keys a wavefront of few_rows takes at a time
 constexpr float kSlack = 8.0f;              // how far (powers of two) a score may exceed the running maximum
 constexpr int kMaxSplits = 256;
 
@@ -198,18 +198,6 @@ struct Packed {
 template <typename Keys>
 RVQ_INLINE int position_of(const ClipRows &r, int i) { return Keys::kAll ? r.nk - 1 : r.nk - r.nq + i; }
 
-// The frames that some query between positions p_first and p_last sees: sinks, then the window.
-RVQ_INLINE Seen seen_between(int p_first, int p_last, int window, int sinks)
-{
-    Seen s = {0, 0, 0};
-    if (p_last < 0) return s;
-    const int64_t low = static_cast<int64_t>(p_first) - window + 1;
-    s.low = low > 0 ? static_cast<int>(low) : 0;
-    s.first = min(min(sinks, s.low), p_last + 1);
-    s.count = s.first + max(0, p_last + 1 - s.low);
-    return s;
-}
-
 // ---------------------------------------------------------------- few rows
 
 // kN values of 8 keys, as the kN operands of 8 keys at one dim.
@@ -304,10 +292,14 @@ RVQ_INLINE void few_rows(const RowsArgs &a, const Plan &p, int block, char *s_me
 
         f32x4 o[kSets][kN];
         float m[kSets], l[kSets];
+        // the split's part of the keys stays the same, whichever of the turn's queries a pass is for
+        const Shared shared = share(r.beyond ? -1 : position_of<Keys>(r, base), r.beyond ? -1 : position_of<Keys>(r, base + count - 1),
+                                    a.window, a.sinks, p.few_splits);
+        const Seen &seen = shared.seen;
         // over the keys that the queries first .. last see; rows of others come out without sense
         auto pass = [&](int first, int last) __attribute__((always_inline)) {
             const int p_first = position_of<Keys>(r, first), p_last = position_of<Keys>(r, last);
-            const Seen seen = seen_between(r.beyond ? -1 : p_first, r.beyond ? -1 : p_last, a.window, a.sinks);
+            const bool alone = !Keys::kAll && first == last && count > 1;
             // positions up to `through` are seen by all of the queries if they are above `from` (or sinks)
             const int through = p_first, from = below_window(p_last, a.window);
 #pragma unroll
@@ -317,14 +309,12 @@ RVQ_INLINE void few_rows(const RowsArgs &a, const Plan &p, int block, char *s_me
 #pragma unroll
                 for (int n = 0; n < kN; ++n) o[s][n] = f32x4{};
             }
-            const int tiles = (seen.count + kKeys - 1) / kKeys;
-            const int per = (tiles + p.few_splits - 1) / p.few_splits;
-            const int end = min(tiles, (split + 1) * per);
+            const int end = min(shared.tiles, (split + 1) * shared.per);
             // lane n holds the place of the tile's key n % 32
             auto find = [&](int tile) -> uint32_t {
-                const int nth = tile * kKeys + (lane & 31);
-                if (tile >= end || nth >= seen.count) return kPastEnd;
-                return keys.find(seen_position(seen, nth));
+                if (tile >= end) return kPastEnd;
+                const int j = shared_frame(shared, tile * kKeys + (lane & 31), alone, p_first, a.window, a.sinks);
+                return j < 0 ? kPastEnd : keys.find(j);
             };
             struct Part {
                 int tile;
@@ -434,7 +424,7 @@ RVQ_INLINE void few_rows(const RowsArgs &a, const Plan &p, int block, char *s_me
                 }
             };
             Part part;
-            int tile = split * per + wave;
+            int tile = split * shared.per + wave;
             uint32_t next = find(tile);
             for (; tile < end; tile += kWaves) {
                 load(part, tile, next);
