@@ -137,7 +137,9 @@ RVQ_API rvq_status rvq_window_attention_backward(const rvq_attention_shape *shap
  *   workspace       device memory of at least rvq_cross_attention_bytes(shape)
  *                   bytes, 16-byte aligned (NULL where that is 0)
  *
- * A value that is not finite reaches the results of its own clip alone.
+ * A value that is not finite reaches the results of its own clip alone: as
+ * above an infinite one makes the output infinite there, with its sign, NaN or
+ * infinities of both signs make it NaN.
  * Padded batches: a clip's rows have to follow one another, so rows of padding
  * may stand behind the last clip or before the first only.
  *
@@ -239,7 +241,8 @@ RVQ_API rvq_status rvq_cache_attention(const rvq_cache_shape *shape, int32_t q_h
  * frame without a valid page gets quiet NaN, and so do all queries of a clip
  * whose count is beyond the table. A value that a query does not see has no
  * influence on its output, not even where it is infinite or NaN; a seen one
- * that is not finite makes the output not finite there.
+ * that is infinite makes the output infinite there, with its sign, NaN or
+ * infinities of both signs make it NaN (a key with score -inf is not seen).
  */
 RVQ_API int64_t rvq_cache_chunk_attention_bytes(const rvq_cache_shape *shape, int32_t q_heads, int64_t n_tokens);
 RVQ_API rvq_status rvq_cache_chunk_attention(const rvq_cache_shape *shape, int32_t q_heads, int64_t n_tokens,

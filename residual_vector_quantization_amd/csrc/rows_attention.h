@@ -47,11 +47,13 @@
 // accumulators.
 //
 // Values that a row does not see: its weights there are 0, but 0 times a value
-// that is not finite is not 0. Where rows of a workgroup see different keys and a
-// result is not finite, few_rows makes a pass for each query of its own, over the
-// same part of the keys with only what that query sees; tile_rows repeats its pass to find, for every result,
-// whether keys that are seen have an infinity of either sign there (a NaN is
-// both), and once more with these values taken as 0.
+// that is not finite is not 0. And of a value that is seen, an infinity times a
+// weight of 0 (a second part, or one below float32's numbers) would be NaN. So
+// where a result is not finite, few_rows goes over its part of the keys again for
+// each such row alone, with what it sees only (one_row), and tile_rows repeats its
+// pass to find, for every result, whether keys that are seen have an infinity of
+// either sign there (a NaN is both), and once more with these values taken as 0.
+// The joins leave sums that are not finite unscaled, for a factor may be 0 too.
 #pragma once
 
 #include <float.h>
@@ -241,7 +243,113 @@ template <int kD> constexpr int kJoinBytes = kWaves * 16 * (kD + 4 + 2) * 4;
 // Where two sets of rows would not leave registers enough their queries stay in the LDS (48 clips of 4 frames over up to
 // 4000, 32 heads of 128 over 4: 102 -> 93 us, spilled registers 47 -> 27).
 template <typename T, int kD, int kSets> constexpr bool kStaged = kSets == 2 && kD == 128 && sizeof(T) == 2;
-template <typename T, int kD, int kSets> constexpr int kFewBytes = kJoinBytes<kD> + (kStaged<T, kD, kSets> ? kSets * kD / 32 * 1024 : 0);
+template <typename T, int kD, int kSets> constexpr int kStagedBytes = kJoinBytes<kD> + (kStaged<T, kD, kSets> ? kSets * kD / 32 * 1024 : 0);
+template <typename T, int kD, int kSets> constexpr int kFewBytes = kStagedBytes<T, kD, kSets> + 16;
+
+// A partial sum times a factor. An infinite one stays so if the factor is 0.
+__device__ inline float scaled(float x, float factor) { return fabsf(x) <= FLT_MAX ? x * factor : x; }
+
+// Where few_rows leaves a query's results: the outputs, or a split's partial ones. top in powers of two.
+template <typename T>
+RVQ_INLINE void put(const RowsArgs &a, const Plan &p, const ClipRows &r, int clip, int split, int i, int h, int d, int dim,
+                    float top, float total, float y)
+{
+    if (p.few_splits == 1) {
+        T *out = static_cast<T *>(a.out.data) + static_cast<int64_t>(r.q0 + i) * a.out.token + h * a.out.head;
+        out[d] = static_cast<T>(total == 0.0f ? 0.0f : y / total);
+        if (a.lse && d == 0)
+            a.lse[static_cast<int64_t>(h) * a.q_tokens + r.q0 + i] = total == 0.0f ? -INFINITY : (top + log2f(total)) * kLn2;
+    } else {
+        const int64_t at_row = p.all_few ? r.q0 + i : static_cast<int64_t>(clip) * p.few_limit + i;
+        const int64_t slot = (at_row * a.q_heads + h) * p.few_splits + split;
+        p.few[stats_floats(p.few_rows * p.few_splits) + slot * dim + d] = y;
+        if (d == 0) {
+            p.few[2 * slot] = top;
+            p.few[2 * slot + 1] = total;
+        }
+    }
+}
+
+// One row of few_rows again, query i and head h over the workgroup's own part of the keys, after a result that is not
+// finite: only what the query sees is read, and infinities and NaN are noted apart from the sums. Rare and simple: a
+// thread a key for the scores of kThreads keys, then a thread a dim for their values.
+template <typename T, int kD, typename Keys>
+RVQ_INLINE void one_row(const RowsArgs &a, const Plan &p, const ClipRows &r, const Keys &keys, const Shared &shared, int clip,
+                        int split, int i, int h, char *s_mem)
+{
+    constexpr int kSlices = kThreads / kD;
+    float *s_weight = reinterpret_cast<float *>(s_mem);                       // of each key; -1: not seen
+    uint32_t *s_place = reinterpret_cast<uint32_t *>(s_weight + kThreads);
+    float *s_value = reinterpret_cast<float *>(s_place + kThreads);           // one a thread
+    float *s_wave = s_value + kThreads;
+    const int wave = threadIdx.x >> 6, d = threadIdx.x % kD, slice = threadIdx.x / kD;
+    const T *q = static_cast<const T *>(a.q.data) + static_cast<int64_t>(r.q0 + i) * a.q.token + h * a.q.head;
+    const int position = position_of<Keys>(r, i);
+    const int last = min(min(shared.tiles, (split + 1) * shared.per) * kKeys, shared.seen.count);
+    float top = -INFINITY, sum = 0.0f, y = 0.0f;
+    bool plus = false, minus = false;
+    for (int nth0 = split * shared.per * kKeys; nth0 < last; nth0 += kThreads) {
+        const int nth = nth0 + static_cast<int>(threadIdx.x);
+        const int j = nth < last ? shared_frame(shared, nth, !Keys::kAll, position, a.window, a.sinks) : -1;
+        uint32_t place = j < 0 ? kPastEnd : keys.find(j);
+        float x = -INFINITY;
+        if (place == kNoPage) sum = __builtin_nanf("");
+        else if (place != kPastEnd) {
+            x = 0.0f;
+            const T *key = keys.key(place);
+#pragma unroll 1
+            for (int n = 0; n < kD; n += 8) {
+                const vec8<T> u = load8(q + n), w = load8(key + n);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x = __builtin_fmaf(to_float(u[e]), to_float(w[e]), x);
+            }
+            x *= p.factor;
+        }
+        float most = x;
+#pragma unroll
+        for (int m = 32; m > 0; m >>= 1) most = fmaxf(most, __shfl_xor(most, m));
+        __syncthreads();      // what was left in the LDS has been read
+        if ((threadIdx.x & 63) == 0) s_wave[wave] = most;
+        __syncthreads();
+        const float before = top;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) top = fmaxf(top, s_wave[w]);
+        const float keep = before == -INFINITY ? 0.0f : fast_exp2(before - top);
+        const bool sees = x != -INFINITY;
+        const float weight = sees ? fast_exp2(x - top) : -1.0f;
+        sum = sum * keep + (sees ? weight : 0.0f);
+        s_weight[threadIdx.x] = weight;
+        s_place[threadIdx.x] = place;
+        __syncthreads();
+        y *= keep;
+#pragma unroll 1
+        for (int n = slice; n < min(kThreads, last - nth0); n += kSlices) {
+            const float w = s_weight[n];
+            if (w == -1.0f) continue;
+            const float v = to_float(keys.value(s_place[n])[d]);
+            const bool up = !(v <= FLT_MAX), down = !(v >= -FLT_MAX);
+            plus = plus || up;
+            minus = minus || down;
+            y += up || down ? 0.0f * w : w * v;
+        }
+    }
+    if (plus || minus) y = plus && minus ? __builtin_nanf("") : plus ? INFINITY : -INFINITY;
+    sum = wave_sum(sum);
+    __syncthreads();
+    s_value[threadIdx.x] = y;
+    if ((threadIdx.x & 63) == 0) s_wave[wave] = sum;
+    __syncthreads();
+    if (slice == 0) {
+        float total = 0.0f;
+        y = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) total += s_wave[w];
+#pragma unroll
+        for (int n = 0; n < kSlices; ++n) y += s_value[n * kD + d];
+        put<T>(a, p, r, clip, split, i, h, d, kD, top, total, y);
+    }
+    __syncthreads();
+}
 
 template <typename T, int kD, typename Keys, int kSets>
 RVQ_INLINE void few_rows(const RowsArgs &a, const Plan &p, int block, char *s_mem)
@@ -292,14 +400,10 @@ RVQ_INLINE void few_rows(const RowsArgs &a, const Plan &p, int block, char *s_me
 
         f32x4 o[kSets][kN];
         float m[kSets], l[kSets];
-        // the split's part of the keys stays the same, whichever of the turn's queries a pass is for
-        const Shared shared = share(r.beyond ? -1 : position_of<Keys>(r, base), r.beyond ? -1 : position_of<Keys>(r, base + count - 1),
-                                    a.window, a.sinks, p.few_splits);
+        const int p_first = position_of<Keys>(r, base), p_last = position_of<Keys>(r, base + count - 1);
+        const Shared shared = share(r.beyond ? -1 : p_first, r.beyond ? -1 : p_last, a.window, a.sinks, p.few_splits);
         const Seen &seen = shared.seen;
-        // over the keys that the queries first .. last see; rows of others come out without sense
-        auto pass = [&](int first, int last) __attribute__((always_inline)) {
-            const int p_first = position_of<Keys>(r, first), p_last = position_of<Keys>(r, last);
-            const bool alone = !Keys::kAll && first == last && count > 1;
+        {
             // positions up to `through` are seen by all of the queries if they are above `from` (or sinks)
             const int through = p_first, from = below_window(p_last, a.window);
 #pragma unroll
@@ -313,7 +417,7 @@ RVQ_INLINE void few_rows(const RowsArgs &a, const Plan &p, int block, char *s_me
             // lane n holds the place of the tile's key n % 32
             auto find = [&](int tile) -> uint32_t {
                 if (tile >= end) return kPastEnd;
-                const int j = shared_frame(shared, tile * kKeys + (lane & 31), alone, p_first, a.window, a.sinks);
+                const int j = shared_frame(shared, tile * kKeys + (lane & 31), false, 0, a.window, a.sinks);
                 return j < 0 ? kPastEnd : keys.find(j);
             };
             struct Part {
@@ -431,9 +535,11 @@ RVQ_INLINE void few_rows(const RowsArgs &a, const Plan &p, int block, char *s_me
                 next = find(tile + kWaves);
                 use(part);
             }
-        };
-        // joins the wavefronts and writes the rows of queries first .. last
-        auto finish = [&](int first, int last) __attribute__((always_inline)) {
+        }
+        // joins the wavefronts and writes the rows
+        uint32_t *s_odd = reinterpret_cast<uint32_t *>(s_mem + kStagedBytes<T, kD, kSets>);   // rows with something not finite, a bit each
+        if (threadIdx.x == 0) *s_odd = 0;
+        {
 #pragma unroll
             for (int s = 0; s < kSets; ++s) {
                 if (s >= sets) break;
@@ -452,7 +558,6 @@ RVQ_INLINE void few_rows(const RowsArgs &a, const Plan &p, int block, char *s_me
                 for (int at = threadIdx.x; at < rows * kD; at += kThreads) {
                     const int row = at / kD, d = at - row * kD, nth = (16 * s + row) / heads;
                     const int i = base + nth, h = head0 + (16 * s + row) - nth * heads;
-                    if (i < first || i > last) continue;
                     float top = -INFINITY, total = 0.0f, y = 0.0f;
 #pragma unroll
                     for (int w = 0; w < kWaves; ++w) top = fmaxf(top, s_max[w][row]);
@@ -463,46 +568,21 @@ RVQ_INLINE void few_rows(const RowsArgs &a, const Plan &p, int block, char *s_me
                         total += s_sum[w][row] * f;
                         y += s_out[w][row][d] * f;
                     }
-                    if (p.few_splits == 1) {
-                        T *out = static_cast<T *>(a.out.data) + static_cast<int64_t>(r.q0 + i) * a.out.token + h * a.out.head;
-                        out[d] = static_cast<T>(total == 0.0f ? 0.0f : y / total);
-                        if (a.lse && d == 0)
-                            a.lse[static_cast<int64_t>(h) * a.q_tokens + r.q0 + i] =
-                                total == 0.0f ? -INFINITY : (top - kShift + log2f(total)) * kLn2;
-                    } else {
-                        const int64_t at_row = p.all_few ? r.q0 + i : static_cast<int64_t>(clip) * p.few_limit + i;
-                        const int64_t slot = (at_row * a.q_heads + h) * p.few_splits + split;
-                        p.few[stats_floats(p.few_rows * p.few_splits) + slot * kD + d] = y;
-                        if (d == 0) {
-                            p.few[2 * slot] = top - kShift;
-                            p.few[2 * slot + 1] = total;
-                        }
-                    }
+                    if (!(fabsf(y) <= FLT_MAX)) atomicOr(s_odd, 1u << (16 * s + row));
+                    put<T>(a, p, r, clip, split, i, h, d, kD, top - kShift, total, y);
                 }
             }
-        };
-        // all queries at once, or, after a result that is not finite, one after another
-        bool each = Keys::kAll || count == 1;
-        for (int first = base, last = base + count - 1;;) {
-            pass(first, last);
-            if (!each) {
-                each = true;
-                bool odd = false;
-#pragma unroll
-                for (int s = 0; s < kSets; ++s)
-#pragma unroll
-                    for (int n = 0; n < kN; ++n)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) odd = odd || !(fabsf(o[s][n][i]) <= FLT_MAX);
-                if (__syncthreads_or(odd)) {
-                    last = first;
-                    continue;
-                }
+        }
+        __syncthreads();
+        uint32_t rows = *s_odd;
+        if (rows != 0) {
+            __threadfence();      // what these rows are now is written before what they become
+            __syncthreads();
+            while (rows != 0) {
+                const int row = __builtin_ctz(rows), nth = row / heads;
+                rows &= rows - 1;
+                one_row<T, kD, Keys>(a, p, r, keys, shared, clip, split, base + nth, head0 + row - nth * heads, s_mem);
             }
-            finish(first, last);
-            if (last == base + count - 1) break;
-            first = ++last;
-            __syncthreads();      // what was left in the LDS has been read
         }
         if (base + count < r.nq) __syncthreads();
     }
@@ -947,6 +1027,14 @@ void join_rows(RowsArgs a, Plan p)
     f32x4 y = {};
 #pragma unroll 8
     for (int s = 0; s < splits; ++s) y += *reinterpret_cast<const f32x4 *>(sums + s * kD) * s_factor[nth][s];
+    bool odd = false;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) odd = odd || !(fabsf(y[n]) <= FLT_MAX);
+    if (odd) {
+        y = f32x4{};
+        for (int s = 0; s < splits; ++s)
+            for (int n = 0; n < 4; ++n) y[n] += scaled(sums[s * kD + n], s_factor[nth][s]);
+    }
     if (own >= a.q_heads) return;
     T *out = static_cast<T *>(a.out.data) + static_cast<int64_t>(token) * a.out.token + head * a.out.head;
     T z[4];
