@@ -238,8 +238,7 @@ def rvq_window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q
         out = q.new_empty(size)
     out_heads = _require_heads(out, "out", q.dtype, q.device, size[1], size[2], size[0])
     lse = q.new_empty((size[1], size[0]), dtype=torch.float32)
-    st = _lib().rvq_window_attention(shape, q_heads, k_heads, v_heads, out_heads, lse.data_ptr(), _stream(q))
-    _check("rvq_window_attention", st)
+    _launch("rvq_window_attention", q.device, shape, q_heads, k_heads, v_heads, out_heads, lse.data_ptr(), _stream(q))
     return out, lse
 
 
@@ -413,9 +412,8 @@ def rvq_cache_append(k: torch.Tensor, v: torch.Tensor, k_pool: torch.Tensor, v_p
         _offsets(cu, "cu", dev, clips)
     elif n != clips:
         raise ValueError("without cu, k must have one frame per clip")
-    st = _lib().rvq_cache_append(_cache_shape(k_pool, clips, cols), k_heads, v_heads, n, _ptr(cu), table.data_ptr(),
-                                 lens.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), _stream(k_pool))
-    _check("rvq_cache_append", st)
+    _launch("rvq_cache_append", dev, _cache_shape(k_pool, clips, cols), k_heads, v_heads, n, _ptr(cu),
+            table.data_ptr(), lens.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), _stream(k_pool))
 
 
 def _cache_attention_bytes(shape: bytes, q_heads: int) -> int:
@@ -457,11 +455,9 @@ def rvq_cache_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Ten
     if workspace is None:
         workspace = q.new_empty(_cache_attention_bytes(shape, hq), dtype=torch.uint8)
     _require(workspace, "workspace", torch.uint8, 1, dev)
-    st = _lib().rvq_cache_attention(shape, hq, q_heads, k_pool.data_ptr(), v_pool.data_ptr(), table.data_ptr(),
-                                    lens.data_ptr(), _window(window), sinks,
-                                    1.0 / math.sqrt(dim) if scale is None else scale, out_heads, workspace.data_ptr(),
-                                    workspace.numel(), _stream(k_pool))
-    _check("rvq_cache_attention", st)
+    _launch("rvq_cache_attention", dev, shape, hq, q_heads, k_pool.data_ptr(), v_pool.data_ptr(), table.data_ptr(),
+            lens.data_ptr(), _window(window), sinks, 1.0 / math.sqrt(dim) if scale is None else scale, out_heads,
+            workspace.data_ptr(), workspace.numel(), _stream(k_pool))
     return out
 
 
@@ -656,10 +652,9 @@ def rvq_cache_reserve(table: torch.Tensor, lens: torch.Tensor, new_lens: torch.T
         raise ValueError("new_lens must match lens")
     table_out, refs_out = torch.empty_like(table), torch.empty_like(refs)
     missing, work = table.new_empty(1), _scratch(table, refs)
-    st = _lib().rvq_cache_reserve(_ptr(table), _ptr(lens), _ptr(new_lens), _ptr(refs), table.shape[0], table.shape[1],
-                                  page_size, refs.shape[0], _ptr(table_out), _ptr(refs_out), _ptr(missing),
-                                  _ptr(work), work.numel(), _stream(table))
-    _check("rvq_cache_reserve", st)
+    _launch("rvq_cache_reserve", table.device, _ptr(table), _ptr(lens), _ptr(new_lens), _ptr(refs), table.shape[0],
+            table.shape[1], page_size, refs.shape[0], _ptr(table_out), _ptr(refs_out), _ptr(missing), _ptr(work),
+            work.numel(), _stream(table))
     return table_out, refs_out, missing
 
 
@@ -683,11 +678,9 @@ def rvq_cache_fork(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, 
         raise ValueError("parents and children must match and be no more than there are clips")
     table_out, lens_out, refs_out = torch.empty_like(table), torch.empty_like(lens), torch.empty_like(refs)
     missing, work = table.new_empty(1), _scratch(table, refs)
-    st = _lib().rvq_cache_fork(_cache_shape(k_pool, *table.shape), _layers(k_pool), _ptr(table), _ptr(lens),
-                               _ptr(refs), _ptr(parents), _ptr(children), children.shape[0], _ptr(k_pool),
-                               _ptr(v_pool), _ptr(table_out), _ptr(lens_out), _ptr(refs_out), _ptr(missing),
-                               _ptr(work), work.numel(), _stream(k_pool))
-    _check("rvq_cache_fork", st)
+    _launch("rvq_cache_fork", dev, _cache_shape(k_pool, *table.shape), _layers(k_pool), _ptr(table), _ptr(lens),
+            _ptr(refs), _ptr(parents), _ptr(children), children.shape[0], _ptr(k_pool), _ptr(v_pool), _ptr(table_out),
+            _ptr(lens_out), _ptr(refs_out), _ptr(missing), _ptr(work), work.numel(), _stream(k_pool))
     return table_out, lens_out, refs_out, missing
 
 
@@ -703,10 +696,9 @@ def rvq_cache_free(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, 
     if sinks < 0:
         raise ValueError(f"sinks={sinks} must not be negative")
     table_out, lens_out, refs_out = torch.empty_like(table), torch.empty_like(lens), torch.empty_like(refs)
-    st = _lib().rvq_cache_free(_ptr(table), _ptr(lens), _ptr(refs), _ptr(drop), table.shape[0], table.shape[1],
-                               page_size, refs.shape[0], _window(window), sinks, _ptr(table_out), _ptr(lens_out),
-                               _ptr(refs_out), _stream(table))
-    _check("rvq_cache_free", st)
+    _launch("rvq_cache_free", table.device, _ptr(table), _ptr(lens), _ptr(refs), _ptr(drop), table.shape[0],
+            table.shape[1], page_size, refs.shape[0], _window(window), sinks, _ptr(table_out), _ptr(lens_out),
+            _ptr(refs_out), _stream(table))
     return table_out, lens_out, refs_out
 
 
@@ -717,10 +709,9 @@ def rvq_cache_compact(table: torch.Tensor, refs: torch.Tensor, k_pool: torch.Ten
     _require_table(table, None, dev, refs, k_pool.shape[-4])
     table_out, refs_out = torch.empty_like(table), torch.empty_like(refs)
     live, work = table.new_empty(1), _scratch(table, refs)
-    st = _lib().rvq_cache_compact(_cache_shape(k_pool, *table.shape), _layers(k_pool), _ptr(table), _ptr(refs),
-                                  _ptr(k_pool), _ptr(v_pool), _ptr(table_out), _ptr(refs_out), _ptr(live),
-                                  _ptr(work), work.numel(), _stream(k_pool))
-    _check("rvq_cache_compact", st)
+    _launch("rvq_cache_compact", dev, _cache_shape(k_pool, *table.shape), _layers(k_pool), _ptr(table), _ptr(refs),
+            _ptr(k_pool), _ptr(v_pool), _ptr(table_out), _ptr(refs_out), _ptr(live), _ptr(work), work.numel(),
+            _stream(k_pool))
     return table_out, refs_out, live
 
 
@@ -731,6 +722,5 @@ def rvq_cache_copy(src: torch.Tensor, dst: torch.Tensor, k_pool: torch.Tensor, v
     _require(dst, "dst", torch.int32, 1, k_pool.device)
     if src.shape != dst.shape:
         raise ValueError("src and dst must match")
-    st = _lib().rvq_cache_copy(_cache_shape(k_pool, 0, 0), _layers(k_pool), _ptr(src), _ptr(dst), src.shape[0], _ptr(k_pool),
-                               _ptr(v_pool), _stream(k_pool))
-    _check("rvq_cache_copy", st)
+    _launch("rvq_cache_copy", k_pool.device, _cache_shape(k_pool, 0, 0), _layers(k_pool), _ptr(src), _ptr(dst),
+            src.shape[0], _ptr(k_pool), _ptr(v_pool), _stream(k_pool))
