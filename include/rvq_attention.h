@@ -258,7 +258,8 @@ RVQ_API rvq_status rvq_cache_chunk_attention(const rvq_cache_shape *shape, int32
  * + i, or 2 i and 2 i + 1 where interleaved != 0; the values behind rot_dim
  * stay as they are. With inverse != 0 the angles are negative: the gradient of
  * the same call without it. frequencies [rot_dim / 2] are radians a position,
- * device float64; angles are taken in float64, so far positions lose nothing.
+ * device float64; angles are taken in two float64 parts, known to 2^-50 of a
+ * turn, so far positions lose nothing.
  */
 typedef struct rvq_rotation {
     const double *frequencies;

@@ -16,9 +16,11 @@
 // in the half layout these are the two partners of its pairs, 16 bytes of each
 // half; in the interleaved one they are neighbours. What does not turn is
 // copied by the other threads of the row.
-// Angles: positions go up to 2^31 and a turn has to be known to 2^-26 or so, so
-// position * frequency is taken in turns in float64, whole turns and quarters
-// leave exactly, and what is left (an eighth of a turn at most) goes through
+// Angles: positions go up to 2^31, and a turn has to be known to 2^-26 or so, 2^-55 of
+// what position * frequency can be in turns. So the frequency is taken in turns as
+// the sum of two float64, and the product less its whole turns comes out of one
+// fma, with 2^-53 of a turn left; quarters leave exactly, and the rest (an
+// eighth of a turn at most) goes through
 // the Taylor series of sine and cosine in float32; they are cut off where the
 // next term is below 2^-28. Values turn in float32 and are rounded once.
 #include <limits.h>
@@ -46,8 +48,10 @@ struct Params {
 // cos and sin of 2 pi position f.
 __device__ inline void turn(double position, double f, float &c, float &s)
 {
-    double t = position * (f * 0.15915494309189533577);
-    t -= __builtin_rint(t);
+    // f / 2 pi in two parts; the product with the position keeps what rounding would cut off
+    const double high = f * 0x1.45f306dc9c883p-3;
+    const double low = __builtin_fma(f, 0x1.45f306dc9c883p-3, -high) + f * -0x1.6b01ec5417056p-57;
+    double t = __builtin_fma(position, high, -__builtin_rint(position * high)) + position * low;
     const double quarters = __builtin_rint(4.0 * t);
     const float x = static_cast<float>(__builtin_fma(quarters, -0.25, t)) * 6.283185307179586f;
     const float y = x * x;
