@@ -132,6 +132,33 @@ def test_infinities_of_weights_that_are_no_float32(typ, dim, nq, nk, strong):
     check_out(got, ref["out"], *signs(v, [0, new], [0, nk], lambda a, b: attention_oracle.sees(a, b, None, 0), 2))
 
 
+@pytest.mark.parametrize("typ,dim", [("bf16", 64), ("fp16", 128), ("fp32", 64)])
+@pytest.mark.parametrize("nq,nk,hq", [(1, 40, 2), (3, 700, 2), (2, 5000, 16), (90, 700, 2)])
+def test_all_values_of_a_clip(typ, dim, nq, nk, hq):
+    """All dims of every result of one clip are NaN, or of NaN and infinities; its lse and the other clip stay."""
+    m = rvq()
+    announce("cross, all values", typ=typ, dim=dim, nq=nq, nk=nk, heads=hq)
+    q, k, v, _ = make(TYPES[typ], dim, hq, 1, [nq, nq], [nk, nk])
+    cu_q, cu_k = offsets([nq, nq]), offsets([nk, nk])
+    ref = cross_oracle.attention(q, k, v, cu_q, cu_k, 1 / math.sqrt(dim))
+    out, lse = m.rvq_cross_attention(q, k, v, ints(cu_q), ints(cu_k))
+    close("lse", lse, ref["lse"])
+    for value, first in ((math.nan, 0), (math.nan, nk - 1), (math.inf, 0)):
+        x = v.clone()
+        x[first:nk, :, 1:] = value
+        if value == math.inf:
+            x[nk // 2, :, 2:] = -math.inf
+        got, got_lse = m.rvq_cross_attention(q, k, x, ints(cu_q), ints(cu_k))
+        torch.cuda.synchronize()
+        assert torch.equal(got_lse, lse) and torch.equal(got[nq:], out[nq:])
+        check_out(got, ref["out"], *signs(x, cu_q, cu_k, lambda a, b: torch.ones(a, b), hq))
+    k[5:nk] = math.nan
+    got, got_lse = m.rvq_cross_attention(q, k, v, ints(cu_q), ints(cu_k))
+    torch.cuda.synchronize()
+    assert torch.isnan(got[:nq]).all() and torch.isnan(got_lse[:, :nq]).all()
+    assert torch.equal(got[nq:], out[nq:]) and torch.equal(got_lse[:, nq:], lse[:, nq:])
+
+
 # ---------------------------------------------------------------- scores at the ends of their range
 
 @pytest.mark.parametrize("typ,dim", [("bf16", 64), ("fp16", 64), ("fp32", 64), ("fp32", 128)])
