@@ -229,6 +229,8 @@ RVQ_API rvq_status rvq_cache_attention(const rvq_cache_shape *shape, int32_t q_h
  *   cu         [n_clips + 1] int32: clip b's queries are cu[b] .. cu[b+1]-1
  *              (non-decreasing, within 0..n_tokens; rows outside every clip
  *              are not written); NULL: one query each, n_tokens == n_clips
+ *              (what rvq_cache_attention does, as fast, with lse and with weights
+ *              in two parts)
  *   lens       counts with the new frames, whose keys and values are in the
  *              cache: query i of n is at position lens[b] - n + i. Queries at
  *              negative positions see nothing

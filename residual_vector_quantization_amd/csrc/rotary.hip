@@ -5,9 +5,9 @@
 //
 // and, as the gradient, the same with -t (a rotation's transpose). Bound by
 // HBM: every value is read once and written once. Measured: 65,536 tokens of 16
-// and 4 heads of 128 in bfloat16, out of a fused projection, 0.67 GB in 131 us, 5.1
-// TB/s, what a large copy reaches; 27,224 new frames of 32, 8 and 8 heads of 128
-// turned and written into pages of 16, 0.67 GB in 137 us; the next frames of 96
+// and 4 heads of 128 in bfloat16, out of a fused projection, 0.67 GB in 127 to
+// 131 us, 5.1 to 5.3 TB/s, what a large copy reaches; 27,224 new frames of 32, 8 and 8 heads of 128
+// turned and written into pages of 16, 0.67 GB in 134 us; the next frames of 96
 // streams 5 us, the launch and three reads one after another.
 // A thread keeps to one token and to the same pairs of every head it goes
 // through, so that a pair's sine and cosine are made once for several heads;

@@ -9,8 +9,9 @@
 // once for all of them. Two kinds of workgroups share one launch, as the
 // lengths of the clips' queries are known on the device alone:
 // - few_rows takes a whole clip of up to 16 kSets rows (where there are few rows in
-//   all, also one with more, in turns) and is bound by HBM. Its wavefronts take 32 keys in turn, which go from memory into registers and
-//   from there into 16-wide products with the rows as columns:
+//   all, also one with more, in turns) and is bound by HBM. Its wavefronts take 32
+//   keys in turn, which go from memory into registers and from there into 16-wide
+//   products with the rows as columns:
 //     S^T [key][row] = K Q^T,  O^T [dim][row] = V^T P^T.
 //   Only keys that some row sees are gone over (sinks, then the window), and
 //   the keys of S^T's rows are numbered so that a lane's scores belong to the 8
@@ -23,17 +24,17 @@
 // second launch (join_rows) joins them in order.
 //
 // Measured, bfloat16: 2048 new frames over 45,000 in pages of 64, 32 heads of 128
-// over 8: 1.55 to 1.6 ms, 960 to 1000 TFLOP/s, where a large library product
-// reaches 1130 to 1170 (matrix cores busy in 42% of the cycles at 2.2 GHz, no LDS bank
-// conflicts). The next frame of 12 clips of up to 45,000: 246 us, 5.4 TB/s. 64
+// over 8: 1.56 to 1.65 ms, 935 to 990 TFLOP/s, where a large library product
+// reaches 1130 to 1170 (matrix cores busy in 44% of the cycles, no LDS bank
+// conflicts). The next frame of 12 clips of up to 45,000: 248 us, 5.3 TB/s. 64
 // single queries over up to 1500 packed states, 16 heads of 64: 38 us and 4 for the
 // join, 4.3 TB/s (a plain read of as much reaches 6.2 where all workgroups move
 // through memory side by side and 4.5 to 5.4 where each has a stretch of its own, as
-// here). 8 clips of up to 4 frames over up to 1500, 16 heads of 128 over 8: 14 us and 4,
+// here). 8 clips of up to 4 frames over up to 1500, 16 heads of 128 over 8: 13.5 us and 4,
 // of which 6 to 8 are the chain of reads before the first product (offsets, count, page
 // number, row) and the launch. float16, 12 clips of up to 2000 queries over up to 750
-// states, 16 heads of 128 over 4: 112 us, 600 TFLOP/s, for a workgroup has 12 tiles at
-// most: 16,384 queries over 64 n keys take 41 + 7.7 n us, 27 of the 41 for 134 MB of
+// states, 16 heads of 128 over 4: 113 us, 600 TFLOP/s, and 4 for a join launch that finds
+// nothing to join, for a workgroup has 12 tiles at most: 16,384 queries over 64 n keys take 41 + 7.7 n us, 27 of the 41 for 134 MB of
 // queries and results.
 //
 // Running maxima move only when a score exceeds them by more than 2^kSlack.
@@ -241,7 +242,7 @@ __device__ inline float groups_sum(float x)
 
 template <int kD> constexpr int kJoinBytes = kWaves * 16 * (kD + 4 + 2) * 4;
 // Where two sets of rows would not leave registers enough their queries stay in the LDS (48 clips of 4 frames over up to
-// 4000, 32 heads of 128 over 4: 102 -> 93 us, spilled registers 47 -> 27).
+// 4000, 32 heads of 128 over 4: 85.6 -> 74.3 us, spilled registers 17 -> none; 8 such clips 26.4 -> 25.3).
 template <typename T, int kD, int kSets> constexpr bool kStaged = kSets == 2 && kD == 128 && sizeof(T) == 2;
 template <typename T, int kD, int kSets> constexpr int kStagedBytes = kJoinBytes<kD> + (kStaged<T, kD, kSets> ? kSets * kD / 32 * 1024 : 0);
 template <typename T, int kD, int kSets> constexpr int kFewBytes = kStagedBytes<T, kD, kSets> + 16;
@@ -982,7 +983,8 @@ RVQ_INLINE void tile_rows(const RowsArgs &a, const Plan &p, int block, char *s_m
 
 // ---------------------------------------------------------------- launches
 
-// The tiles' workgroups come first: they last longer.
+// The tiles' workgroups come first: they last longer. Registers spilled, here and in only_few_rows: over pages 9 of 168 in
+// 16 bits at dim 64 with two sets of rows, 68 in float32 at dim 128; none elsewhere.
 template <typename T, int kD, typename Keys, int kSets>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? (kD == 64 ? 3 : 2) : 1)
 void all_rows(RowsArgs a, Plan p, int tile_groups)
@@ -1068,10 +1070,10 @@ void join_rows(RowsArgs a, Plan p)
 inline Plan plan(const RowsArgs &a, int64_t keys, int64_t &floats)
 {
     // few_rows: up to kWanted workgroups, each with kTurns tiles a wavefront or more, as every split of a row writes its
-    // accumulator (8 clips of 4 frames over up to 4000, 8 query heads a key head of 128: kTurns 1, 2, 3, 4 take 53, 39, 32,
-    // 42 us; 12 clips of up to 45000 frames: 512, 1024, 2048, 4096, 8192 workgroups take 293, 266, 255, 246, 262 us); with 32
-    // rows, which take more registers and write twice as much, up to 768 (the same drafts of 48 clips: 512, 1024, 2048, 4096
-    // take 106, 102, 121, 121 us; 24 single frames beside 8 chunks 75, 81, 82, 82).
+    // accumulator (8 clips of 4 frames over up to 4000, 8 query heads a key head of 128: kTurns 1, 2, 3, 4 take 31, 26, 25,
+    // 30 us; 12 clips of up to 45000 frames: 1024, 2048, 4096, 8192 workgroups take 262, 256, 248, 264 us); with 32
+    // rows, which take more registers and write twice as much, up to 768 (the same drafts of 48 clips: 512, 768, 1024, 2048,
+    // 4096 take 80, 74, 76, 83, 83 us; 24 single frames beside 8 chunks 75, 74, 78, 78, 78).
     // tile_rows: as many workgroups as the chip holds at once, 2 a CU in 16 bits (256 frames over 8000: 256, 384, 512, 768
     // workgroups take 84, 72, 62, 74 us), with least_tiles tiles each. In dim 64 it holds 3, which pays where keys are many
     // (2 clips of 1024 frames over 8000, 16 heads over 4: 256, 512, 768 workgroups take 202, 125, 111 us; 27 tiles a row in
@@ -1090,8 +1092,11 @@ inline Plan plan(const RowsArgs &a, int64_t keys, int64_t &floats)
     const int rows = heads <= 16 && average * heads <= 16 ? 16 : 32;
     p.few_limit = rows / heads;
     // One clip alone has either many or few. few_rows takes all where there are so few that tile_rows' workgroups do not
-    // pay: up to 4 turns, or 8 where that is no more than 64 queries (8 clips of 4 frames, 8 query heads a key head: dim 64
-    // 20 -> 17 us, dim 128 36 -> 33; 8 turns for 6 float32 clips of up to 50 queries, 8 heads: 20 -> 27 us).
+    // pay: up to 4 turns, or 8 where that is no more than 64 queries. 4 and 8 turns: 8 clips of 4 frames, 8 query heads a
+    // key head of 128, bfloat16 32.0 and 31.0 us, float32 91.0 and 87.6; 4 heads of 64 16.3 and 16.0, 22.7 and 20.9; 16
+    // clips of 4, 2 heads of 128 27.5 and 26.7, 62.6 and 59.8. With one query head a key head 8 turns are 128 queries: 8
+    // clips of 12 take 16.5 and 16.0, 22.9 and 20.8, but 6 float32 clips of up to 50, which go through all of the turns one
+    // after another, 19.7 and 25.0.
     const int64_t turns = 8 * p.few_limit <= 64 ? 8 : 4;
     p.all_few = !a.cu_q || a.q_tokens <= (a.n_clips == 1 ? 1 : turns) * p.few_limit;
     p.any_few = p.all_few || a.n_clips != 1;
